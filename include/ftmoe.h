@@ -419,6 +419,101 @@ int ft_moe_profile_read(ft_moe_pool *p, ft_moe_profile *out, int32_t reset);
 enum { FT_DBG_H_CODES = 0, FT_DBG_H_SCALES = 1, FT_DBG_ROW_SLOT = 2 };
 int ft_moe_debug_read(ft_moe_pool *p, int32_t what, void *dst, int64_t bytes);
 
+/* ------------------------------------------------------------------------
+ * Dense feed-forward operators: the blocks of a model that are not routed
+ * (dense first layers, always-on blocks), beside the pool's routed experts.
+ * They keep no state and need no pool: the caller owns every buffer.
+ *
+ * Weights are [out][in] row-major as in an expert blob.  A leading dimension
+ * (ld_*) is the distance between two rows in elements; 0 means rows follow
+ * each other (the width itself).  Any size and stride is taken; operands
+ * whose base addresses and row strides are multiples of 16 bytes (and whose
+ * widths along K are whole 16-byte pieces) run the fast kernels, others a
+ * general one several times slower.
+ *
+ * Every call enqueues its work on `hip_stream` (NULL = the null stream of the
+ * current device) and returns; nothing is read after that on the host and
+ * nothing is allocated, so calls may be captured into a HIP graph.  All
+ * pointers are memory of the stream's device, which need not be the current
+ * device.  An output may not overlap an input, another output or `work`.
+ * `work` is scratch memory (16-byte aligned, at least the bytes that the
+ * operator's *_work function returns for the same description); its contents
+ * are undefined afterwards and nothing in it is kept between calls, but
+ * calls that share it must not overlap in time: calls on different streams,
+ * and graphs that may be replayed at once, need one each.
+ *
+ * Results do not depend on timing: every sum has a fixed order.
+ */
+enum { FT_DT_BF16 = 1, FT_DT_F16 = 2, FT_DT_F32 = 3 };
+
+/* A gated feed-forward block.
+ *   g = x Wg^T, u = x Wu^T, h = silu(g) * u, y = h Wd^T
+ * x [T][H], Wg and Wu [I][H], Wd [H][I], y [T][H], gu [T][2 I] holding g in
+ * columns 0..I-1 and u in I..2I-1.  All tensors have type `dtype` (bf16 or
+ * fp16); sums are fp32, and g, u, h and the gradients of g and u are rounded
+ * to `dtype` where they are stored.  Sizes up to 2^24 - 1 per dimension. */
+typedef struct {
+  int32_t dtype;             /* FT_DT_BF16 or FT_DT_F16 */
+  int32_t tokens;            /* T >= 0 */
+  int32_t hidden, inter;     /* H, I >= 1 */
+  int64_t ld_x, ld_y;        /* rows of x and dx; of y and dy */
+  int64_t ld_gu;             /* rows of gu */
+  int64_t ld_w_in, ld_w_out; /* rows of Wg, Wu and their gradients; of Wd and its gradient */
+} ft_moe_gated_ffn;
+
+/* Scratch bytes of a forward (backward = 0) or backward call. */
+int ft_moe_gated_ffn_work(const ft_moe_gated_ffn *d, int32_t backward, int64_t *bytes);
+
+/* y, and gu when it is not NULL (what the backward pass needs).  h is formed
+ * from the fp32 g and u.  With no tokens nothing is written. */
+int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn *d, const void *x, const void *w_gate, const void *w_up,
+                             const void *w_down, void *y, void *gu, void *work, int64_t work_bytes, void *hip_stream);
+
+/* Gradients of a scalar with derivative dy [T][H] with respect to y:
+ *   dh = dy Wd, s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s
+ *   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T (g s u)
+ * with g and u as gu holds them.  dx may be NULL; dw_gate, dw_up and dw_down
+ * may all be NULL (frozen weights; x is then not read and may be NULL), and
+ * are written, not added to.  With no tokens the weight gradients are 0. */
+int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn *d, const void *x, const void *w_gate, const void *w_up,
+                              const void *w_down, const void *gu, const void *dy, void *dx, void *dw_gate,
+                              void *dw_up, void *dw_down, void *work, int64_t work_bytes, void *hip_stream);
+
+/* 8-bit rows: scale[r] = fp32(max|x[r]| / 127), codes[r][c] = x[r][c] /
+ * scale[r] rounded to the nearest integer, ties to even (correctly rounded,
+ * within -127..127).  A row of zeros, or one whose scale is below the
+ * smallest fp32, gets scale 0 and codes 0; a row that holds an infinity or a
+ * NaN gets codes 0 and scale NaN, so everything computed from it is NaN.
+ * x [rows][cols] has type dtype (bf16, fp16 or fp32); codes [rows][cols]
+ * signed bytes.  Used for tokens at each call and once for the output
+ * channels of a weight matrix. */
+int ft_moe_int_quantize(int32_t dtype, int32_t rows, int32_t cols, const void *x, int64_t ld_x, int8_t *codes,
+                        int64_t ld_codes, float *scale, void *hip_stream);
+
+/* Product of 8-bit codes with a scale per token and per output channel:
+ *   y[t][n] = x_scale[t] w_scale[n] sum_k x[t][k] w[n][k]
+ * The sums are exact 32-bit integers (K up to 131071); y has type out_dtype
+ * (bf16, fp16 or fp32). */
+typedef struct {
+  int32_t out_dtype;         /* FT_DT_* of y */
+  int32_t tokens;            /* T >= 0 */
+  int32_t in, out;           /* K, N >= 1 */
+  int64_t ld_x, ld_w, ld_y;  /* rows of the token codes, of the weight codes, of y */
+} ft_moe_int_product;
+int ft_moe_int_matmul_work(const ft_moe_int_product *d, int64_t *bytes);
+int ft_moe_int_matmul(const ft_moe_int_product *d, const int8_t *x, const float *x_scale, const int8_t *w,
+                      const float *w_scale, void *y, void *work, int64_t work_bytes, void *hip_stream);
+
+/* The gated block on 8-bit weights: x is quantised per token, g and u are
+ * 8-bit products, h = silu(g) * u (fp32) is quantised per token, y is an
+ * 8-bit product.  x and y have type d->dtype, the weights are codes with one
+ * scale per row (as ft_moe_int_quantize leaves them), d->ld_w_in and
+ * d->ld_w_out are the code rows, d->ld_gu is not used; H, I <= 131071. */
+int ft_moe_int_gated_ffn_work(const ft_moe_gated_ffn *d, int64_t *bytes);
+int ft_moe_int_gated_ffn(const ft_moe_gated_ffn *d, const void *x, const int8_t *w_gate, const float *gate_scale,
+                         const int8_t *w_up, const float *up_scale, const int8_t *w_down, const float *down_scale,
+                         void *y, void *work, int64_t work_bytes, void *hip_stream);
+
 void ft_moe_destroy_pool(ft_moe_pool *p);
 const char *ft_moe_last_error(void);
 

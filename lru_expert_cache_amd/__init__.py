@@ -38,7 +38,10 @@ EXPORTED = ["ft_moe_init_pool", "ft_moe_layer_forward", "ft_moe_pool_stats", "ft
             "ft_moe_reserve", "ft_moe_resize_pool", "ft_moe_decide_mode", "ft_moe_measure_mode",
             "ft_moe_ffn_kernel_name", "ft_moe_mfma_rate", "ft_moe_layer_forward_noalloc",
             "ft_moe_set_hybrid_share_format", "ft_moe_get_hybrid_share", "ft_moe_rebalance",
-            "ft_moe_debug_read"]
+            "ft_moe_debug_read", "ft_moe_gated_ffn_work", "ft_moe_gated_ffn_forward", "ft_moe_gated_ffn_backward",
+            "ft_moe_int_quantize", "ft_moe_int_matmul_work", "ft_moe_int_matmul", "ft_moe_int_gated_ffn_work",
+            "ft_moe_int_gated_ffn"]
+FT_DT_BF16, FT_DT_F16, FT_DT_F32 = 1, 2, 3
 FT_DBG_H_CODES, FT_DBG_H_SCALES, FT_DBG_ROW_SLOT = 0, 1, 2
 
 FT_MODE_OFFLOAD, FT_MODE_HYBRID, FT_MODE_FUSED = 0, 1, 2
@@ -108,6 +111,18 @@ class ft_moe_profile(ctypes.Structure):
                 for i, st in enumerate(FT_STAGES)}
 
 
+class ft_moe_gated_ffn(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("inter", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_gu", ctypes.c_int64), ("ld_w_in", ctypes.c_int64), ("ld_w_out", ctypes.c_int64)]
+
+
+class ft_moe_int_product(ctypes.Structure):
+    _fields_ = [("out_dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("in", ctypes.c_int32),
+                ("out", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -164,6 +179,18 @@ def lib() -> ctypes.CDLL:
     L.ft_moe_set_profiling.restype = ctypes.c_int
     L.ft_moe_profile_read.argtypes = [P, ctypes.POINTER(ft_moe_profile), ctypes.c_int32]
     L.ft_moe_profile_read.restype = ctypes.c_int
+    I32, I64 = ctypes.c_int32, ctypes.c_int64
+    FFN, PROD, I64P = ctypes.POINTER(ft_moe_gated_ffn), ctypes.POINTER(ft_moe_int_product), ctypes.POINTER(I64)
+    for name, args in (("ft_moe_gated_ffn_work", [FFN, I32, I64P]),
+                       ("ft_moe_gated_ffn_forward", [FFN] + [P] * 7 + [I64, P]),
+                       ("ft_moe_gated_ffn_backward", [FFN] + [P] * 11 + [I64, P]),
+                       ("ft_moe_int_quantize", [I32, I32, I32, P, I64, P, I64, P, P]),
+                       ("ft_moe_int_matmul_work", [PROD, I64P]),
+                       ("ft_moe_int_matmul", [PROD] + [P] * 6 + [I64, P]),
+                       ("ft_moe_int_gated_ffn_work", [FFN, I64P]),
+                       ("ft_moe_int_gated_ffn", [FFN] + [P] * 9 + [I64, P])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = ctypes.c_int
     L.ft_moe_destroy_pool.argtypes = [P]
     L.ft_moe_destroy_pool.restype = None
     L.ft_moe_last_error.argtypes = []
@@ -388,3 +415,77 @@ def ft_moe_profile_read(pool, reset: bool = False) -> dict:
 def ft_moe_destroy_pool(pool):
     if pool:
         lib().ft_moe_destroy_pool(pool)
+
+
+# ---------------------------------------------------------------- dense feed-forward operators
+# Tensors are passed as device addresses or objects with data_ptr(); `work` is a
+# tensor of scratch memory (its size is read from it) or None where none is
+# needed; stream None is the null stream of the current device.
+
+
+def make_gated_ffn(dtype, tokens, hidden, inter, ld_x=0, ld_y=0, ld_gu=0, ld_w_in=0, ld_w_out=0):
+    return ft_moe_gated_ffn(int(dtype), int(tokens), int(hidden), int(inter), int(ld_x), int(ld_y), int(ld_gu),
+                            int(ld_w_in), int(ld_w_out))
+
+
+def make_int_matmul(tokens, in_features, out_features, out_dtype, ld_x=0, ld_w=0, ld_y=0):
+    return ft_moe_int_product(int(out_dtype), int(tokens), int(in_features), int(out_features), int(ld_x), int(ld_w),
+                              int(ld_y))
+
+
+def _stream(stream) -> int:
+    if stream is None or isinstance(stream, int):
+        return stream or 0
+    return int(stream.cuda_stream)
+
+
+def _work(work):
+    return (0, 0) if work is None else (work.data_ptr(), work.numel() * work.element_size())
+
+
+def _work_bytes(fn, *args) -> int:
+    n = ctypes.c_int64()
+    _check(fn(*args, ctypes.byref(n)))
+    return n.value
+
+
+def ft_moe_gated_ffn_work(d: ft_moe_gated_ffn, backward: bool = False) -> int:
+    return _work_bytes(lib().ft_moe_gated_ffn_work, ctypes.byref(d), int(bool(backward)))
+
+
+def ft_moe_gated_ffn_forward(d: ft_moe_gated_ffn, x, w_gate, w_up, w_down, y, gu=None, work=None, stream=None) -> int:
+    return _check(lib().ft_moe_gated_ffn_forward(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                                 _ptr(y), _ptr(gu), *_work(work), _stream(stream)))
+
+
+def ft_moe_gated_ffn_backward(d: ft_moe_gated_ffn, x, w_gate, w_up, w_down, gu, dy, dx=None, dw_gate=None, dw_up=None,
+                              dw_down=None, work=None, stream=None) -> int:
+    return _check(lib().ft_moe_gated_ffn_backward(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                                  _ptr(gu), _ptr(dy), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
+                                                  _ptr(dw_down), *_work(work), _stream(stream)))
+
+
+def ft_moe_int_quantize(dtype: int, rows: int, cols: int, x, codes, scale, ld_x: int = 0, ld_codes: int = 0,
+                        stream=None) -> int:
+    return _check(lib().ft_moe_int_quantize(int(dtype), int(rows), int(cols), _ptr(x), int(ld_x), _ptr(codes),
+                                            int(ld_codes), _ptr(scale), _stream(stream)))
+
+
+def ft_moe_int_matmul_work(d: ft_moe_int_product) -> int:
+    return _work_bytes(lib().ft_moe_int_matmul_work, ctypes.byref(d))
+
+
+def ft_moe_int_matmul(d: ft_moe_int_product, x, x_scale, w, w_scale, y, work=None, stream=None) -> int:
+    return _check(lib().ft_moe_int_matmul(ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y),
+                                          *_work(work), _stream(stream)))
+
+
+def ft_moe_int_gated_ffn_work(d: ft_moe_gated_ffn) -> int:
+    return _work_bytes(lib().ft_moe_int_gated_ffn_work, ctypes.byref(d))
+
+
+def ft_moe_int_gated_ffn(d: ft_moe_gated_ffn, x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, y, work=None,
+                         stream=None) -> int:
+    return _check(lib().ft_moe_int_gated_ffn(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(gate_scale), _ptr(w_up),
+                                             _ptr(up_scale), _ptr(w_down), _ptr(down_scale), _ptr(y), *_work(work),
+                                             _stream(stream)))

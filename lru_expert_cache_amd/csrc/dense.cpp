@@ -1,0 +1,411 @@
+// C entry points of the dense feed-forward operators: argument checks, the
+// layout of the scratch memory, and the sequence of products of each call.
+#include <initializer_list>
+
+#include "dense.h"
+
+using namespace ftmoe;
+
+namespace {
+
+constexpr int32_t kMaxDim = (1 << 24) - 1;  // tokens and widths
+constexpr int32_t kMaxIntK = 131071;        // 127 * 127 * K < 2^31
+constexpr int64_t kAlign = 256;             // parts of the scratch memory
+
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {  // an error message that could not be stored
+    return FT_E_HIP;
+  }
+}
+
+int bad(const char* what) {
+  set_error("%s", what);
+  return FT_E_INVALID;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// scratch memory, handed out in order; the same code lays it out (base 0) and uses it
+struct Carve {
+  uint8_t* base;
+  int64_t used = 0;
+  uint8_t* take(int64_t bytes) {
+    uint8_t* p = base + used;
+    used += up(bytes, kAlign);
+    return p;
+  }
+};
+
+struct Arg {
+  const void* p;
+  int64_t align;  // of the element type
+  const char* name;
+};
+
+// Every pointer is there, aligned for its elements and memory of one device,
+// the stream's; that device is made current while the guard lives.
+struct DeviceGuard {
+  int back = -1;
+  ~DeviceGuard() {
+    if (back >= 0) (void)hipSetDevice(back);
+  }
+  int enter(hipStream_t s, std::initializer_list<Arg> args) {
+    for (const Arg& a : args) {
+      if (!a.p) {
+        set_error("%s is NULL", a.name);
+        return FT_E_INVALID;
+      }
+      if (reinterpret_cast<uintptr_t>(a.p) % uintptr_t(a.align)) {
+        set_error("%s is not aligned to %lld bytes", a.name, (long long)a.align);
+        return FT_E_INVALID;
+      }
+    }
+    int cur = 0, dev = 0;
+    FT_HIP_CHECK(hipGetDevice(&cur));
+    dev = cur;
+    if (s) FT_HIP_CHECK(hipStreamGetDevice(s, &dev));
+    for (const Arg& a : args) {
+      hipPointerAttribute_t at;
+      if (hipPointerGetAttributes(&at, a.p) != hipSuccess) {
+        (void)hipGetLastError();
+        at.type = hipMemoryTypeUnregistered;
+      }
+      if ((at.type != hipMemoryTypeDevice && at.type != hipMemoryTypeManaged) || at.device != dev) {
+        set_error("%s is not memory of device %d, the stream's", a.name, dev);
+        return FT_E_INVALID;
+      }
+    }
+    if (dev != cur) {
+      FT_HIP_CHECK(hipSetDevice(dev));
+      back = cur;
+    }
+    return FT_OK;
+  }
+};
+
+bool dim_ok(int64_t v, int64_t lo) { return v >= lo && v <= kMaxDim; }
+// a row distance: 0 = the width; a limit keeps every byte offset within 64 bits
+bool row_ok(int64_t& ld, int64_t width) {
+  if (ld == 0) ld = width;
+  return ld >= width && ld < (int64_t(1) << 32);
+}
+bool div4(const void* p, int64_t es, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && ld % 4 == 0; }
+
+// checks a block's description and fills in the row distances
+int check_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
+  if (!d) return bad("NULL description");
+  o = *d;
+  if (o.dtype != FT_DT_BF16 && o.dtype != FT_DT_F16) return bad("dtype must be FT_DT_BF16 or FT_DT_F16");
+  if (!dim_ok(o.tokens, 0) || !dim_ok(o.hidden, 1) || !dim_ok(o.inter, 1)) {
+    set_error("bad sizes: tokens %d, hidden %d, inter %d", o.tokens, o.hidden, o.inter);
+    return FT_E_INVALID;
+  }
+  if (!row_ok(o.ld_x, o.hidden) || !row_ok(o.ld_y, o.hidden) || !row_ok(o.ld_gu, 2 * int64_t(o.inter)) ||
+      !row_ok(o.ld_w_in, o.hidden) || !row_ok(o.ld_w_out, o.inter))
+    return bad("a row distance (ld_*) is smaller than its row, or 2^32 or more");
+  return FT_OK;
+}
+
+// ------------------------------------------------------------ gated block
+struct FfnWork {
+  int64_t ldi;  // elements between rows of h, and half of a row of dgu
+  uint8_t *h, *dgu;
+  int64_t bytes;
+};
+FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
+  FfnWork w{};
+  Carve c{static_cast<uint8_t*>(base)};
+  w.ldi = up(d.inter, 64);
+  w.h = c.take(int64_t(d.tokens) * w.ldi * 2);
+  if (backward) w.dgu = c.take(int64_t(d.tokens) * w.ldi * 4);
+  w.bytes = c.used;
+  return w;
+}
+
+const uint8_t* u8(const void* p) { return static_cast<const uint8_t*>(p); }
+uint8_t* u8(void* p) { return static_cast<uint8_t*>(p); }
+
+DenseProblem product(const void* a, int64_t lda, const void* b, int64_t ldb, int m, int n, int k, void* c, int64_t ldc,
+                     int64_t es, int64_t es_c) {
+  DenseProblem p{};
+  p.a[0] = p.a[1] = u8(a);
+  p.b[0] = p.b[1] = u8(b);
+  p.lda = lda * es;
+  p.ldb = ldb * es;
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  p.segs = 1;
+  p.c = u8(c);
+  p.ldc = ldc;
+  p.vec4 = !c || div4(c, es_c, ldc);
+  return p;
+}
+
+int run(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s) {
+  FT_HIP_CHECK(launch_dense_any(form, dtype, l, s));
+  return FT_OK;
+}
+int run(DenseForm form, int dtype, const DenseProblem& p, hipStream_t s) {
+  DenseLaunch l{};
+  l.p[0] = p;
+  l.count = 1;
+  return run(form, dtype, l, s);
+}
+
+bool same(const void* p, std::initializer_list<const void*> others) {
+  for (const void* o : others)
+    if (p && p == o) return true;
+  return false;
+}
+
+// ------------------------------------------------------------ 8-bit
+int check_product(const ft_moe_int_product* d, ft_moe_int_product& o) {
+  if (!d) return bad("NULL description");
+  o = *d;
+  if (o.out_dtype < FT_DT_BF16 || o.out_dtype > FT_DT_F32) return bad("unknown out_dtype");
+  if (!dim_ok(o.tokens, 0) || !dim_ok(o.out, 1) || o.in < 1 || o.in > kMaxIntK) {
+    set_error("bad sizes: tokens %d, in %d (at most %d), out %d", o.tokens, o.in, kMaxIntK, o.out);
+    return FT_E_INVALID;
+  }
+  if (!row_ok(o.ld_x, o.in) || !row_ok(o.ld_w, o.in) || !row_ok(o.ld_y, o.out))
+    return bad("a row distance (ld_*) is smaller than its row, or 2^32 or more");
+  return FT_OK;
+}
+int64_t size_of(int dtype) { return dtype == FT_DT_F32 ? 4 : 2; }
+
+struct IntWork {
+  int64_t ldx, ldh, ldf;
+  int8_t *xq, *hq;
+  float *xs, *hs, *h;
+  int64_t bytes;
+};
+IntWork int_work(const ft_moe_gated_ffn& d, void* base) {
+  IntWork w{};
+  Carve c{static_cast<uint8_t*>(base)};
+  const int64_t T = d.tokens;
+  w.ldx = up(d.hidden, 128);
+  w.ldh = up(d.inter, 128);
+  w.ldf = up(d.inter, 32);
+  w.xq = reinterpret_cast<int8_t*>(c.take(T * w.ldx));
+  w.xs = reinterpret_cast<float*>(c.take(T * 4));
+  w.h = reinterpret_cast<float*>(c.take(T * w.ldf * 4));
+  w.hq = reinterpret_cast<int8_t*>(c.take(T * w.ldh));
+  w.hs = reinterpret_cast<float*>(c.take(T * 4));
+  w.bytes = c.used;
+  return w;
+}
+int check_int_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
+  if (const int rc = check_ffn(d, o)) return rc;
+  if (o.hidden > kMaxIntK || o.inter > kMaxIntK) {
+    set_error("bad sizes: hidden %d, inter %d (8 bit: at most %d)", o.hidden, o.inter, kMaxIntK);
+    return FT_E_INVALID;
+  }
+  return FT_OK;
+}
+
+int check_work(const void* work, int64_t have, int64_t need) {
+  if (have < need || (need > 0 && !work)) {
+    set_error("the call needs %lld bytes of scratch memory, %lld given", (long long)need,
+              (long long)(work ? have : 0));
+    return FT_E_INVALID;
+  }
+  return FT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ft_moe_gated_ffn_work(const ft_moe_gated_ffn* d, int32_t backward, int64_t* bytes) {
+  return guarded([&]() -> int {
+    ft_moe_gated_ffn o;
+    if (const int rc = check_ffn(d, o)) return rc;
+    if (!bytes) return bad("bytes is NULL");
+    *bytes = ffn_work(o, backward != 0, nullptr).bytes;
+    return FT_OK;
+  });
+}
+
+int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const void* w_gate, const void* w_up,
+                             const void* w_down, void* y, void* gu, void* work, int64_t work_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    ft_moe_gated_ffn d;
+    if (const int rc = check_ffn(desc, d)) return rc;
+    if (d.tokens == 0) return FT_OK;
+    const FfnWork w = ffn_work(d, false, work);
+    if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
+    if (same(y, {x, w_gate, w_up, w_down, gu, work}) || same(gu, {x, w_gate, w_up, w_down, work}))
+      return bad("an output is also another argument");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    DeviceGuard g;
+    if (const int rc = g.enter(s, {{x, 2, "x"}, {w_gate, 2, "w_gate"}, {w_up, 2, "w_up"}, {w_down, 2, "w_down"},
+                                   {y, 2, "y"}, {gu ? gu : y, 2, "gu"}, {work, 16, "work"}}))
+      return rc;
+
+    DenseProblem p = product(x, d.ld_x, w_gate, d.ld_w_in, d.tokens, d.inter, d.hidden, w.h, w.ldi, 2, 2);
+    p.b[1] = u8(w_up);
+    p.gu = u8(gu);
+    p.ldgu = d.ld_gu;
+    p.off_u = d.inter;
+    if (gu) p.vec4 = div4(gu, 2, d.ld_gu) && d.inter % 4 == 0;
+    if (const int rc = run(kDenseGated, d.dtype, p, s)) return rc;
+    p = product(w.h, w.ldi, w_down, d.ld_w_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2, 2);
+    return run(kDenseRows, d.dtype, p, s);
+  });
+}
+
+int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const void* w_gate, const void* w_up,
+                              const void* w_down, const void* gu, const void* dy, void* dx, void* dw_gate, void* dw_up,
+                              void* dw_down, void* work, int64_t work_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    ft_moe_gated_ffn d;
+    if (const int rc = check_ffn(desc, d)) return rc;
+    const bool grads = dw_gate || dw_up || dw_down;
+    if (grads && !(dw_gate && dw_up && dw_down)) return bad("weight gradients are given together or not at all");
+    if (!grads && (!dx || d.tokens == 0)) return FT_OK;
+    const FfnWork w = ffn_work(d, true, work);
+    if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
+    for (const void* o : {(const void*)dx, (const void*)dw_gate, (const void*)dw_up, (const void*)dw_down, (const void*)work})
+      if (same(o, {x, w_gate, w_up, w_down, gu, dy})) return bad("an output is also another argument");
+    if (same(dx, {dw_gate, dw_up, dw_down, work}) || same(dw_gate, {dw_up, dw_down, work}) ||
+        same(dw_up, {dw_down, work}) || same(dw_down, {work}))
+      return bad("an output is given twice");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    const int T = d.tokens, H = d.hidden, I = d.inter;
+    // what is read and written of the tokens, the weights and their gradients
+    const void* any = grads ? dw_gate : dx;
+    DeviceGuard g;
+    if (const int rc = g.enter(s, {{T && grads ? x : any, 2, "x"}, {T && dx ? w_gate : any, 2, "w_gate"},
+                                   {T && dx ? w_up : any, 2, "w_up"}, {T ? w_down : any, 2, "w_down"},
+                                   {T ? gu : any, 2, "gu"}, {T ? dy : any, 2, "dy"}, {T && dx ? dx : any, 2, "dx"},
+                                   {grads ? dw_gate : any, 2, "dw_gate"}, {grads ? dw_up : any, 2, "dw_up"},
+                                   {grads ? dw_down : any, 2, "dw_down"}, {T ? work : any, T ? 16 : 2, "work"}}))
+      return rc;
+
+    if (T > 0) {
+      DenseProblem p = product(dy, d.ld_y, w_down, d.ld_w_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2, 2);
+      p.gu = const_cast<uint8_t*>(u8(gu));
+      p.ldgu = d.ld_gu;
+      p.off_u = I;
+      p.dgu = w.dgu;
+      p.lddgu = 2 * w.ldi;
+      p.off_du = w.ldi;
+      p.vec4 = div4(gu, 2, d.ld_gu) && I % 4 == 0;
+      if (const int rc = run(kDenseGrad, d.dtype, p, s)) return rc;
+    }
+    if (T > 0 && dx) {
+      DenseProblem p = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2, 2);
+      p.a[1] = w.dgu + 2 * w.ldi;
+      p.b[1] = u8(w_up);
+      p.segs = 2;
+      if (const int rc = run(kDenseCols, d.dtype, p, s)) return rc;
+    }
+    if (!grads) return FT_OK;
+    DenseLaunch l{};
+    l.p[0] = product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2, 2);
+    l.p[1] = product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2, 2);
+    l.p[2] = product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2, 2);
+    l.count = 3;
+    return run(kDenseOuter, d.dtype, l, s);
+  });
+}
+
+int ft_moe_int_quantize(int32_t dtype, int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes,
+                        int64_t ld_codes, float* scale, void* hip_stream) {
+  return guarded([&]() -> int {
+    if (dtype < FT_DT_BF16 || dtype > FT_DT_F32) return bad("unknown dtype");
+    if (!dim_ok(rows, 0) || !dim_ok(cols, 1)) {
+      set_error("bad sizes: rows %d, cols %d", rows, cols);
+      return FT_E_INVALID;
+    }
+    if (!row_ok(ld_x, cols) || !row_ok(ld_codes, cols))
+      return bad("a row distance (ld_*) is smaller than its row, or 2^32 or more");
+    if (rows == 0) return FT_OK;
+    if (same(codes, {x, scale}) || same(scale, {x})) return bad("an output is also another argument");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    DeviceGuard g;
+    if (const int rc = g.enter(s, {{x, size_of(dtype), "x"}, {codes, 1, "codes"}, {scale, 4, "scale"}})) return rc;
+    FT_HIP_CHECK(launch_int_quantize(dtype, rows, cols, x, ld_x, codes, ld_codes, scale, s));
+    return FT_OK;
+  });
+}
+
+int ft_moe_int_matmul_work(const ft_moe_int_product* d, int64_t* bytes) {
+  return guarded([&]() -> int {
+    ft_moe_int_product o;
+    if (const int rc = check_product(d, o)) return rc;
+    if (!bytes) return bad("bytes is NULL");
+    *bytes = 0;
+    return FT_OK;
+  });
+}
+
+int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const float* x_scale, const int8_t* w,
+                      const float* w_scale, void* y, void* work, int64_t work_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    ft_moe_int_product d;
+    if (const int rc = check_product(desc, d)) return rc;
+    if (d.tokens == 0) return FT_OK;
+    if (const int rc = check_work(work, work_bytes, 0)) return rc;
+    if (same(y, {x, x_scale, w, w_scale, work})) return bad("an output is also another argument");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    const int64_t es = size_of(d.out_dtype);
+    DeviceGuard g;
+    if (const int rc = g.enter(s, {{x, 1, "x"}, {x_scale, 4, "x_scale"}, {w, 1, "w"}, {w_scale, 4, "w_scale"}, {y, es, "y"}}))
+      return rc;
+    DenseProblem p = product(x, d.ld_x, w, d.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1, es);
+    p.xs = x_scale;
+    p.ws[0] = p.ws[1] = w_scale;
+    return run(kDenseInt, d.out_dtype, p, s);
+  });
+}
+
+int ft_moe_int_gated_ffn_work(const ft_moe_gated_ffn* d, int64_t* bytes) {
+  return guarded([&]() -> int {
+    ft_moe_gated_ffn o;
+    if (const int rc = check_int_ffn(d, o)) return rc;
+    if (!bytes) return bad("bytes is NULL");
+    *bytes = int_work(o, nullptr).bytes;
+    return FT_OK;
+  });
+}
+
+int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8_t* w_gate, const float* gate_scale,
+                         const int8_t* w_up, const float* up_scale, const int8_t* w_down, const float* down_scale,
+                         void* y, void* work, int64_t work_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    ft_moe_gated_ffn d;
+    if (const int rc = check_int_ffn(desc, d)) return rc;
+    if (d.tokens == 0) return FT_OK;
+    const IntWork w = int_work(d, work);
+    if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
+    if (same(y, {x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, work}) ||
+        same(work, {x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale}))
+      return bad("an output is also another argument");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    DeviceGuard g;
+    if (const int rc = g.enter(s, {{x, 2, "x"}, {w_gate, 1, "w_gate"}, {gate_scale, 4, "gate_scale"}, {w_up, 1, "w_up"},
+                                   {up_scale, 4, "up_scale"}, {w_down, 1, "w_down"}, {down_scale, 4, "down_scale"},
+                                   {y, 2, "y"}, {work, 16, "work"}}))
+      return rc;
+    const int T = d.tokens, H = d.hidden, I = d.inter;
+    FT_HIP_CHECK(launch_int_quantize(d.dtype, T, H, x, d.ld_x, w.xq, w.ldx, w.xs, s));
+    DenseProblem p = product(w.xq, w.ldx, w_gate, d.ld_w_in, T, I, H, w.h, w.ldf, 1, 4);
+    p.b[1] = u8(w_up);
+    p.xs = w.xs;
+    p.ws[0] = gate_scale;
+    p.ws[1] = up_scale;
+    if (const int rc = run(kDenseIntGated, FT_DT_F32, p, s)) return rc;
+    FT_HIP_CHECK(launch_int_quantize(FT_DT_F32, T, I, w.h, w.ldf, w.hq, w.ldh, w.hs, s));
+    p = product(w.hq, w.ldh, w_down, d.ld_w_out, T, H, I, y, d.ld_y, 1, 2);
+    p.xs = w.hs;
+    p.ws[0] = p.ws[1] = down_scale;
+    return run(kDenseInt, d.dtype, p, s);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,196 @@
+// Dense (not routed) feed-forward operators: what their translation units share.
+//
+// Every operator is made of matrix products of one form,
+//   C[m][n] = sum_k A(m, k) B(n, k),   m a token or a weight row, n contiguous in C,
+// whose operands lie in memory either along K ("K rows": element (r, k) at
+// r * ld + k) or across it ("K columns": at k * ld + r):
+//   forward  g, u = x Wg^T, x Wu^T     A = x   K rows      B = Wg, Wu  K rows      -> h (and gu)
+//            y = h Wd^T                A = h   K rows      B = Wd      K rows
+//   backward dh = dy Wd                A = dy  K rows      B = Wd      K columns   -> dg, du, h
+//            dx = dg Wg + du Wu        A = dgu K rows      B = Wg, Wu  K columns   (two K segments)
+//            dWg, dWu, dWd             A = dg, du, dy, K columns       B = x, x, h  K columns   (K = tokens)
+//   8 bit    as forward, on codes, with the scales applied to the exact sums
+// Products are given as DenseProblems; one launch takes up to three of the same form.
+#pragma once
+#include "common.h"
+#include "gmem.h"
+
+namespace ftmoe {
+
+// How a product's operands lie and what becomes of its sums.
+enum DenseForm {
+  kDenseGated = 0,  // K rows x K rows, two B matrices: h = silu(g) * u, and gu when given
+  kDenseRows,       // K rows x K rows: c = sums
+  kDenseGrad,       // K rows x K columns: sums are dh; reads gu, writes dgu, and h unless c is null
+  kDenseCols,       // K rows x K columns: c = sums, one or two K segments
+  kDenseOuter,      // K columns x K columns: c = sums
+  kDenseInt,        // 8-bit codes, K rows x K rows: c = xs[m] ws[n] sums
+  kDenseIntGated,   // 8-bit codes, two B matrices: h in fp32
+  kDenseForms
+};
+constexpr bool dense_a_rows(int form) { return form != kDenseOuter; }
+constexpr bool dense_b_rows(int form) {
+  return form == kDenseGated || form == kDenseRows || form == kDenseInt || form == kDenseIntGated;
+}
+constexpr bool dense_two_b(int form) { return form == kDenseGated || form == kDenseIntGated; }
+constexpr bool dense_int(int form) { return form == kDenseInt || form == kDenseIntGated; }
+
+struct DenseProblem {
+  const uint8_t* a[2];   // by K segment
+  const uint8_t* b[2];   // by K segment (kDenseCols), or the two matrices of a gated form
+  int64_t lda, ldb;      // bytes
+  int32_t m, n, k;       // k: elements of each K segment
+  int32_t segs;          // K segments, 1 or 2
+  uint8_t* c;            // h for the gated forms and kDenseGrad
+  int64_t ldc;           // elements, as the following
+  uint8_t* gu;           // kDenseGated: written unless null; kDenseGrad: read
+  int64_t ldgu, off_u;   // u's first column in gu
+  uint8_t* dgu;          // kDenseGrad: written
+  int64_t lddgu, off_du;
+  const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
+  const float* ws[2];
+  int32_t vec4;          // c, gu and dgu take aligned accesses of four elements at n % 4 == 0
+};
+constexpr int kDenseMaxProblems = 3;
+struct DenseLaunch {
+  DenseProblem p[kDenseMaxProblems];
+  int32_t count;
+};
+
+// dense_any.hip: any size, stride and alignment.  dtype: FT_DT_* of the
+// operands (16-bit forms) or of c (kDenseInt).
+hipError_t launch_dense_any(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s);
+
+// int_quant.hip: rows of x (FT_DT_*) to 8-bit codes and scales
+hipError_t launch_int_quantize(int dtype, int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes,
+                               int64_t ld_codes, float* scale, hipStream_t s);
+
+#ifdef __HIPCC__
+// ------------------------------------------------------------ device side
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef int intx16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// Operand types.  A 32x32 matrix instruction takes 16 bytes of K per lane of
+// either operand: lane l holds row l % 32, K bytes 16 (l / 32) .. + 15 of a
+// 32-byte step, and the sums of first-operand rows 8 (i / 4) + 4 (l / 32) +
+// i % 4 and second-operand row l % 32.
+struct DenseBf16 {
+  typedef __bf16 elem;
+  typedef bf16x4 elem4;
+  typedef floatx16 acc;
+  typedef float sum;
+  static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16((bf16x8)a, (bf16x8)b, c, 0, 0, 0);
+  }
+};
+struct DenseF16 {
+  typedef _Float16 elem;
+  typedef f16x4 elem4;
+  typedef floatx16 acc;
+  typedef float sum;
+  static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16((f16x8)a, (f16x8)b, c, 0, 0, 0);
+  }
+};
+struct DenseI8 {
+  typedef int8_t elem;
+  typedef intx16 acc;
+  typedef int sum;
+  static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8((intx4)a, (intx4)b, c, 0, 0, 0);
+  }
+};
+
+// 1 / (1 + e^-g) from the hardware exp2 and reciprocal (each about 1 ulp);
+// e^-g overflowing to infinity gives 0
+__device__ inline float dense_sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+}
+
+// four neighbouring elements of a row: one aligned access when all are there
+// and rows are aligned for it (vec4), else one by one
+template <typename E>
+__device__ inline void dense_store(uint8_t* base, int64_t at, const float* v, int cnt, bool vec4) {
+  typedef E ev4 __attribute__((ext_vector_type(4)));
+  E* p = reinterpret_cast<E*>(base) + at;
+  if (vec4 && cnt == 4) {
+    gstore<ev4>(p, ev4{E(v[0]), E(v[1]), E(v[2]), E(v[3])});
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) gstore<E>(p + i, E(v[i]));
+  }
+}
+template <typename E>
+__device__ inline void dense_load(const uint8_t* base, int64_t at, float* v, int cnt, bool vec4) {
+  typedef E ev4 __attribute__((ext_vector_type(4)));
+  const E* p = reinterpret_cast<const E*>(base) + at;
+  if (vec4 && cnt == 4) {
+    const ev4 x = gload<ev4>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = float(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(gload<E>(p + i)) : 0.f;
+  }
+}
+
+// What becomes of the sums of row m, columns n .. n + cnt - 1 (cnt <= 4; n a
+// multiple of 4); v1: the second matrix of a gated form.  E: the operands'
+// type, TO: c's type where it differs (8-bit forms).  Rounding: h, g, u, dg
+// and du are rounded once, to the type they are stored in, from fp32 values.
+template <int FORM, typename E, typename TO, typename S>
+__device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
+                                                                 const S* v0, const S* v1) {
+  const bool vec4 = p.vec4 != 0;
+  if constexpr (FORM == kDenseRows || FORM == kDenseCols || FORM == kDenseOuter) {
+    dense_store<TO>(p.c, m * p.ldc + n, v0, cnt, vec4);
+  } else if constexpr (FORM == kDenseGated) {
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = v0[i] * dense_sigmoid(v0[i]) * v1[i];
+    dense_store<TO>(p.c, m * p.ldc + n, h, cnt, vec4);
+    if (p.gu) {
+      dense_store<TO>(p.gu, m * p.ldgu + n, v0, cnt, vec4);
+      dense_store<TO>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt, vec4);
+    }
+  } else if constexpr (FORM == kDenseGrad) {
+    float g[4], u[4], dg[4], du[4], h[4];
+    dense_load<E>(p.gu, m * p.ldgu + n, g, cnt, vec4);
+    dense_load<E>(p.gu, m * p.ldgu + p.off_u + n, u, cnt, vec4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = dense_sigmoid(g[i]), gs = g[i] * s;
+      dg[i] = v0[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      du[i] = v0[i] * gs;
+      h[i] = gs * u[i];
+    }
+    dense_store<E>(p.dgu, m * p.lddgu + n, dg, cnt, vec4);
+    dense_store<E>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt, vec4);
+    if (p.c) dense_store<E>(p.c, m * p.ldc + n, h, cnt, vec4);
+  } else {
+    // the int32 sums are exact; their conversion and the scales round in fp32
+    const float xs = p.xs[m];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(v0[i]) * xs * p.ws[0][n + i] : 0.f;
+    if constexpr (FORM == kDenseIntGated) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = i < cnt ? float(v1[i]) * xs * p.ws[1][n + i] : 0.f;
+        v[i] = v[i] * dense_sigmoid(v[i]) * u;
+      }
+    }
+    dense_store<TO>(p.c, m * p.ldc + n, v, cnt, vec4);
+  }
+}
+#endif
+
+}  // namespace ftmoe
