@@ -1,5 +1,6 @@
 // C entry points of the dense feed-forward operators: argument checks, the
 // layout of the scratch memory, and the sequence of products of each call.
+#include <algorithm>
 #include <initializer_list>
 
 #include "dense.h"
@@ -109,22 +110,6 @@ int check_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
   return FT_OK;
 }
 
-// ------------------------------------------------------------ gated block
-struct FfnWork {
-  int64_t ldi;  // elements between rows of h, and half of a row of dgu
-  uint8_t *h, *dgu;
-  int64_t bytes;
-};
-FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
-  FfnWork w{};
-  Carve c{static_cast<uint8_t*>(base)};
-  w.ldi = up(d.inter, 64);
-  w.h = c.take(int64_t(d.tokens) * w.ldi * 2);
-  if (backward) w.dgu = c.take(int64_t(d.tokens) * w.ldi * 4);
-  w.bytes = c.used;
-  return w;
-}
-
 const uint8_t* u8(const void* p) { return static_cast<const uint8_t*>(p); }
 uint8_t* u8(void* p) { return static_cast<uint8_t*>(p); }
 
@@ -145,15 +130,64 @@ DenseProblem product(const void* a, int64_t lda, const void* b, int64_t ldb, int
   return p;
 }
 
-int run(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s) {
-  FT_HIP_CHECK(launch_dense_any(form, dtype, l, s));
+DenseShape shape(const DenseProblem& p) { return {p.m, p.n, p.k, p.segs}; }
+
+// scratch bytes for the parts of a product's K
+int64_t parts_bytes(DenseForm form, std::initializer_list<DenseShape> shapes) {
+  const int splits = dense_plan(form, shapes.begin(), int(shapes.size())).splits;
+  int64_t n = 0;
+  for (const DenseShape& s : shapes) n += up(dense_part_bytes(form, s, splits), kAlign);
+  return n;
+}
+
+// One launch (two when K is cut into parts): up to three products of one form.
+int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems, uint8_t* part, hipStream_t s) {
+  DenseLaunch l{};
+  DenseShape shapes[kDenseMaxProblems];
+  bool tiled = true;
+  for (const DenseProblem& p : problems) {
+    tiled = tiled && dense_tileable(form, p);
+    shapes[l.count] = shape(p);
+    l.p[l.count++] = p;
+  }
+  l.splits = 1;
+  if (!tiled) {
+    FT_HIP_CHECK(launch_dense_any(form, dtype, l, s));
+    return FT_OK;
+  }
+  const DensePlan plan = dense_plan(form, shapes, l.count);
+  l.splits = plan.splits;
+  for (int i = 0; i < l.count && plan.splits > 1; ++i) {
+    l.p[i].part = part;
+    part += up(dense_part_bytes(form, shapes[i], plan.splits), kAlign);
+  }
+  FT_HIP_CHECK(launch_dense_tile(form, dtype, plan.tile, l, s));
   return FT_OK;
 }
-int run(DenseForm form, int dtype, const DenseProblem& p, hipStream_t s) {
-  DenseLaunch l{};
-  l.p[0] = p;
-  l.count = 1;
-  return run(form, dtype, l, s);
+
+// ------------------------------------------------------------ gated block
+struct FfnWork {
+  int64_t ldi;  // elements between rows of h, and half of a row of dgu
+  uint8_t *h, *dgu, *part;
+  int64_t bytes;
+};
+FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
+  FfnWork w{};
+  Carve c{static_cast<uint8_t*>(base)};
+  w.ldi = up(d.inter, 64);
+  w.h = c.take(int64_t(d.tokens) * w.ldi * 2);
+  const int T = d.tokens, H = d.hidden, I = d.inter;
+  int64_t part;
+  if (backward) {
+    w.dgu = c.take(int64_t(d.tokens) * w.ldi * 4);
+    part = std::max({parts_bytes(kDenseGrad, {{T, I, H, 1}}), parts_bytes(kDenseCols, {{T, H, I, 2}}),
+                     parts_bytes(kDenseOuter, {{I, H, T, 1}, {I, H, T, 1}, {H, I, T, 1}})});
+  } else {
+    part = std::max(parts_bytes(kDenseGated, {{T, I, H, 1}}), parts_bytes(kDenseRows, {{T, H, I, 1}}));
+  }
+  w.part = c.take(part);
+  w.bytes = c.used;
+  return w;
 }
 
 bool same(const void* p, std::initializer_list<const void*> others) {
@@ -181,6 +215,7 @@ struct IntWork {
   int64_t ldx, ldh, ldf;
   int8_t *xq, *hq;
   float *xs, *hs, *h;
+  uint8_t* part;
   int64_t bytes;
 };
 IntWork int_work(const ft_moe_gated_ffn& d, void* base) {
@@ -195,6 +230,8 @@ IntWork int_work(const ft_moe_gated_ffn& d, void* base) {
   w.h = reinterpret_cast<float*>(c.take(T * w.ldf * 4));
   w.hq = reinterpret_cast<int8_t*>(c.take(T * w.ldh));
   w.hs = reinterpret_cast<float*>(c.take(T * 4));
+  w.part = c.take(std::max(parts_bytes(kDenseIntGated, {{d.tokens, d.inter, d.hidden, 1}}),
+                           parts_bytes(kDenseInt, {{d.tokens, d.hidden, d.inter, 1}})));
   w.bytes = c.used;
   return w;
 }
@@ -252,9 +289,9 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
     p.ldgu = d.ld_gu;
     p.off_u = d.inter;
     if (gu) p.vec4 = div4(gu, 2, d.ld_gu) && d.inter % 4 == 0;
-    if (const int rc = run(kDenseGated, d.dtype, p, s)) return rc;
+    if (const int rc = run(kDenseGated, d.dtype, {p}, w.part, s)) return rc;
     p = product(w.h, w.ldi, w_down, d.ld_w_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2, 2);
-    return run(kDenseRows, d.dtype, p, s);
+    return run(kDenseRows, d.dtype, {p}, w.part, s);
   });
 }
 
@@ -295,22 +332,21 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       p.lddgu = 2 * w.ldi;
       p.off_du = w.ldi;
       p.vec4 = div4(gu, 2, d.ld_gu) && I % 4 == 0;
-      if (const int rc = run(kDenseGrad, d.dtype, p, s)) return rc;
+      if (const int rc = run(kDenseGrad, d.dtype, {p}, w.part, s)) return rc;
     }
     if (T > 0 && dx) {
       DenseProblem p = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2, 2);
       p.a[1] = w.dgu + 2 * w.ldi;
       p.b[1] = u8(w_up);
       p.segs = 2;
-      if (const int rc = run(kDenseCols, d.dtype, p, s)) return rc;
+      if (const int rc = run(kDenseCols, d.dtype, {p}, w.part, s)) return rc;
     }
     if (!grads) return FT_OK;
-    DenseLaunch l{};
-    l.p[0] = product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2, 2);
-    l.p[1] = product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2, 2);
-    l.p[2] = product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2, 2);
-    l.count = 3;
-    return run(kDenseOuter, d.dtype, l, s);
+    return run(kDenseOuter, d.dtype,
+               {product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2, 2),
+                product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2, 2),
+                product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2, 2)},
+               w.part, s);
   });
 }
 
@@ -339,7 +375,7 @@ int ft_moe_int_matmul_work(const ft_moe_int_product* d, int64_t* bytes) {
     ft_moe_int_product o;
     if (const int rc = check_product(d, o)) return rc;
     if (!bytes) return bad("bytes is NULL");
-    *bytes = 0;
+    *bytes = parts_bytes(kDenseInt, {{o.tokens, o.out, o.in, 1}});
     return FT_OK;
   });
 }
@@ -350,17 +386,19 @@ int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const flo
     ft_moe_int_product d;
     if (const int rc = check_product(desc, d)) return rc;
     if (d.tokens == 0) return FT_OK;
-    if (const int rc = check_work(work, work_bytes, 0)) return rc;
+    const int64_t need = parts_bytes(kDenseInt, {{d.tokens, d.out, d.in, 1}});
+    if (const int rc = check_work(work, work_bytes, need)) return rc;
     if (same(y, {x, x_scale, w, w_scale, work})) return bad("an output is also another argument");
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const int64_t es = size_of(d.out_dtype);
     DeviceGuard g;
-    if (const int rc = g.enter(s, {{x, 1, "x"}, {x_scale, 4, "x_scale"}, {w, 1, "w"}, {w_scale, 4, "w_scale"}, {y, es, "y"}}))
+    if (const int rc = g.enter(s, {{x, 1, "x"}, {x_scale, 4, "x_scale"}, {w, 1, "w"}, {w_scale, 4, "w_scale"}, {y, es, "y"},
+                                   {need ? work : y, need ? 16 : es, "work"}}))
       return rc;
     DenseProblem p = product(x, d.ld_x, w, d.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1, es);
     p.xs = x_scale;
     p.ws[0] = p.ws[1] = w_scale;
-    return run(kDenseInt, d.out_dtype, p, s);
+    return run(kDenseInt, d.out_dtype, {p}, u8(work), s);
   });
 }
 
@@ -399,12 +437,12 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
     p.xs = w.xs;
     p.ws[0] = gate_scale;
     p.ws[1] = up_scale;
-    if (const int rc = run(kDenseIntGated, FT_DT_F32, p, s)) return rc;
+    if (const int rc = run(kDenseIntGated, FT_DT_F32, {p}, w.part, s)) return rc;
     FT_HIP_CHECK(launch_int_quantize(FT_DT_F32, T, I, w.h, w.ldf, w.hq, w.ldh, w.hs, s));
     p = product(w.hq, w.ldh, w_down, d.ld_w_out, T, H, I, y, d.ld_y, 1, 2);
     p.xs = w.hs;
     p.ws[0] = p.ws[1] = down_scale;
-    return run(kDenseInt, d.dtype, p, s);
+    return run(kDenseInt, d.dtype, {p}, w.part, s);
   });
 }
 

@@ -33,6 +33,7 @@ constexpr bool dense_b_rows(int form) {
   return form == kDenseGated || form == kDenseRows || form == kDenseInt || form == kDenseIntGated;
 }
 constexpr bool dense_two_b(int form) { return form == kDenseGated || form == kDenseIntGated; }
+constexpr int dense_elem(int form) { return form == kDenseInt || form == kDenseIntGated ? 1 : 2; }
 constexpr bool dense_int(int form) { return form == kDenseInt || form == kDenseIntGated; }
 
 struct DenseProblem {
@@ -50,16 +51,39 @@ struct DenseProblem {
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
   int32_t vec4;          // c, gu and dgu take aligned accesses of four elements at n % 4 == 0
+  uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };
 constexpr int kDenseMaxProblems = 3;
 struct DenseLaunch {
   DenseProblem p[kDenseMaxProblems];
   int32_t count;
+  int32_t splits;        // parts that K is cut into (tiled kernels)
+  int32_t tiles;         // of all problems (set by the launchers)
 };
+
+// How a product (or up to three of one form) is run on the tiled kernels:
+// 256 x 256 or 128 x 128 tiles, K cut into `splits` parts whose sums are then
+// added in order by a second kernel.  A rule on sizes alone (dense_plan.cpp).
+struct DensePlan {
+  int32_t tile;
+  int32_t splits;
+};
+struct DenseShape {
+  int32_t m, n, k, segs;
+};
+DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count);
+int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits);
 
 // dense_any.hip: any size, stride and alignment.  dtype: FT_DT_* of the
 // operands (16-bit forms) or of c (kDenseInt).
 hipError_t launch_dense_any(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s);
+
+// dense_tile_*.hip: operands on 16-byte addresses and row distances (dense_tileable)
+bool dense_tileable(DenseForm form, const DenseProblem& p);
+hipError_t launch_dense_tile(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s);
+hipError_t launch_dense_tile_bf16(DenseForm form, int tile, const DenseLaunch& l, hipStream_t s);
+hipError_t launch_dense_tile_f16(DenseForm form, int tile, const DenseLaunch& l, hipStream_t s);
+hipError_t launch_dense_tile_int(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s);
 
 // int_quant.hip: rows of x (FT_DT_*) to 8-bit codes and scales
 hipError_t launch_int_quantize(int dtype, int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes,
@@ -77,7 +101,10 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-// Operand types.  A 32x32 matrix instruction takes 16 bytes of K per lane of
+// Operand types.  A 16x16 matrix instruction takes 16 bytes of K per lane of
+// either operand: lane l holds row l % 16, K bytes 16 (l / 16) .. + 15 of a
+// 64-byte step, and the sums of first-operand rows 4 (l / 16) + i and
+// second-operand row l % 16, i = 0..3.  A 32x32 matrix instruction takes 16 bytes of K per lane of
 // either operand: lane l holds row l % 32, K bytes 16 (l / 32) .. + 15 of a
 // 32-byte step, and the sums of first-operand rows 8 (i / 4) + 4 (l / 32) +
 // i % 4 and second-operand row l % 32.
@@ -89,6 +116,10 @@ struct DenseBf16 {
   static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16((bf16x8)a, (bf16x8)b, c, 0, 0, 0);
   }
+  typedef floatx4 acc4;
+  static __device__ __attribute__((always_inline)) inline acc4 mfma16(u32x4 a, u32x4 b, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16((bf16x8)a, (bf16x8)b, c, 0, 0, 0);
+  }
 };
 struct DenseF16 {
   typedef _Float16 elem;
@@ -98,6 +129,10 @@ struct DenseF16 {
   static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16((f16x8)a, (f16x8)b, c, 0, 0, 0);
   }
+  typedef floatx4 acc4;
+  static __device__ __attribute__((always_inline)) inline acc4 mfma16(u32x4 a, u32x4 b, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16((f16x8)a, (f16x8)b, c, 0, 0, 0);
+  }
 };
 struct DenseI8 {
   typedef int8_t elem;
@@ -105,6 +140,10 @@ struct DenseI8 {
   typedef int sum;
   static __device__ __attribute__((always_inline)) inline acc mfma(u32x4 a, u32x4 b, acc c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8((intx4)a, (intx4)b, c, 0, 0, 0);
+  }
+  typedef intx4 acc4;
+  static __device__ __attribute__((always_inline)) inline acc4 mfma16(u32x4 a, u32x4 b, acc4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8((intx4)a, (intx4)b, c, 0, 0, 0);
   }
 };
 

@@ -1,0 +1,443 @@
+// The dense products on large tiles: device code, instantiated by the
+// dense_tile_*.hip units.
+//
+// A workgroup owns TM x TN results (TN counts the columns of both matrices in
+// a gated form) and walks K in steps of 128 bytes.  Each operand's tile is two
+// halves ("units"), lo and hi, and so is each wave's part of the tile: it owns
+// the four quadrants lo/hi x lo/hi of its rows and columns in accumulators.
+//
+// Schedule.  A step is four products, lo x lo, lo x hi, hi x hi, hi x lo (A x
+// B), chosen so that each unit is read from LDS once, one product ahead of its
+// use, into registers.  Its LDS slot is free from then on, and the load of the
+// same unit two steps later starts at once: with two slots per unit (128 KB for
+// 256 x 256) three halves of a step are always in flight, 1.5 steps ahead of
+// their use.  One barrier per half step makes a half's loads visible (vmcnt of
+// everything older than the two latest halves) and frees the slots read in
+// the half before.  Reads and loads are spread between the matrix
+// instructions.  With one slot's worth less in flight the loop ran 10% slower;
+// with the reads of a step in K order (slots free only at its end) 15%.
+//
+// Loads.  buffer_load ... lds moves 16 bytes per lane straight into LDS, lane
+// i at + 16 i of a uniform address: 1 KB per instruction.  An operand along K
+// is staged as rows of 128 bytes (8 rows per instruction), one across K as its
+// 64 rows of k, a unit's elements wide.  Lanes outside the matrix (rows past
+// the end, K past the end) are given an offset beyond the buffer's range, for
+// which the load writes zeros, so any size runs without an edge case in the loop.
+//
+// Bank conflicts.  Units cannot be padded (the loads write contiguously), so
+// the 16-byte pieces of a row are permuted instead, on the side of the source
+// addresses: row r holds piece c at place c ^ key(r), key(r) distinct for the
+// rows that one LDS cycle reads (SQ_LDS_BANK_CONFLICT counts none).
+//
+// Operands.  Lane l of a 16x16 matrix instruction needs row l % 16, K bytes
+// 16 (l / 16) .. + 15 of a 64-byte step.  Along K that is one 16-byte LDS
+// read.  Across K two ds_read_b64_tr_b16 turn 4 (k) x 16 (row) blocks while
+// they are read: lane i of each group of 16 gives the address of four rows'
+// elements at k = i / 4 and receives row i's four k.  The weights (n) are the
+// first operand, so a lane ends with runs of n of one row m.
+//
+// Bound by the matrix cores at the card's power limit: at 8192^3 the clock
+// drops to 1.9 GHz with them busy 75% of the cycles.  The 16x16 instructions
+// ran 6% faster than the 32x32 ones (which draw more: 1.65 GHz), eight waves
+// 36% faster than four of 128 x 128.  8192^3, sustained: bf16 1.32 PFLOP/s,
+// 8 bit 2.16; K across both operands 1.23.
+#pragma once
+#include <algorithm>
+#include <type_traits>
+
+#include "dense.h"
+
+namespace ftmoe {
+
+#define FT_L3 __attribute__((address_space(3)))
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kOutside = 0x80000000u;  // an offset beyond every buffer's range
+constexpr int kTileKB = 128;                // bytes of K per step
+
+// 16 bytes per lane from buffer r at off to LDS offset lds + 16 * lane
+// (lds uniform); lanes outside the buffer's range write zeros.  Written in
+// assembly because the compiler, unable to tell which LDS bytes such a load
+// writes, waits for all of them before every transposing read.  It has no
+// result register; who reads the LDS bytes waits for vmcnt first.
+typedef uint32_t tile_rsrc __attribute__((ext_vector_type(4)));
+__device__ __attribute__((always_inline)) inline tile_rsrc tile_buffer(const uint8_t* p, uint32_t bytes) {
+  const uint64_t a = uint64_t(uintptr_t(p));
+  return tile_rsrc{uint32_t(a), uint32_t(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+__device__ __attribute__((always_inline)) inline void tile_load16(tile_rsrc r, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(r)
+               : "m0");
+}
+
+// LDS keys: the 16-byte pieces of a staged row are permuted, see above.  An
+// operand along K has 128-byte rows, two of them side by side over the 256
+// bytes of the banks; one LDS cycle of a fragment read takes the 16 rows of 16
+// lanes.  B rows are handed out to lanes as n = 8 (r / 4) + 4 t + r % 4 (lane
+// row r, fragment t of a pair), so a lane's sums of a pair are 8 neighbours.
+__device__ __attribute__((always_inline)) inline int tile_key_a(int r) { return (r >> 1) & 7; }
+__device__ __attribute__((always_inline)) inline int tile_key_b(int n) { return ((n >> 1) & 1) | ((n >> 3) & 3) << 1; }
+// An operand across K: rows of R elements of one k; one LDS cycle of a
+// transposing read takes 32 bytes of the rows k = 0..3 and 8..11 (+ 4, + 16).
+template <int R>
+__device__ __attribute__((always_inline)) inline int tile_key_cols(int k) {
+  return R >= 128 ? ((k & 3) | ((k >> 3) & 1) << 2) << 1 : (((k >> 1) & 1) | ((k >> 3) & 1) << 1) << 1;
+}
+
+// One operand: halves (units) of R rows, loaded by NW waves.
+template <bool ROWS, bool IS_B, int R, int NW, int ES>
+struct TileOperand {
+  static constexpr int kUnit = R * kTileKB;        // bytes of a staged unit
+  static constexpr int kPer = kUnit / 1024 / NW;   // load instructions per wave and unit
+  static constexpr int KE = kTileKB / ES;
+  static_assert(kPer * NW * 1024 == kUnit, "whole instructions per wave");
+  uint32_t off[kPer];   // byte offset of this lane's piece in a unit at its first K step
+  uint32_t edge[kPer];  // ROWS: the piece's byte in the 128 of its row; else its first column
+  const uint8_t* base[2];  // by K segment, or by matrix (TWO); at the tile's first row
+  int64_t ld;
+  int rows;             // rows (columns) from the tile's first
+
+  __device__ __attribute__((always_inline)) inline void init(int w, int lane) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int idx = w * kPer + q;
+      if constexpr (ROWS) {
+        const int r = idx * 8 + (lane >> 3);
+        edge[q] = uint32_t((lane & 7) ^ (IS_B ? tile_key_b(r) : tile_key_a(r))) * 16;
+        off[q] = uint32_t(r) * uint32_t(ld) + edge[q];
+      } else {
+        constexpr int kPieces = R / 8;
+        const int at = idx * 64 + lane, k = at / kPieces, c = (at % kPieces) ^ tile_key_cols<R>(k);
+        edge[q] = uint32_t(c) * 8;
+        off[q] = uint32_t(k) * uint32_t(ld) + uint32_t(c) * 16;
+      }
+    }
+  }
+  // load instruction q of unit `half` (R rows from half * R; of matrix `half`
+  // from its first row when TWO), K step kb of segment seg, elems of K in it
+  template <bool TWO>
+  __device__ __attribute__((always_inline)) inline void load(int half, int seg, int kb, int elems, uint32_t dst, int w,
+                                                             int q) const {
+    const int first = TWO ? 0 : half * R;
+    const uint8_t* p = base[TWO ? half : seg];
+    dst += uint32_t(w * kPer + q) * 1024;
+    if constexpr (ROWS) {
+      const int64_t at = int64_t(kb) * kTileKB, bytes = max(int64_t(rows - first) * ld - at, int64_t(0));
+      const auto buf = tile_buffer(p + int64_t(first) * ld + at, uint32_t(min(bytes, int64_t(0x7FFFFFFF))));
+      tile_load16(buf, dst, edge[q] < uint32_t(elems * ES) ? off[q] : kOutside);
+    } else {
+      const auto buf = tile_buffer(p + int64_t(kb) * KE * ld + first * ES, uint32_t(elems) * uint32_t(ld));
+      tile_load16(buf, dst, int(edge[q]) < rows - first ? off[q] : kOutside);
+    }
+  }
+};
+
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+struct TileKernel {
+  typedef typename D::elem E;
+  typedef typename D::acc4 Acc;
+  static constexpr bool AR = dense_a_rows(FORM), BR = dense_b_rows(FORM), TWO = dense_two_b(FORM);
+  static constexpr int NW = WM * WN, ES = int(sizeof(E)), KE = kTileKB / ES;
+  static constexpr int HM = TM / 2, HN = TN / 2;             // rows of a unit
+  static constexpr int MF = HM / WM / 16, NF = HN / WN / 16; // fragments of a wave per unit
+  static constexpr int KS = kTileKB / 64;                    // matrix instructions along K per step
+  static constexpr int NOUT = TWO ? HN : TN;                 // output columns of a tile
+  typedef TileOperand<AR, false, HM, NW, ES> OA;
+  typedef TileOperand<BR, true, HN, NW, ES> OB;
+  // LDS: two of each unit: A lo, A hi, B lo, B hi
+  static constexpr int kLds = 2 * (2 * OA::kUnit + 2 * OB::kUnit);
+  static_assert(!BR || NF % 2 == 0, "B rows are handed out to pairs of fragments");
+  static_assert(AR == BR || ES == 2, "8-bit operands lie along K");
+
+  static __device__ __attribute__((always_inline)) inline int at_a(int par, int half) { return (par * 2 + half) * OA::kUnit; }
+  static __device__ __attribute__((always_inline)) inline int at_b(int par, int half) {
+    return (par * 2 + half) * OB::kUnit;  // from the first B unit, 4 A units in
+  }
+
+  struct FragA { u32x4 v[MF][KS]; };
+  struct FragB { u32x4 v[NF][KS]; };
+
+  // LDS addresses of a lane's fragment reads within a unit, one per value that
+  // a constant offset does not reach (the pieces' places are permuted): along
+  // K by K step, for B by fragment of a pair too; across K by fragment
+  static constexpr int kAddrA = AR ? KS : MF, kAddrB = BR ? KS : NF;
+  static __device__ __attribute__((always_inline)) inline uint32_t addr_rows(int row0, int lane, int ks, bool is_b) {
+    const int r = lane & 15, row = is_b ? 8 * (r >> 2) + (r & 3) : r;
+    return uint32_t((row0 + row) * kTileKB + (((4 * ks + (lane >> 4)) ^ (r >> 1)) * 16));
+  }
+  template <int R>
+  static __device__ __attribute__((always_inline)) inline uint32_t addr_cols(int row0, int lane) {
+    const int i = lane & 15, m = row0 + (i & 3) * 4, k = 8 * (lane >> 4) + (i >> 2);
+    return uint32_t(k * (R * 2) + (((m >> 3) ^ tile_key_cols<R>(k)) * 16) + (m & 7) * 2);
+  }
+  static __device__ __attribute__((always_inline)) inline u32x4 lds_rows(uint32_t at) {
+    return *(FT_L3 const u32x4*)at;
+  }
+  template <int R>
+  static __device__ __attribute__((always_inline)) inline u32x4 lds_cols(uint32_t at) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FT_L3 s16x4*)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FT_L3 s16x4*)(at + 4 * R * 2));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 l = (u32x2)lo, h = (u32x2)hi;
+    return u32x4{l[0], l[1], h[0], h[1]};
+  }
+  // read q of a unit's fragments, K steps outermost; unit: its byte offset
+  static __device__ __attribute__((always_inline)) inline void read_a(FragA& f, const uint32_t (&at)[kAddrA], int unit, int q) {
+    const int ks = q / MF, i = q % MF;
+    if constexpr (AR)
+      f.v[i][ks] = lds_rows(at[ks] + unit + i * 16 * kTileKB);
+    else
+      f.v[i][ks] = lds_cols<HM>(at[i] + unit + ks * 32 * HM * 2);
+  }
+  static __device__ __attribute__((always_inline)) inline void read_b(FragB& f, const uint32_t (&at)[kAddrB], int unit, int q) {
+    const int ks = q / NF, j = q % NF;
+    if constexpr (BR)
+      f.v[j][ks] = lds_rows(at[ks] + unit + ((j / 2) * 32 + (j % 2) * 4) * kTileKB);
+    else
+      f.v[j][ks] = lds_cols<HN>(at[j] + unit + ks * 32 * HN * 2);
+  }
+
+  static __device__ __attribute__((always_inline)) inline void run(const DenseLaunch& l, uint8_t* lds) {
+    // workgroups are dealt to the eight XCDs in turn by their number: XCD x
+    // takes the contiguous range x of the tiles, which run down blocks of
+    // kGroup row tiles, so the 32 tiles an XCD works on at a time share rows
+    // of A and of B in its L2
+    const int total = l.tiles * l.splits, lin = int(blockIdx.x);
+    int item = int(int64_t(total) * (lin & 7) / 8) + (lin >> 3);
+    if (item >= int(int64_t(total) * ((lin & 7) + 1) / 8)) return;
+    const int split = item / l.tiles;
+    item -= split * l.tiles;
+    int pi = 0, tm = 0, tn = 0;
+    for (;; ++pi) {
+      tm = (l.p[pi].m + TM - 1) / TM;
+      tn = (l.p[pi].n + NOUT - 1) / NOUT;
+      if (item < tm * tn || pi == l.count - 1) break;
+      item -= tm * tn;
+    }
+    const DenseProblem& p = l.p[pi];
+    constexpr int kGroup = 8;
+    const int grp = item / (kGroup * tn), in = item - grp * kGroup * tn;
+    const int gh = min(kGroup, tm - grp * kGroup);
+    const int m0 = (grp * kGroup + in % gh) * TM, n0 = in / gh * NOUT;
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int wm = w % WM, wn = w / WM;
+
+    OA oa;
+    OB ob;
+    oa.ld = p.lda, oa.rows = p.m - m0;
+    ob.ld = p.ldb, ob.rows = p.n - n0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      oa.base[i] = p.a[i] + (AR ? int64_t(m0) * p.lda : int64_t(m0) * ES);
+      ob.base[i] = p.b[i] + (BR ? int64_t(n0) * p.ldb : int64_t(n0) * ES);
+    }
+    oa.init(w, lane);
+    ob.init(w, lane);
+    // this workgroup's K steps: first .. first + steps - 1 of all
+    const int K = p.k, per = (K + KE - 1) / KE, all = per * p.segs;
+    const int first = int(int64_t(all) * split / l.splits), steps = int(int64_t(all) * (split + 1) / l.splits) - first;
+
+    const uint32_t lds0 = uint32_t(uintptr_t((FT_L3 uint8_t*)lds));
+    // loads of one unit of K step `step`, instruction q; a step past the end loads zeros
+    auto load_a = [&](int step, int par, int half, int q) {
+      const int seg = first + step >= per ? 1 : 0, kb = first + step - seg * per;
+      oa.template load<false>(half, p.segs > 1 ? seg : 0, kb, step < steps ? min(K - kb * KE, KE) : 0, lds0 + at_a(par, half), w, q);
+    };
+    auto load_b = [&](int step, int par, int half, int q) {
+      const int seg = first + step >= per ? 1 : 0, kb = first + step - seg * per;
+      ob.template load<TWO>(half, p.segs > 1 ? seg : 0, kb, step < steps ? min(K - kb * KE, KE) : 0, lds0 + 4 * OA::kUnit + at_b(par, half), w, q);
+    };
+
+    Acc acc[2][2][MF][NF];  // by halves of A and B
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int i = 0; i < MF * NF; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[x >> 1][x & 1][i / NF][i % NF][e] = 0;
+
+    // the products of one pair of units, with more(e) after product e: what is
+    // read and loaded meanwhile is spread between them
+    constexpr int kMma = MF * NF * KS, kReadA = MF * KS, kReadB = NF * KS;
+    auto mma = [&](Acc (&c)[MF][NF], const FragA& a, const FragB& b, auto more) {
+#pragma unroll
+      for (int e = 0; e < kMma; ++e) {
+        const int ks = e / (MF * NF), i = e / NF % MF, j = e % NF;
+        c[i][j] = D::mfma16(b.v[j][ks], a.v[i][ks], c[i][j]);
+        more(e);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto spread = [&](int e, int count, auto what) {
+#pragma unroll
+      for (int q = e * count / kMma; q < (e + 1) * count / kMma; ++q) what(q);
+    };
+    // this wave's LDS reads have ended and all but its latest loads landed; then all waves'
+    constexpr int kHalf = OA::kPer + OB::kPer;  // loads of half a step
+    auto meet = [&]() {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((2 * kHalf) & 0xF | (2 * kHalf) >> 4 << 14 | 0x70);  // vmcnt(2 kHalf) lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+
+    uint32_t addr_a[kAddrA], addr_b[kAddrB];
+#pragma unroll
+    for (int i = 0; i < kAddrA; ++i)
+      addr_a[i] = lds0 + (AR ? addr_rows(wm * MF * 16, lane, i, false) : addr_cols<HM>(wm * MF * 16 + i * 16, lane));
+#pragma unroll
+    for (int i = 0; i < kAddrB; ++i)
+      addr_b[i] = lds0 + 4 * OA::kUnit +
+                  (BR ? addr_rows(wn * NF * 16, lane, i, true) : addr_cols<HN>(wn * NF * 16 + i * 16, lane));
+    FragA al, ah;
+    FragB bx, by;
+    // half steps of loads, in the order they are waited for
+    auto load_lo = [&](int step) {
+#pragma unroll
+      for (int q = 0; q < OA::kPer; ++q) load_a(step, step & 1, 0, q);
+#pragma unroll
+      for (int q = 0; q < OB::kPer; ++q) load_b(step, step & 1, 0, q);
+    };
+    auto load_hi = [&](int step) {
+#pragma unroll
+      for (int q = 0; q < OB::kPer; ++q) load_b(step, step & 1, 1, q);
+#pragma unroll
+      for (int q = 0; q < OA::kPer; ++q) load_a(step, step & 1, 1, q);
+    };
+    load_lo(0);
+    load_hi(0);
+    load_lo(1);
+    meet();
+#pragma unroll
+    for (int q = 0; q < kReadA; ++q) read_a(al, addr_a, at_a(0, 0), q);
+#pragma unroll
+    for (int q = 0; q < kReadB; ++q) read_b(bx, addr_b, at_b(0, 0), q);
+    load_hi(1);
+
+    // one K step: lo x lo, lo x hi, hi x hi, hi x lo; `lo` holds B lo on entry,
+    // `hi` takes B hi and then the next step's B lo
+    auto step = [&](int kb, auto parity, FragB& lo, FragB& hi) {
+      constexpr int P = decltype(parity)::value;  // kb % 2
+      meet();  // B hi, A hi of this step are there; the slots of A lo, B lo are free
+      mma(acc[0][0], al, lo, [&](int e) {
+        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(P, 1), q); });
+        spread(e, OA::kPer, [&](int q) { load_a(kb + 2, P, 0, q); });
+      });
+      mma(acc[0][1], al, hi, [&](int e) {
+        spread(e, kReadA, [&](int q) { read_a(ah, addr_a, at_a(P, 1), q); });
+        spread(e, OB::kPer, [&](int q) { load_b(kb + 2, P, 0, q); });
+      });
+      meet();  // A lo, B lo of the next step are there; the slots of B hi, A hi are free
+      mma(acc[1][1], ah, hi, [&](int e) {
+        spread(e, kReadA, [&](int q) { read_a(al, addr_a, at_a(1 - P, 0), q); });
+        spread(e, OB::kPer, [&](int q) { load_b(kb + 2, P, 1, q); });
+      });
+      mma(acc[1][0], ah, lo, [&](int e) {
+        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(1 - P, 0), q); });
+        spread(e, OA::kPer, [&](int q) { load_a(kb + 2, P, 1, q); });
+      });
+    };
+    int kb = 0;
+    for (; kb + 1 < steps; kb += 2) {
+      step(kb, std::integral_constant<int, 0>(), bx, by);
+      step(kb + 1, std::integral_constant<int, 1>(), by, bx);
+    }
+    if (kb < steps) step(kb, std::integral_constant<int, 0>(), bx, by);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the end
+
+    const int grp4 = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        const int64_t m = m0 + x * HM + wm * MF * 16 + i * 16 + (lane & 15);
+        if (m >= p.m) continue;
+#pragma unroll
+        for (int y = 0; y < (TWO ? 1 : 2); ++y)
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            const int nb = n0 + (TWO ? 0 : y * HN) + wn * NF * 16;
+            const int n = nb + (BR ? (j / 2) * 32 + 8 * grp4 + 4 * (j % 2) : j * 16 + 4 * grp4);
+            const int cnt = min(p.n - n, 4);
+            if (cnt <= 0) continue;
+            typename D::sum v0[4], v1[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v0[q] = acc[x][y][i][j][q], v1[q] = acc[x][1][i][j][q];
+            if (p.part) {
+              // the sums of a part of K: whole groups of four (columns past the end hold zeros)
+              const int64_t ldp = (p.n + 3) / 4 * 4, mat = int64_t(p.m) * ldp;
+              typename D::sum* s = reinterpret_cast<typename D::sum*>(p.part) + split * (TWO ? 2 : 1) * mat + m * ldp + n;
+              gstore<Acc>(s, acc[x][y][i][j]);
+              if constexpr (TWO) gstore<Acc>(s + mat, acc[x][1][i][j]);
+              continue;
+            }
+            dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1);
+          }
+      }
+  }
+};
+
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_dense_tile(DenseLaunch l) {
+  typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[K::kLds];
+  K::run(l, lds);
+}
+
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+hipError_t launch_tile(DenseLaunch l, hipStream_t s) {
+  typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
+  int64_t tiles = 0;
+  for (int i = 0; i < l.count; ++i)
+    tiles += int64_t((l.p[i].m + TM - 1) / TM) * ((l.p[i].n + K::NOUT - 1) / K::NOUT);
+  if (tiles == 0) return hipSuccess;
+  if (tiles * l.splits > (1 << 30)) return hipErrorInvalidValue;
+  l.tiles = int32_t(tiles);
+  const uint32_t grid = uint32_t((tiles * l.splits + 7) / 8 * 8);
+  hipLaunchKernelGGL((k_dense_tile<D, FORM, TO, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
+  return hipGetLastError();
+}
+
+// The parts' sums added in order, then what the form makes of them.  Bound by
+// the reads of the parts.
+template <typename D, int FORM, typename TO>
+__global__ __launch_bounds__(256) void k_dense_join(DenseLaunch l) {
+  typedef typename D::acc4 Acc;
+  constexpr bool TWO = dense_two_b(FORM);
+  const DenseProblem& p = l.p[blockIdx.y];
+  const int64_t ldp = (p.n + 3) / 4 * 4, mat = int64_t(p.m) * ldp;
+  const int64_t at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at >= mat) return;
+  const typename D::sum* s = reinterpret_cast<const typename D::sum*>(p.part) + at;
+  Acc v0 = gload<Acc>(s), v1 = TWO ? gload<Acc>(s + mat) : v0;
+  for (int i = 1; i < l.splits; ++i) {
+    s += (TWO ? 2 : 1) * mat;
+    v0 += gload<Acc>(s);
+    if constexpr (TWO) v1 += gload<Acc>(s + mat);
+  }
+  const int64_t m = at / ldp;
+  const int n = int(at - m * ldp);
+  typename D::sum a[4], b[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a[q] = v0[q], b[q] = v1[q];
+  dense_emit<FORM, typename D::elem, TO>(p, m, n, min(p.n - n, 4), a, b);
+}
+
+template <typename D, int FORM, typename TO>
+hipError_t launch_tiles(int tile, const DenseLaunch& l, hipStream_t s) {
+  const hipError_t e = tile == 256 ? launch_tile<D, FORM, TO, 256, 256, 2, 4>(l, s)
+                                   : launch_tile<D, FORM, TO, 128, 128, 2, 2>(l, s);
+  if (e != hipSuccess || l.splits == 1) return e;
+  int64_t most = 0;
+  for (int i = 0; i < l.count; ++i) most = std::max(most, int64_t(l.p[i].m) * ((l.p[i].n + 3) / 4));
+  if (most == 0) return hipSuccess;
+  hipLaunchKernelGGL((k_dense_join<D, FORM, TO>), dim3(uint32_t((most + 255) / 256), l.count), dim3(256), 0, s, l);
+  return hipGetLastError();
+}
+
+}  // namespace ftmoe
