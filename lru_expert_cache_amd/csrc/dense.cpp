@@ -132,8 +132,14 @@ DenseProblem product(const void* a, int64_t lda, const void* b, int64_t ldb, int
 
 DenseShape shape(const DenseProblem& p) { return {p.m, p.n, p.k, p.segs}; }
 
+// products that dense_few.hip runs
+bool dense_few(DenseForm form, const DenseShape* shapes, int count) {
+  return dense_a_rows(form) && dense_b_rows(form) && count == 1 && shapes[0].m <= kDenseFewRows;
+}
+
 // scratch bytes for the parts of a product's K
 int64_t parts_bytes(DenseForm form, std::initializer_list<DenseShape> shapes) {
+  if (dense_few(form, shapes.begin(), int(shapes.size()))) return 0;
   const int splits = dense_plan(form, shapes.begin(), int(shapes.size())).splits;
   int64_t n = 0;
   for (const DenseShape& s : shapes) n += up(dense_part_bytes(form, s, splits), kAlign);
@@ -153,6 +159,10 @@ int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems,
   l.splits = 1;
   if (!tiled) {
     FT_HIP_CHECK(launch_dense_any(form, dtype, l, s));
+    return FT_OK;
+  }
+  if (dense_few(form, shapes, l.count)) {
+    FT_HIP_CHECK(launch_dense_few(form, dtype, l, s));
     return FT_OK;
   }
   const DensePlan plan = dense_plan(form, shapes, l.count);

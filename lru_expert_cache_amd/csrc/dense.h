@@ -85,6 +85,10 @@ hipError_t launch_dense_tile_bf16(DenseForm form, int tile, const DenseLaunch& l
 hipError_t launch_dense_tile_f16(DenseForm form, int tile, const DenseLaunch& l, hipStream_t s);
 hipError_t launch_dense_tile_int(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s);
 
+// dense_few.hip: tileable products of up to kDenseFewRows tokens, both operands along K
+constexpr int kDenseFewRows = 64;
+hipError_t launch_dense_few(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s);
+
 // int_quant.hip: rows of x (FT_DT_*) to 8-bit codes and scales
 hipError_t launch_int_quantize(int dtype, int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes,
                                int64_t ld_codes, float* scale, hipStream_t s);
