@@ -171,27 +171,50 @@ __device__ inline void dense_store(uint8_t* base, int64_t at, const float* v, in
       if (i < cnt) gstore<E>(p + i, E(v[i]));
   }
 }
+// What the sums of row m, columns n .. n + cnt - 1 are combined with, read
+// ahead of the stores (which the compiler cannot move reads across).
+template <int FORM, typename E>
+struct DenseWith {};
 template <typename E>
-__device__ inline void dense_load(const uint8_t* base, int64_t at, float* v, int cnt, bool vec4) {
+struct DenseWith<kDenseGrad, E> {
   typedef E ev4 __attribute__((ext_vector_type(4)));
-  const E* p = reinterpret_cast<const E*>(base) + at;
-  if (vec4 && cnt == 4) {
-    const ev4 x = gload<ev4>(p);
+  ev4 g, u;
+  __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int64_t m, int n, int cnt) {
+    const E* s = reinterpret_cast<const E*>(p.gu) + m * p.ldgu + n;
+    if (p.vec4 && cnt == 4) {
+      g = gload<ev4>(s);
+      u = gload<ev4>(s + p.off_u);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = float(x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(gload<E>(p + i)) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        g[i] = i < cnt ? gload<E>(s + i) : E(0);
+        u[i] = i < cnt ? gload<E>(s + p.off_u + i) : E(0);
+      }
+    }
   }
-}
+};
+// scales of four columns (of each matrix)
+struct DenseScales {
+  float w0[4], w1[4];
+  template <bool TWO>
+  __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = n + i < p.n ? n + i : p.n - 1;
+      w0[i] = gload<float>(p.ws[0] + at);
+      w1[i] = TWO ? gload<float>(p.ws[1] + at) : 0.f;
+    }
+  }
+};
 
 // What becomes of the sums of row m, columns n .. n + cnt - 1 (cnt <= 4; n a
 // multiple of 4); v1: the second matrix of a gated form.  E: the operands'
 // type, TO: c's type where it differs (8-bit forms).  Rounding: h, g, u, dg
 // and du are rounded once, to the type they are stored in, from fp32 values.
-template <int FORM, typename E, typename TO, typename S>
+template <int FORM, typename E, typename TO>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
-                                                                 const S* v0, const S* v1) {
+                                                                 const float* v0, const float* v1,
+                                                                 const DenseWith<FORM, E>& with) {
   const bool vec4 = p.vec4 != 0;
   if constexpr (FORM == kDenseRows || FORM == kDenseCols || FORM == kDenseOuter) {
     dense_store<TO>(p.c, m * p.ldc + n, v0, cnt, vec4);
@@ -204,34 +227,47 @@ __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProb
       dense_store<TO>(p.gu, m * p.ldgu + n, v0, cnt, vec4);
       dense_store<TO>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt, vec4);
     }
-  } else if constexpr (FORM == kDenseGrad) {
-    float g[4], u[4], dg[4], du[4], h[4];
-    dense_load<E>(p.gu, m * p.ldgu + n, g, cnt, vec4);
-    dense_load<E>(p.gu, m * p.ldgu + p.off_u + n, u, cnt, vec4);
+  } else {
+    static_assert(FORM == kDenseGrad, "8-bit sums take their scales");
+    float dg[4], du[4], h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float s = dense_sigmoid(g[i]), gs = g[i] * s;
-      dg[i] = v0[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      const float g = float(with.g[i]), u = float(with.u[i]);
+      const float s = dense_sigmoid(g), gs = g * s;
+      dg[i] = v0[i] * u * s * (1.0f + g * (1.0f - s));
       du[i] = v0[i] * gs;
-      h[i] = gs * u[i];
+      h[i] = gs * u;
     }
     dense_store<E>(p.dgu, m * p.lddgu + n, dg, cnt, vec4);
     dense_store<E>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt, vec4);
     if (p.c) dense_store<E>(p.c, m * p.ldc + n, h, cnt, vec4);
+  }
+}
+// the 8-bit forms: the int32 sums are exact; their conversion and the scales round in fp32
+template <int FORM, typename TO>
+__device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
+                                                                 const int* v0, const int* v1, float xs,
+                                                                 const DenseScales& ws) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = float(v0[i]) * xs * ws.w0[i];
+    if constexpr (FORM == kDenseIntGated) v[i] = v[i] * dense_sigmoid(v[i]) * (float(v1[i]) * xs * ws.w1[i]);
+  }
+  dense_store<TO>(p.c, m * p.ldc + n, v, cnt, p.vec4 != 0);
+}
+// the same with everything read on the spot
+template <int FORM, typename E, typename TO, typename S>
+__device__ __attribute__((always_inline)) inline void dense_finish(const DenseProblem& p, int64_t m, int n, int cnt,
+                                                                   const S* v0, const S* v1) {
+  if constexpr (dense_int(FORM)) {
+    DenseScales ws;
+    ws.fetch<dense_two_b(FORM)>(p, n);
+    dense_emit<FORM, TO>(p, m, n, cnt, v0, v1, gload<float>(p.xs + m), ws);
   } else {
-    // the int32 sums are exact; their conversion and the scales round in fp32
-    const float xs = p.xs[m];
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(v0[i]) * xs * p.ws[0][n + i] : 0.f;
-    if constexpr (FORM == kDenseIntGated) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = i < cnt ? float(v1[i]) * xs * p.ws[1][n + i] : 0.f;
-        v[i] = v[i] * dense_sigmoid(v[i]) * u;
-      }
-    }
-    dense_store<TO>(p.c, m * p.ldc + n, v, cnt, vec4);
+    DenseWith<FORM, E> with;
+    if constexpr (FORM == kDenseGrad) with.fetch(p, m, n, cnt);
+    dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1, with);
   }
 }
 #endif

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256) void k_dense_any(DenseLaunch l) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v0[j] = acc[0][i + j], v1[j] = acc[NB - 1][i + j];
     const int cnt = p.n - n < 4 ? p.n - n : 4;
-    if (cnt > 0) dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1);
+    if (cnt > 0) dense_finish<FORM, E, TO>(p, m, n, cnt, v0, v1);
   }
 }
 

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
     Sum s0[4], s1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) s0[i] = v0[i], s1[i] = v1[i];
-    if (cnt > 0) dense_emit<FORM, E, TO>(p, m, n, cnt, s0, s1);
+    if (cnt > 0) dense_finish<FORM, E, TO>(p, m, n, cnt, s0, s1);
   }
 }
 

@@ -350,35 +350,73 @@ struct TileKernel {
     if (kb < steps) step(kb, std::integral_constant<int, 0>(), bx, by);
     __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the end
 
+    // results: lane l has row m = l % 16 of each A fragment and four columns of each B fragment
     const int grp4 = lane >> 4;
+    auto column = [&](int y, int j) {
+      return n0 + (TWO ? 0 : y * HN) + wn * NF * 16 + (BR ? (j / 2) * 32 + 8 * grp4 + 4 * (j % 2) : j * 16 + 4 * grp4);
+    };
+    auto row = [&](int xi) { return int64_t(m0) + (xi / MF) * HM + wm * MF * 16 + xi % MF * 16 + (lane & 15); };
+    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF;
+    if (p.part) {
+      // the sums of a part of K: whole groups of four (columns past the end hold zeros)
+      typedef typename D::sum Sum;
+      const int64_t ldp = (p.n + 3) / 4 * 4, mat = int64_t(p.m) * ldp;
+      Sum* const s = reinterpret_cast<Sum*>(p.part) + split * (TWO ? 2 : 1) * mat;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int xi = 0; xi < kRows; ++xi)
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int64_t m = m0 + x * HM + wm * MF * 16 + i * 16 + (lane & 15);
-        if (m >= p.m) continue;
-#pragma unroll
-        for (int y = 0; y < (TWO ? 1 : 2); ++y)
+        for (int y = 0; y < YS; ++y)
 #pragma unroll
           for (int j = 0; j < NF; ++j) {
-            const int nb = n0 + (TWO ? 0 : y * HN) + wn * NF * 16;
-            const int n = nb + (BR ? (j / 2) * 32 + 8 * grp4 + 4 * (j % 2) : j * 16 + 4 * grp4);
-            const int cnt = min(p.n - n, 4);
-            if (cnt <= 0) continue;
-            typename D::sum v0[4], v1[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v0[q] = acc[x][y][i][j][q], v1[q] = acc[x][1][i][j][q];
-            if (p.part) {
-              // the sums of a part of K: whole groups of four (columns past the end hold zeros)
-              const int64_t ldp = (p.n + 3) / 4 * 4, mat = int64_t(p.m) * ldp;
-              typename D::sum* s = reinterpret_cast<typename D::sum*>(p.part) + split * (TWO ? 2 : 1) * mat + m * ldp + n;
-              gstore<Acc>(s, acc[x][y][i][j]);
-              if constexpr (TWO) gstore<Acc>(s + mat, acc[x][1][i][j]);
-              continue;
-            }
-            dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1);
+            const int64_t m = row(xi);
+            const int n = column(y, j);
+            if (m >= p.m || n >= p.n) continue;
+            gstore<Acc>(s + m * ldp + n, acc[xi / MF][y][xi % MF][j]);
+            if constexpr (TWO) gstore<Acc>(s + mat + m * ldp + n, acc[xi / MF][1][xi % MF][j]);
           }
+      return;
+    }
+    // what the sums are combined with is read ahead: the scales at once, gu a row ahead
+    DenseScales ws[YS][NF];
+    float xs[kRows];
+    DenseWith<FORM, E> with[2][YS][NF];
+    if constexpr (dense_int(FORM)) {
+#pragma unroll
+      for (int y = 0; y < YS; ++y)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) ws[y][j].template fetch<TWO>(p, column(y, j));
+#pragma unroll
+      for (int xi = 0; xi < kRows; ++xi) xs[xi] = gload<float>(p.xs + min(row(xi), int64_t(p.m) - 1));
+    }
+    auto fetch = [&](int xi) {
+      if constexpr (FORM == kDenseGrad) {
+#pragma unroll
+        for (int y = 0; y < YS; ++y)
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            with[xi & 1][y][j].fetch(p, row(xi), column(y, j), row(xi) < p.m ? min(p.n - column(y, j), 4) : 0);
       }
+    };
+    fetch(0);
+#pragma unroll
+    for (int xi = 0; xi < kRows; ++xi) {
+      if (xi + 1 < kRows) fetch(xi + 1);
+      const int64_t m = row(xi);
+#pragma unroll
+      for (int y = 0; y < YS; ++y)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const int n = column(y, j), cnt = min(p.n - n, 4);
+          if (m >= p.m || cnt <= 0) continue;
+          typename D::sum v0[4], v1[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v0[q] = acc[xi / MF][y][xi % MF][j][q], v1[q] = acc[xi / MF][1][xi % MF][j][q];
+          if constexpr (dense_int(FORM))
+            dense_emit<FORM, TO>(p, m, n, cnt, v0, v1, xs[xi], ws[y][j]);
+          else
+            dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1, with[xi & 1][y][j]);
+        }
+    }
   }
 };
 
@@ -414,18 +452,28 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseLaunch l) {
   const int64_t at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= mat) return;
   const typename D::sum* s = reinterpret_cast<const typename D::sum*>(p.part) + at;
-  Acc v0 = gload<Acc>(s), v1 = TWO ? gload<Acc>(s + mat) : v0;
-  for (int i = 1; i < l.splits; ++i) {
-    s += (TWO ? 2 : 1) * mat;
-    v0 += gload<Acc>(s);
-    if constexpr (TWO) v1 += gload<Acc>(s + mat);
+  // eight parts are read at a time, and added in order
+  constexpr int kAhead = 8;
+  Acc v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
+  for (int i = 0; i < l.splits; i += kAhead) {
+    Acc a[kAhead], b[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      a[q] = b[q] = Acc{0, 0, 0, 0};
+      if (i + q < l.splits) {
+        a[q] = gload<Acc>(s + (i + q) * (TWO ? 2 : 1) * mat);
+        if constexpr (TWO) b[q] = gload<Acc>(s + ((i + q) * 2 + 1) * mat);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) v0 += a[q], v1 += b[q];
   }
   const int64_t m = at / ldp;
   const int n = int(at - m * ldp);
   typename D::sum a[4], b[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) a[q] = v0[q], b[q] = v1[q];
-  dense_emit<FORM, typename D::elem, TO>(p, m, n, min(p.n - n, 4), a, b);
+  dense_finish<FORM, typename D::elem, TO>(p, m, n, min(p.n - n, 4), a, b);
 }
 
 template <typename D, int FORM, typename TO>

@@ -8,8 +8,8 @@
 // neighbour is nearer and where a tie is.  So codes depend neither on the
 // reciprocal's accuracy nor on the order in which a row is walked.
 //
-// Bound by HBM: each row is read once from memory (the second walk over it
-// finds it in the caches) and its codes are written once.
+// Bound by HBM: each row is read once into registers and its codes are
+// written once.
 #include "dense.h"
 
 namespace ftmoe {
@@ -25,43 +25,55 @@ __device__ inline int row_code(float x, float s, float r) {
   return int(fminf(fmaxf(n, -127.0f), 127.0f));
 }
 
-// Calls f(column, values, count) for up to four neighbouring elements at a time.
-template <typename E, typename F>
-__device__ inline void walk_row(const E* x, int cols, bool vec4, F f) {
+// Four neighbours of a row from column c; beyond the row's end, zeros.
+template <typename E>
+__device__ inline void load4(const E* x, int c, int cols, bool vec4, float* v) {
   typedef E ev4 __attribute__((ext_vector_type(4)));
-  for (int64_t c = int64_t(threadIdx.x) * 4; c < cols; c += int64_t(blockDim.x) * 4) {
-    float v[4];
-    const int cnt = cols - c < 4 ? int(cols - c) : 4;
-    if (vec4 && cnt == 4) {
-      const ev4 e = gload<ev4>(x + c);
+  const int cnt = cols - c;
+  if (vec4 && cnt >= 4) {
+    const ev4 e = gload<ev4>(x + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = float(e[i]);
-    } else {
+    for (int i = 0; i < 4; ++i) v[i] = float(e[i]);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(gload<E>(x + c + i)) : 0.f;
-    }
-    f(c, v, cnt);
+    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(gload<E>(x + c + i)) : 0.f;
   }
 }
 
-template <typename E>
-__global__ __launch_bounds__(256) void k_int_quantize(const E* x, int64_t ld_x, int cols, int8_t* codes,
-                                                      int64_t ld_codes, float* scale, int vec_in, int vec_out) {
+// A row by THREADS threads, which keep up to 4 * GROUPS of its elements each;
+// what a longer row has beyond that is read twice.
+template <typename E, int THREADS, int GROUPS>
+__global__ __launch_bounds__(THREADS) void k_int_quantize(const E* x, int64_t ld_x, int cols, int8_t* codes,
+                                                          int64_t ld_codes, float* scale, int vec_in, int vec_out) {
+  constexpr int kSweep = THREADS * 4;
   const int64_t row = blockIdx.x;
   const E* xr = x + row * ld_x;
   int8_t* cr = codes + row * ld_codes;
-  __shared__ uint32_t top[4];
+  const int c0 = int(threadIdx.x) * 4;
   // magnitudes compare as integers; infinities and NaN lie above every finite one
   uint32_t mx = 0;
-  walk_row<E>(xr, cols, vec_in != 0, [&](int64_t, const float* v, int) {
+  float v[GROUPS][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  });
+  for (int g = 0; g < GROUPS; ++g) load4<E>(xr, c0 + g * kSweep, cols, vec_in != 0, v[g]);
+  for (int c = c0 + GROUPS * kSweep; c < cols; c += kSweep) {
+    float t[4];
+    load4<E>(xr, c, cols, vec_in != 0, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(t[i]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(v[g][i]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) mx = max(mx, uint32_t(__shfl_xor(int(mx), o)));
-  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = mx;
-  __syncthreads();
-  mx = max(max(top[0], top[1]), max(top[2], top[3]));
+  if constexpr (THREADS > 64) {
+    __shared__ uint32_t top[THREADS / 64];
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) mx = max(mx, top[i]);
+  }
   const bool finite = mx < 0x7F800000u;
   const float s = finite ? __uint_as_float(mx) / 127.0f : __uint_as_float(0x7FC00000u);
   if (threadIdx.x == 0) scale[row] = s;
@@ -69,19 +81,26 @@ __global__ __launch_bounds__(256) void k_int_quantize(const E* x, int64_t ld_x, 
   // tiny scales are taken into the normal range, exactly, so that r is finite
   const float k = s < 0x1p-100f ? 0x1p100f : 1.0f;
   const float sk = live ? s * k : 1.0f, r = __builtin_amdgcn_rcpf(sk);
-  walk_row<E>(xr, cols, vec_in != 0, [&](int64_t c, const float* v, int cnt) {
+  auto put = [&](int c, const float* t) {
     int q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = live ? row_code(v[i] * k, sk, r) : 0;
-    if (vec_out && cnt == 4) {
+    for (int i = 0; i < 4; ++i) q[i] = live ? row_code(t[i] * k, sk, r) : 0;
+    if (vec_out && c + 4 <= cols) {
       gstore<uint32_t>(cr + c, uint32_t(q[0] & 255) | uint32_t(q[1] & 255) << 8 | uint32_t(q[2] & 255) << 16 |
                                    uint32_t(q[3]) << 24);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < cnt) gstore<int8_t>(cr + c + i, int8_t(q[i]));
+        if (c + i < cols) gstore<int8_t>(cr + c + i, int8_t(q[i]));
     }
-  });
+  };
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) put(c0 + g * kSweep, v[g]);
+  for (int c = c0 + GROUPS * kSweep; c < cols; c += kSweep) {
+    float t[4];
+    load4<E>(xr, c, cols, vec_in != 0, t);
+    put(c, t);
+  }
 }
 
 template <typename E>
@@ -89,8 +108,17 @@ hipError_t launch(int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_
                   float* scale, hipStream_t s) {
   const int vec_in = reinterpret_cast<uintptr_t>(x) % (4 * sizeof(E)) == 0 && ld_x % 4 == 0;
   const int vec_out = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && ld_codes % 4 == 0;
-  hipLaunchKernelGGL((k_int_quantize<E>), dim3(uint32_t(rows)), dim3(256), 0, s, static_cast<const E*>(x), ld_x, cols,
-                     codes, ld_codes, scale, vec_in, vec_out);
+  const E* e = static_cast<const E*>(x);
+  // 256 threads hold 4096 elements, 512 8192
+  if (cols <= 1024)
+    hipLaunchKernelGGL((k_int_quantize<E, 64, 4>), dim3(uint32_t(rows)), dim3(64), 0, s, e, ld_x, cols, codes, ld_codes,
+                       scale, vec_in, vec_out);
+  else if (cols <= 4096)
+    hipLaunchKernelGGL((k_int_quantize<E, 256, 4>), dim3(uint32_t(rows)), dim3(256), 0, s, e, ld_x, cols, codes,
+                       ld_codes, scale, vec_in, vec_out);
+  else
+    hipLaunchKernelGGL((k_int_quantize<E, 512, 4>), dim3(uint32_t(rows)), dim3(512), 0, s, e, ld_x, cols, codes,
+                       ld_codes, scale, vec_in, vec_out);
   return hipGetLastError();
 }
 
