@@ -93,7 +93,6 @@ bool row_ok(int64_t& ld, int64_t width) {
   if (ld == 0) ld = width;
   return ld >= width && ld < (int64_t(1) << 32);
 }
-bool div4(const void* p, int64_t es, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && ld % 4 == 0; }
 
 // checks a block's description and fills in the row distances
 int check_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
@@ -114,7 +113,7 @@ const uint8_t* u8(const void* p) { return static_cast<const uint8_t*>(p); }
 uint8_t* u8(void* p) { return static_cast<uint8_t*>(p); }
 
 DenseProblem product(const void* a, int64_t lda, const void* b, int64_t ldb, int m, int n, int k, void* c, int64_t ldc,
-                     int64_t es, int64_t es_c) {
+                     int64_t es) {
   DenseProblem p{};
   p.a[0] = p.a[1] = u8(a);
   p.b[0] = p.b[1] = u8(b);
@@ -126,7 +125,6 @@ DenseProblem product(const void* a, int64_t lda, const void* b, int64_t ldb, int
   p.segs = 1;
   p.c = u8(c);
   p.ldc = ldc;
-  p.vec4 = !c || div4(c, es_c, ldc);
   return p;
 }
 
@@ -293,14 +291,13 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
                                    {y, 2, "y"}, {gu ? gu : y, 2, "gu"}, {work, 16, "work"}}))
       return rc;
 
-    DenseProblem p = product(x, d.ld_x, w_gate, d.ld_w_in, d.tokens, d.inter, d.hidden, w.h, w.ldi, 2, 2);
+    DenseProblem p = product(x, d.ld_x, w_gate, d.ld_w_in, d.tokens, d.inter, d.hidden, w.h, w.ldi, 2);
     p.b[1] = u8(w_up);
     p.gu = u8(gu);
     p.ldgu = d.ld_gu;
     p.off_u = d.inter;
-    if (gu) p.vec4 = div4(gu, 2, d.ld_gu) && d.inter % 4 == 0;
     if (const int rc = run(kDenseGated, d.dtype, {p}, w.part, s)) return rc;
-    p = product(w.h, w.ldi, w_down, d.ld_w_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2, 2);
+    p = product(w.h, w.ldi, w_down, d.ld_w_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2);
     return run(kDenseRows, d.dtype, {p}, w.part, s);
   });
 }
@@ -334,18 +331,17 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       return rc;
 
     if (T > 0) {
-      DenseProblem p = product(dy, d.ld_y, w_down, d.ld_w_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2, 2);
+      DenseProblem p = product(dy, d.ld_y, w_down, d.ld_w_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2);
       p.gu = const_cast<uint8_t*>(u8(gu));
       p.ldgu = d.ld_gu;
       p.off_u = I;
       p.dgu = w.dgu;
       p.lddgu = 2 * w.ldi;
       p.off_du = w.ldi;
-      p.vec4 = div4(gu, 2, d.ld_gu) && I % 4 == 0;
       if (const int rc = run(kDenseGrad, d.dtype, {p}, w.part, s)) return rc;
     }
     if (T > 0 && dx) {
-      DenseProblem p = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2, 2);
+      DenseProblem p = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2);
       p.a[1] = w.dgu + 2 * w.ldi;
       p.b[1] = u8(w_up);
       p.segs = 2;
@@ -353,9 +349,9 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
     }
     if (!grads) return FT_OK;
     return run(kDenseOuter, d.dtype,
-               {product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2, 2),
-                product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2, 2),
-                product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2, 2)},
+               {product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2),
+                product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2),
+                product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2)},
                w.part, s);
   });
 }
@@ -405,7 +401,7 @@ int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const flo
     if (const int rc = g.enter(s, {{x, 1, "x"}, {x_scale, 4, "x_scale"}, {w, 1, "w"}, {w_scale, 4, "w_scale"}, {y, es, "y"},
                                    {need ? work : y, need ? 16 : es, "work"}}))
       return rc;
-    DenseProblem p = product(x, d.ld_x, w, d.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1, es);
+    DenseProblem p = product(x, d.ld_x, w, d.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1);
     p.xs = x_scale;
     p.ws[0] = p.ws[1] = w_scale;
     return run(kDenseInt, d.out_dtype, {p}, u8(work), s);
@@ -442,14 +438,14 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
       return rc;
     const int T = d.tokens, H = d.hidden, I = d.inter;
     FT_HIP_CHECK(launch_int_quantize(d.dtype, T, H, x, d.ld_x, w.xq, w.ldx, w.xs, s));
-    DenseProblem p = product(w.xq, w.ldx, w_gate, d.ld_w_in, T, I, H, w.h, w.ldf, 1, 4);
+    DenseProblem p = product(w.xq, w.ldx, w_gate, d.ld_w_in, T, I, H, w.h, w.ldf, 1);
     p.b[1] = u8(w_up);
     p.xs = w.xs;
     p.ws[0] = gate_scale;
     p.ws[1] = up_scale;
     if (const int rc = run(kDenseIntGated, FT_DT_F32, {p}, w.part, s)) return rc;
     FT_HIP_CHECK(launch_int_quantize(FT_DT_F32, T, I, w.h, w.ldf, w.hq, w.ldh, w.hs, s));
-    p = product(w.hq, w.ldh, w_down, d.ld_w_out, T, H, I, y, d.ld_y, 1, 2);
+    p = product(w.hq, w.ldh, w_down, d.ld_w_out, T, H, I, y, d.ld_y, 1);
     p.xs = w.hs;
     p.ws[0] = p.ws[1] = down_scale;
     return run(kDenseInt, d.dtype, {p}, w.part, s);

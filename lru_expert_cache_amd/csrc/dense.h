@@ -50,7 +50,6 @@ struct DenseProblem {
   int64_t lddgu, off_du;
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
-  int32_t vec4;          // c, gu and dgu take aligned accesses of four elements at n % 4 == 0
   uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };
 constexpr int kDenseMaxProblems = 3;
@@ -157,33 +156,37 @@ __device__ inline float dense_sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
 }
 
-// four neighbouring elements of a row: one aligned access when all are there
-// and rows are aligned for it (vec4), else one by one
+// four neighbouring elements of a row at once, whatever their alignment (the
+// memory system takes any), or the cnt that exist one by one
 template <typename E>
-__device__ inline void dense_store(uint8_t* base, int64_t at, const float* v, int cnt, bool vec4) {
-  typedef E ev4 __attribute__((ext_vector_type(4)));
+struct DenseFour {
+  typedef E plain __attribute__((ext_vector_type(4)));
+  typedef plain __attribute__((aligned(1))) any;
+};
+template <typename E>
+__device__ __attribute__((always_inline)) inline void dense_store(uint8_t* base, int64_t at, const float* v, int cnt) {
   E* p = reinterpret_cast<E*>(base) + at;
-  if (vec4 && cnt == 4) {
-    gstore<ev4>(p, ev4{E(v[0]), E(v[1]), E(v[2]), E(v[3])});
+  if (cnt == 4) {
+    gstore<typename DenseFour<E>::any>(p, typename DenseFour<E>::plain{E(v[0]), E(v[1]), E(v[2]), E(v[3])});
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < cnt) gstore<E>(p + i, E(v[i]));
   }
 }
+
 // What the sums of row m, columns n .. n + cnt - 1 are combined with, read
 // ahead of the stores (which the compiler cannot move reads across).
 template <int FORM, typename E>
 struct DenseWith {};
 template <typename E>
 struct DenseWith<kDenseGrad, E> {
-  typedef E ev4 __attribute__((ext_vector_type(4)));
-  ev4 g, u;
+  typename DenseFour<E>::plain g, u;
   __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int64_t m, int n, int cnt) {
     const E* s = reinterpret_cast<const E*>(p.gu) + m * p.ldgu + n;
-    if (p.vec4 && cnt == 4) {
-      g = gload<ev4>(s);
-      u = gload<ev4>(s + p.off_u);
+    if (cnt == 4) {
+      g = gload<typename DenseFour<E>::any>(s);
+      u = gload<typename DenseFour<E>::any>(s + p.off_u);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -215,17 +218,16 @@ template <int FORM, typename E, typename TO>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                  const float* v0, const float* v1,
                                                                  const DenseWith<FORM, E>& with) {
-  const bool vec4 = p.vec4 != 0;
   if constexpr (FORM == kDenseRows || FORM == kDenseCols || FORM == kDenseOuter) {
-    dense_store<TO>(p.c, m * p.ldc + n, v0, cnt, vec4);
+    dense_store<TO>(p.c, m * p.ldc + n, v0, cnt);
   } else if constexpr (FORM == kDenseGated) {
     float h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = v0[i] * dense_sigmoid(v0[i]) * v1[i];
-    dense_store<TO>(p.c, m * p.ldc + n, h, cnt, vec4);
+    dense_store<TO>(p.c, m * p.ldc + n, h, cnt);
     if (p.gu) {
-      dense_store<TO>(p.gu, m * p.ldgu + n, v0, cnt, vec4);
-      dense_store<TO>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt, vec4);
+      dense_store<TO>(p.gu, m * p.ldgu + n, v0, cnt);
+      dense_store<TO>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt);
     }
   } else {
     static_assert(FORM == kDenseGrad, "8-bit sums take their scales");
@@ -238,9 +240,9 @@ __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProb
       du[i] = v0[i] * gs;
       h[i] = gs * u;
     }
-    dense_store<E>(p.dgu, m * p.lddgu + n, dg, cnt, vec4);
-    dense_store<E>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt, vec4);
-    if (p.c) dense_store<E>(p.c, m * p.ldc + n, h, cnt, vec4);
+    dense_store<E>(p.dgu, m * p.lddgu + n, dg, cnt);
+    dense_store<E>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt);
+    if (p.c) dense_store<E>(p.c, m * p.ldc + n, h, cnt);
   }
 }
 // the 8-bit forms: the int32 sums are exact; their conversion and the scales round in fp32
@@ -254,7 +256,7 @@ __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProb
     v[i] = float(v0[i]) * xs * ws.w0[i];
     if constexpr (FORM == kDenseIntGated) v[i] = v[i] * dense_sigmoid(v[i]) * (float(v1[i]) * xs * ws.w1[i]);
   }
-  dense_store<TO>(p.c, m * p.ldc + n, v, cnt, p.vec4 != 0);
+  dense_store<TO>(p.c, m * p.ldc + n, v, cnt);
 }
 // the same with everything read on the spot
 template <int FORM, typename E, typename TO, typename S>

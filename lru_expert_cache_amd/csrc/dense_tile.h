@@ -93,44 +93,34 @@ struct TileOperand {
   static constexpr int kUnit = R * kTileKB;        // bytes of a staged unit
   static constexpr int kPer = kUnit / 1024 / NW;   // load instructions per wave and unit
   static constexpr int KE = kTileKB / ES;
+  static constexpr int kPieces = R / 8;            // !ROWS: 16-byte pieces of a k row
   static_assert(kPer * NW * 1024 == kUnit, "whole instructions per wave");
-  uint32_t off[kPer];   // byte offset of this lane's piece in a unit at its first K step
-  uint32_t edge[kPer];  // ROWS: the piece's byte in the 128 of its row; else its first column
-  const uint8_t* base[2];  // by K segment, or by matrix (TWO); at the tile's first row
-  int64_t ld;
-  int rows;             // rows (columns) from the tile's first
+  uint32_t row;         // this lane's staged row (ROWS: of the unit, else k) in load 0
+  uint32_t edge[kPer];  // ROWS: the piece's byte in the 128 of its row; else in the k row
 
   __device__ __attribute__((always_inline)) inline void init(int w, int lane) {
+    row = ROWS ? uint32_t(w * kPer * 8 + (lane >> 3)) : uint32_t((w * kPer * 64 + lane) / kPieces);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const int idx = w * kPer + q;
-      if constexpr (ROWS) {
-        const int r = idx * 8 + (lane >> 3);
-        edge[q] = uint32_t((lane & 7) ^ (IS_B ? tile_key_b(r) : tile_key_a(r))) * 16;
-        off[q] = uint32_t(r) * uint32_t(ld) + edge[q];
-      } else {
-        constexpr int kPieces = R / 8;
-        const int at = idx * 64 + lane, k = at / kPieces, c = (at % kPieces) ^ tile_key_cols<R>(k);
-        edge[q] = uint32_t(c) * 8;
-        off[q] = uint32_t(k) * uint32_t(ld) + uint32_t(c) * 16;
-      }
+      const int r = int(row) + q * (ROWS ? 8 : 64 / kPieces);
+      edge[q] = ROWS ? uint32_t((lane & 7) ^ (IS_B ? tile_key_b(r) : tile_key_a(r))) * 16
+                     : uint32_t((lane % kPieces) ^ tile_key_cols<R>(r)) * 16;
     }
   }
-  // load instruction q of unit `half` (R rows from half * R; of matrix `half`
-  // from its first row when TWO), K step kb of segment seg, elems of K in it
-  template <bool TWO>
-  __device__ __attribute__((always_inline)) inline void load(int half, int seg, int kb, int elems, uint32_t dst, int w,
-                                                             int q) const {
-    const int first = TWO ? 0 : half * R;
-    const uint8_t* p = base[TWO ? half : seg];
+  // load instruction q of a unit whose first row (column) lies at p and has
+  // `rows` rows (columns) from there on; `elems` elements of K from p on
+  __device__ __attribute__((always_inline)) inline void load(const uint8_t* p, int64_t ld, int rows, int elems, uint32_t dst,
+                                                             int w, int q) const {
     dst += uint32_t(w * kPer + q) * 1024;
+    const uint32_t r = row + uint32_t(q * (ROWS ? 8 : 64 / kPieces));
+    const uint32_t off = r * uint32_t(ld) + edge[q];
     if constexpr (ROWS) {
-      const int64_t at = int64_t(kb) * kTileKB, bytes = max(int64_t(rows - first) * ld - at, int64_t(0));
-      const auto buf = tile_buffer(p + int64_t(first) * ld + at, uint32_t(min(bytes, int64_t(0x7FFFFFFF))));
-      tile_load16(buf, dst, edge[q] < uint32_t(elems * ES) ? off[q] : kOutside);
+      const int64_t bytes = int64_t(max(rows, 0)) * ld;
+      const auto buf = tile_buffer(p, uint32_t(min(bytes, int64_t(0x7FFFFFFF))));
+      tile_load16(buf, dst, edge[q] < uint32_t(elems * ES) ? off : kOutside);
     } else {
-      const auto buf = tile_buffer(p + int64_t(kb) * KE * ld + first * ES, uint32_t(elems) * uint32_t(ld));
-      tile_load16(buf, dst, int(edge[q]) < rows - first ? off[q] : kOutside);
+      const auto buf = tile_buffer(p, uint32_t(elems) * uint32_t(ld));
+      tile_load16(buf, dst, int(edge[q]) < rows * ES ? off : kOutside);
     }
   }
 };
@@ -200,16 +190,19 @@ struct TileKernel {
       f.v[j][ks] = lds_cols<HN>(at[j] + unit + ks * 32 * HN * 2);
   }
 
-  static __device__ __attribute__((always_inline)) inline void run(const DenseLaunch& l, uint8_t* lds) {
-    // workgroups are dealt to the eight XCDs in turn by their number: XCD x
-    // takes the contiguous range x of the tiles, which run down blocks of
-    // kGroup row tiles, so the 32 tiles an XCD works on at a time share rows
-    // of A and of B in its L2
-    const int total = l.tiles * l.splits, lin = int(blockIdx.x);
-    int item = int(int64_t(total) * (lin & 7) / 8) + (lin >> 3);
-    if (item >= int(int64_t(total) * ((lin & 7) + 1) / 8)) return;
-    const int split = item / l.tiles;
-    item -= split * l.tiles;
+  // Where one workgroup's piece of work (a tile, and a part of K) lies.
+  struct Place {
+    const uint8_t *a[2], *b[2];  // by K segment, or by matrix (TWO); at the tile's first row
+    int64_t lda, ldb;
+    int rows_a, rows_b;          // from the tile's first
+    int k, per, segs;            // elements and steps of a segment
+    int first, count;            // K steps of this part
+    int m0, n0, problem, split;
+  };
+  static __device__ __attribute__((always_inline)) inline Place place(const DenseLaunch& l, int item) {
+    Place o;
+    o.split = item / l.tiles;
+    item -= o.split * l.tiles;
     int pi = 0, tm = 0, tn = 0;
     for (;; ++pi) {
       tm = (l.p[pi].m + TM - 1) / TM;
@@ -218,49 +211,67 @@ struct TileKernel {
       item -= tm * tn;
     }
     const DenseProblem& p = l.p[pi];
+    // down blocks of kGroup row tiles
     constexpr int kGroup = 8;
     const int grp = item / (kGroup * tn), in = item - grp * kGroup * tn;
     const int gh = min(kGroup, tm - grp * kGroup);
-    const int m0 = (grp * kGroup + in % gh) * TM, n0 = in / gh * NOUT;
+    o.problem = pi;
+    o.m0 = (grp * kGroup + in % gh) * TM;
+    o.n0 = in / gh * NOUT;
+    o.lda = p.lda;
+    o.ldb = p.ldb;
+    o.rows_a = p.m - o.m0;
+    o.rows_b = p.n - o.n0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o.a[i] = p.a[i] + (AR ? int64_t(o.m0) * p.lda : int64_t(o.m0) * ES);
+      o.b[i] = p.b[i] + (BR ? int64_t(o.n0) * p.ldb : int64_t(o.n0) * ES);
+    }
+    o.k = p.k;
+    o.per = (p.k + KE - 1) / KE;
+    o.segs = p.segs;
+    const int all = o.per * p.segs;
+    o.first = int(int64_t(all) * o.split / l.splits);
+    o.count = int(int64_t(all) * (o.split + 1) / l.splits) - o.first;
+    return o;
+  }
+
+  static __device__ __attribute__((always_inline)) inline void run(const DenseLaunch& l, uint8_t* lds) {
+    // workgroups are dealt to the eight XCDs in turn by their number: XCD x
+    // takes the contiguous range x of the tiles, so the tiles it works on at a
+    // time share rows of A and of B in its L2; a workgroup takes every
+    // (grid / 8)th tile of the range
+    const int total = l.tiles * l.splits, xcd = int(blockIdx.x) & 7, stride = int(gridDim.x) >> 3;
+    const int end = int(int64_t(total) * (xcd + 1) / 8);
+    int item = int(int64_t(total) * xcd / 8) + (int(blockIdx.x) >> 3);
+    if (item >= end) return;
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int wm = w % WM, wn = w / WM;
-
     OA oa;
     OB ob;
-    oa.ld = p.lda, oa.rows = p.m - m0;
-    ob.ld = p.ldb, ob.rows = p.n - n0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      oa.base[i] = p.a[i] + (AR ? int64_t(m0) * p.lda : int64_t(m0) * ES);
-      ob.base[i] = p.b[i] + (BR ? int64_t(n0) * p.ldb : int64_t(n0) * ES);
-    }
     oa.init(w, lane);
     ob.init(w, lane);
-    // this workgroup's K steps: first .. first + steps - 1 of all
-    const int K = p.k, per = (K + KE - 1) / KE, all = per * p.segs;
-    const int first = int(int64_t(all) * split / l.splits), steps = int(int64_t(all) * (split + 1) / l.splits) - first;
-
     const uint32_t lds0 = uint32_t(uintptr_t((FT_L3 uint8_t*)lds));
-    // loads of one unit of K step `step`, instruction q; a step past the end loads zeros
-    auto load_a = [&](int step, int par, int half, int q) {
-      const int seg = first + step >= per ? 1 : 0, kb = first + step - seg * per;
-      oa.template load<false>(half, p.segs > 1 ? seg : 0, kb, step < steps ? min(K - kb * KE, KE) : 0, lds0 + at_a(par, half), w, q);
+    // load instruction q of a unit of step `at` of a place; beyond its steps, zeros
+    auto load_a = [&](const Place& o, int at, int par, int half, int q) {
+      const int s = o.first + at, seg = o.segs > 1 && s >= o.per ? 1 : 0, kb = s - seg * o.per;
+      const int elems = at < o.count ? min(o.k - kb * KE, KE) : 0;
+      const int64_t step = int64_t(kb) * (AR ? int64_t(kTileKB) : KE * o.lda);
+      oa.load(o.a[seg] + step + half * HM * (AR ? o.lda : int64_t(ES)), o.lda, o.rows_a - half * HM, elems,
+              lds0 + at_a(par, half), w, q);
     };
-    auto load_b = [&](int step, int par, int half, int q) {
-      const int seg = first + step >= per ? 1 : 0, kb = first + step - seg * per;
-      ob.template load<TWO>(half, p.segs > 1 ? seg : 0, kb, step < steps ? min(K - kb * KE, KE) : 0, lds0 + 4 * OA::kUnit + at_b(par, half), w, q);
+    auto load_b = [&](const Place& o, int at, int par, int half, int q) {
+      const int s = o.first + at, seg = o.segs > 1 && s >= o.per ? 1 : 0, kb = s - seg * o.per;
+      const int elems = at < o.count ? min(o.k - kb * KE, KE) : 0;
+      const int64_t step = int64_t(kb) * (BR ? int64_t(kTileKB) : KE * o.ldb);
+      const int first = TWO ? 0 : half * HN;
+      ob.load(o.b[TWO ? half : seg] + step + first * (BR ? o.ldb : int64_t(ES)), o.ldb, o.rows_b - first, elems,
+              lds0 + 4 * OA::kUnit + at_b(par, half), w, q);
     };
 
     Acc acc[2][2][MF][NF];  // by halves of A and B
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int i = 0; i < MF * NF; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[x >> 1][x & 1][i / NF][i % NF][e] = 0;
-
     // the products of one pair of units, with more(e) after product e: what is
     // read and loaded meanwhile is spread between them
     constexpr int kMma = MF * NF * KS, kReadA = MF * KS, kReadB = NF * KS;
@@ -296,60 +307,88 @@ struct TileKernel {
                   (BR ? addr_rows(wn * NF * 16, lane, i, true) : addr_cols<HN>(wn * NF * 16 + i * 16, lane));
     FragA al, ah;
     FragB bx, by;
-    // half steps of loads, in the order they are waited for
-    auto load_lo = [&](int step) {
-#pragma unroll
-      for (int q = 0; q < OA::kPer; ++q) load_a(step, step & 1, 0, q);
-#pragma unroll
-      for (int q = 0; q < OB::kPer; ++q) load_b(step, step & 1, 0, q);
+
+    // one K step: lo x lo, lo x hi, hi x hi, hi x lo; `lo` holds B lo on entry,
+    // `hi` takes B hi and then the next step's B lo.  Loads are those of step
+    // `at` of `from`, two steps on.
+    auto step = [&](auto parity, FragB& lo, FragB& hi, const Place& from, int at) {
+      constexpr int P = decltype(parity)::value;
+      meet();  // B hi, A hi of this step are there; the slots of A lo, B lo are free
+      mma(acc[0][0], al, lo, [&](int e) {
+        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(P, 1), q); });
+        spread(e, OA::kPer, [&](int q) { load_a(from, at, P, 0, q); });
+      });
+      mma(acc[0][1], al, hi, [&](int e) {
+        spread(e, kReadA, [&](int q) { read_a(ah, addr_a, at_a(P, 1), q); });
+        spread(e, OB::kPer, [&](int q) { load_b(from, at, P, 0, q); });
+      });
+      meet();  // A lo, B lo of the next step are there; the slots of B hi, A hi are free
+      mma(acc[1][1], ah, hi, [&](int e) {
+        spread(e, kReadA, [&](int q) { read_a(al, addr_a, at_a(1 - P, 0), q); });
+        spread(e, OB::kPer, [&](int q) { load_b(from, at, P, 1, q); });
+      });
+      mma(acc[1][0], ah, lo, [&](int e) {
+        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(1 - P, 0), q); });
+        spread(e, OA::kPer, [&](int q) { load_a(from, at, P, 1, q); });
+      });
     };
-    auto load_hi = [&](int step) {
+
+    // The pipeline is filled once; behind a tile's last steps it loads and
+    // reads the first of the workgroup's next tile.  Steps run in pairs (the
+    // LDS slots alternate): an odd count is filled up with a step of zeros.
+    Place cur = place(l, item);
+    auto fill = [&](int at, int half) {
+      if (half == 0) {
 #pragma unroll
-      for (int q = 0; q < OB::kPer; ++q) load_b(step, step & 1, 1, q);
+        for (int q = 0; q < OA::kPer; ++q) load_a(cur, at, at, 0, q);
+      }
 #pragma unroll
-      for (int q = 0; q < OA::kPer; ++q) load_a(step, step & 1, 1, q);
+      for (int q = 0; q < OB::kPer; ++q) load_b(cur, at, at, half, q);
+      if (half == 1) {
+#pragma unroll
+        for (int q = 0; q < OA::kPer; ++q) load_a(cur, at, at, 1, q);
+      }
     };
-    load_lo(0);
-    load_hi(0);
-    load_lo(1);
+    fill(0, 0);
+    fill(0, 1);
+    fill(1, 0);
     meet();
 #pragma unroll
     for (int q = 0; q < kReadA; ++q) read_a(al, addr_a, at_a(0, 0), q);
 #pragma unroll
     for (int q = 0; q < kReadB; ++q) read_b(bx, addr_b, at_b(0, 0), q);
-    load_hi(1);
+    fill(1, 1);
 
-    // one K step: lo x lo, lo x hi, hi x hi, hi x lo; `lo` holds B lo on entry,
-    // `hi` takes B hi and then the next step's B lo
-    auto step = [&](int kb, auto parity, FragB& lo, FragB& hi) {
-      constexpr int P = decltype(parity)::value;  // kb % 2
-      meet();  // B hi, A hi of this step are there; the slots of A lo, B lo are free
-      mma(acc[0][0], al, lo, [&](int e) {
-        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(P, 1), q); });
-        spread(e, OA::kPer, [&](int q) { load_a(kb + 2, P, 0, q); });
-      });
-      mma(acc[0][1], al, hi, [&](int e) {
-        spread(e, kReadA, [&](int q) { read_a(ah, addr_a, at_a(P, 1), q); });
-        spread(e, OB::kPer, [&](int q) { load_b(kb + 2, P, 0, q); });
-      });
-      meet();  // A lo, B lo of the next step are there; the slots of B hi, A hi are free
-      mma(acc[1][1], ah, hi, [&](int e) {
-        spread(e, kReadA, [&](int q) { read_a(al, addr_a, at_a(1 - P, 0), q); });
-        spread(e, OB::kPer, [&](int q) { load_b(kb + 2, P, 1, q); });
-      });
-      mma(acc[1][0], ah, lo, [&](int e) {
-        spread(e, kReadB, [&](int q) { read_b(hi, addr_b, at_b(1 - P, 0), q); });
-        spread(e, OA::kPer, [&](int q) { load_a(kb + 2, P, 1, q); });
-      });
-    };
-    int kb = 0;
-    for (; kb + 1 < steps; kb += 2) {
-      step(kb, std::integral_constant<int, 0>(), bx, by);
-      step(kb + 1, std::integral_constant<int, 1>(), by, bx);
+    for (;;) {
+      const bool last = item + stride >= end;
+      Place nxt = last ? cur : place(l, item + stride);
+      if (last) nxt.count = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int i = 0; i < MF * NF; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[x >> 1][x & 1][i / NF][i % NF][e] = 0;
+      int kb = 0;
+      for (; kb + 2 < cur.count; kb += 2) {
+        step(std::integral_constant<int, 0>(), bx, by, cur, kb + 2);
+        step(std::integral_constant<int, 1>(), by, bx, cur, kb + 3);
+      }
+      step(std::integral_constant<int, 0>(), bx, by, nxt, 0);
+      step(std::integral_constant<int, 1>(), by, bx, nxt, 1);
+      finish(l, cur, acc, wm, wn, lane);
+      if (last) break;
+      cur = nxt;
+      item += stride;
     }
-    if (kb < steps) step(kb, std::integral_constant<int, 0>(), bx, by);
     __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the end
+  }
 
+  static __device__ __attribute__((always_inline)) inline void finish(const DenseLaunch& l, const Place& o,
+                                                                      const Acc (&acc)[2][2][MF][NF], int wm, int wn,
+                                                                      int lane) {
+    const DenseProblem& p = l.p[o.problem];
+    const int m0 = o.m0, n0 = o.n0, split = o.split;
     // results: lane l has row m = l % 16 of each A fragment and four columns of each B fragment
     const int grp4 = lane >> 4;
     auto column = [&](int y, int j) {
@@ -436,7 +475,9 @@ hipError_t launch_tile(DenseLaunch l, hipStream_t s) {
   if (tiles == 0) return hipSuccess;
   if (tiles * l.splits > (1 << 30)) return hipErrorInvalidValue;
   l.tiles = int32_t(tiles);
-  const uint32_t grid = uint32_t((tiles * l.splits + 7) / 8 * 8);
+  // as many workgroups as run at a time: one per CU, or two of the small ones
+  const int64_t most = 256 * (K::kLds <= 65536 ? 2 : 1);
+  const uint32_t grid = uint32_t(std::min(most, (tiles * l.splits + 7) / 8 * 8));
   hipLaunchKernelGGL((k_dense_tile<D, FORM, TO, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
   return hipGetLastError();
 }

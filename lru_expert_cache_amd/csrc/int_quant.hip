@@ -25,46 +25,47 @@ __device__ inline int row_code(float x, float s, float r) {
   return int(fminf(fmaxf(n, -127.0f), 127.0f));
 }
 
-// Four neighbours of a row from column c; beyond the row's end, zeros.
-template <typename E>
-__device__ inline void load4(const E* x, int c, int cols, bool vec4, float* v) {
-  typedef E ev4 __attribute__((ext_vector_type(4)));
+// 16 bytes of a row (4 or 8 neighbours) from column c; beyond the row's end, zeros.
+template <typename E, int N>
+__device__ __attribute__((always_inline)) inline void load16(const E* x, int c, int cols, float* v) {
+  typedef E raw __attribute__((ext_vector_type(N)));
+  typedef raw __attribute__((aligned(1))) any;
   const int cnt = cols - c;
-  if (vec4 && cnt >= 4) {
-    const ev4 e = gload<ev4>(x + c);
+  if (cnt >= N) {
+    const raw e = gload<any>(x + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = float(e[i]);
+    for (int i = 0; i < N; ++i) v[i] = float(e[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < cnt ? float(gload<E>(x + c + i)) : 0.f;
+    for (int i = 0; i < N; ++i) v[i] = i < cnt ? float(gload<E>(x + c + i)) : 0.f;
   }
 }
 
-// A row by THREADS threads, which keep up to 4 * GROUPS of its elements each;
+// A row by THREADS threads, which keep up to GROUPS pieces of 16 bytes of it each;
 // what a longer row has beyond that is read twice.
 template <typename E, int THREADS, int GROUPS>
 __global__ __launch_bounds__(THREADS) void k_int_quantize(const E* x, int64_t ld_x, int cols, int8_t* codes,
-                                                          int64_t ld_codes, float* scale, int vec_in, int vec_out) {
-  constexpr int kSweep = THREADS * 4;
+                                                          int64_t ld_codes, float* scale) {
+  constexpr int N = 16 / int(sizeof(E)), kSweep = THREADS * N;
   const int64_t row = blockIdx.x;
   const E* xr = x + row * ld_x;
   int8_t* cr = codes + row * ld_codes;
-  const int c0 = int(threadIdx.x) * 4;
+  const int c0 = int(threadIdx.x) * N;
   // magnitudes compare as integers; infinities and NaN lie above every finite one
   uint32_t mx = 0;
-  float v[GROUPS][4];
+  float v[GROUPS][N];
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) load4<E>(xr, c0 + g * kSweep, cols, vec_in != 0, v[g]);
+  for (int g = 0; g < GROUPS; ++g) load16<E, N>(xr, c0 + g * kSweep, cols, v[g]);
   for (int c = c0 + GROUPS * kSweep; c < cols; c += kSweep) {
-    float t[4];
-    load4<E>(xr, c, cols, vec_in != 0, t);
+    float t[N];
+    load16<E, N>(xr, c, cols, t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(t[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i) mx = max(mx, __float_as_uint(t[i]) & 0x7FFFFFFFu);
   }
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(v[g][i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i) mx = max(mx, __float_as_uint(v[g][i]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) mx = max(mx, uint32_t(__shfl_xor(int(mx), o)));
   if constexpr (THREADS > 64) {
@@ -82,23 +83,24 @@ __global__ __launch_bounds__(THREADS) void k_int_quantize(const E* x, int64_t ld
   const float k = s < 0x1p-100f ? 0x1p100f : 1.0f;
   const float sk = live ? s * k : 1.0f, r = __builtin_amdgcn_rcpf(sk);
   auto put = [&](int c, const float* t) {
-    int q[4];
+    typedef int8_t bytes __attribute__((ext_vector_type(N)));
+    typedef bytes __attribute__((aligned(1))) any;
+    bytes q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = live ? row_code(t[i] * k, sk, r) : 0;
-    if (vec_out && c + 4 <= cols) {
-      gstore<uint32_t>(cr + c, uint32_t(q[0] & 255) | uint32_t(q[1] & 255) << 8 | uint32_t(q[2] & 255) << 16 |
-                                   uint32_t(q[3]) << 24);
+    for (int i = 0; i < N; ++i) q[i] = int8_t(live ? row_code(t[i] * k, sk, r) : 0);
+    if (c + N <= cols) {
+      gstore<any>(cr + c, q);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < cols) gstore<int8_t>(cr + c + i, int8_t(q[i]));
+      for (int i = 0; i < N; ++i)
+        if (c + i < cols) gstore<int8_t>(cr + c + i, q[i]);
     }
   };
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) put(c0 + g * kSweep, v[g]);
   for (int c = c0 + GROUPS * kSweep; c < cols; c += kSweep) {
-    float t[4];
-    load4<E>(xr, c, cols, vec_in != 0, t);
+    float t[N];
+    load16<E, N>(xr, c, cols, t);
     put(c, t);
   }
 }
@@ -106,19 +108,15 @@ __global__ __launch_bounds__(THREADS) void k_int_quantize(const E* x, int64_t ld
 template <typename E>
 hipError_t launch(int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
                   float* scale, hipStream_t s) {
-  const int vec_in = reinterpret_cast<uintptr_t>(x) % (4 * sizeof(E)) == 0 && ld_x % 4 == 0;
-  const int vec_out = reinterpret_cast<uintptr_t>(codes) % 4 == 0 && ld_codes % 4 == 0;
   const E* e = static_cast<const E*>(x);
-  // 256 threads hold 4096 elements, 512 8192
-  if (cols <= 1024)
+  // threads for which four pieces each hold the row, up to 256 x 4
+  const int64_t bytes = int64_t(cols) * int64_t(sizeof(E));
+  if (bytes <= 64 * 64)
     hipLaunchKernelGGL((k_int_quantize<E, 64, 4>), dim3(uint32_t(rows)), dim3(64), 0, s, e, ld_x, cols, codes, ld_codes,
-                       scale, vec_in, vec_out);
-  else if (cols <= 4096)
-    hipLaunchKernelGGL((k_int_quantize<E, 256, 4>), dim3(uint32_t(rows)), dim3(256), 0, s, e, ld_x, cols, codes,
-                       ld_codes, scale, vec_in, vec_out);
+                       scale);
   else
-    hipLaunchKernelGGL((k_int_quantize<E, 512, 4>), dim3(uint32_t(rows)), dim3(512), 0, s, e, ld_x, cols, codes,
-                       ld_codes, scale, vec_in, vec_out);
+    hipLaunchKernelGGL((k_int_quantize<E, 256, 4>), dim3(uint32_t(rows)), dim3(256), 0, s, e, ld_x, cols, codes,
+                       ld_codes, scale);
   return hipGetLastError();
 }
 
