@@ -156,53 +156,63 @@ __device__ inline float dense_sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
 }
 
-// four neighbouring elements of a row at once, whatever their alignment (the
+// N neighbouring elements of a row at once, whatever their alignment (the
 // memory system takes any), or the cnt that exist one by one
-template <typename E>
-struct DenseFour {
-  typedef E plain __attribute__((ext_vector_type(4)));
+template <typename E, int N>
+struct DenseRun {
+  typedef E plain __attribute__((ext_vector_type(N)));
   typedef plain __attribute__((aligned(1))) any;
 };
-template <typename E>
+template <typename E, int N>
 __device__ __attribute__((always_inline)) inline void dense_store(uint8_t* base, int64_t at, const float* v, int cnt) {
   E* p = reinterpret_cast<E*>(base) + at;
-  if (cnt == 4) {
-    gstore<typename DenseFour<E>::any>(p, typename DenseFour<E>::plain{E(v[0]), E(v[1]), E(v[2]), E(v[3])});
+  if (cnt == N) {
+    typename DenseRun<E, N>::plain x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = E(v[i]);
+    gstore<typename DenseRun<E, N>::any>(p, x);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < cnt) gstore<E>(p + i, E(v[i]));
   }
 }
 
 // What the sums of row m, columns n .. n + cnt - 1 are combined with, read
 // ahead of the stores (which the compiler cannot move reads across).
-template <int FORM, typename E>
+template <int FORM, typename E, int N>
 struct DenseWith {};
-template <typename E>
-struct DenseWith<kDenseGrad, E> {
-  typename DenseFour<E>::plain g, u;
+template <typename E, int N>
+struct DenseWith<kDenseGrad, E, N> {
+  typename DenseRun<E, N>::plain g, u;
+  // from a place that exists, whole
+  __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int64_t m, int n) {
+    const E* s = reinterpret_cast<const E*>(p.gu) + m * p.ldgu + n;
+    g = gload<typename DenseRun<E, N>::any>(s);
+    u = gload<typename DenseRun<E, N>::any>(s + p.off_u);
+  }
   __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int64_t m, int n, int cnt) {
     const E* s = reinterpret_cast<const E*>(p.gu) + m * p.ldgu + n;
-    if (cnt == 4) {
-      g = gload<typename DenseFour<E>::any>(s);
-      u = gload<typename DenseFour<E>::any>(s + p.off_u);
+    if (cnt == N) {
+      g = gload<typename DenseRun<E, N>::any>(s);
+      u = gload<typename DenseRun<E, N>::any>(s + p.off_u);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N; ++i) {
         g[i] = i < cnt ? gload<E>(s + i) : E(0);
         u[i] = i < cnt ? gload<E>(s + p.off_u + i) : E(0);
       }
     }
   }
 };
-// scales of four columns (of each matrix)
+// scales of N columns (of each matrix)
+template <int N>
 struct DenseScales {
-  float w0[4], w1[4];
+  float w0[N], w1[N];
   template <bool TWO>
   __device__ __attribute__((always_inline)) inline void fetch(const DenseProblem& p, int n) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int at = n + i < p.n ? n + i : p.n - 1;
       w0[i] = gload<float>(p.ws[0] + at);
       w1[i] = TWO ? gload<float>(p.ws[1] + at) : 0.f;
@@ -210,66 +220,65 @@ struct DenseScales {
   }
 };
 
-// What becomes of the sums of row m, columns n .. n + cnt - 1 (cnt <= 4; n a
-// multiple of 4); v1: the second matrix of a gated form.  E: the operands'
+// What becomes of the sums of row m, columns n .. n + cnt - 1 (cnt <= N); v1: the second matrix of a gated form.  E: the operands'
 // type, TO: c's type where it differs (8-bit forms).  Rounding: h, g, u, dg
 // and du are rounded once, to the type they are stored in, from fp32 values.
-template <int FORM, typename E, typename TO>
+template <int FORM, typename E, typename TO, int N>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                  const float* v0, const float* v1,
-                                                                 const DenseWith<FORM, E>& with) {
+                                                                 const DenseWith<FORM, E, N>& with) {
   if constexpr (FORM == kDenseRows || FORM == kDenseCols || FORM == kDenseOuter) {
-    dense_store<TO>(p.c, m * p.ldc + n, v0, cnt);
+    dense_store<TO, N>(p.c, m * p.ldc + n, v0, cnt);
   } else if constexpr (FORM == kDenseGated) {
-    float h[4];
+    float h[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = v0[i] * dense_sigmoid(v0[i]) * v1[i];
-    dense_store<TO>(p.c, m * p.ldc + n, h, cnt);
+    for (int i = 0; i < N; ++i) h[i] = v0[i] * dense_sigmoid(v0[i]) * v1[i];
+    dense_store<TO, N>(p.c, m * p.ldc + n, h, cnt);
     if (p.gu) {
-      dense_store<TO>(p.gu, m * p.ldgu + n, v0, cnt);
-      dense_store<TO>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt);
+      dense_store<TO, N>(p.gu, m * p.ldgu + n, v0, cnt);
+      dense_store<TO, N>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt);
     }
   } else {
     static_assert(FORM == kDenseGrad, "8-bit sums take their scales");
-    float dg[4], du[4], h[4];
+    float dg[N], du[N], h[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float g = float(with.g[i]), u = float(with.u[i]);
       const float s = dense_sigmoid(g), gs = g * s;
       dg[i] = v0[i] * u * s * (1.0f + g * (1.0f - s));
       du[i] = v0[i] * gs;
       h[i] = gs * u;
     }
-    dense_store<E>(p.dgu, m * p.lddgu + n, dg, cnt);
-    dense_store<E>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt);
-    if (p.c) dense_store<E>(p.c, m * p.ldc + n, h, cnt);
+    dense_store<E, N>(p.dgu, m * p.lddgu + n, dg, cnt);
+    dense_store<E, N>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt);
+    if (p.c) dense_store<E, N>(p.c, m * p.ldc + n, h, cnt);
   }
 }
 // the 8-bit forms: the int32 sums are exact; their conversion and the scales round in fp32
-template <int FORM, typename TO>
+template <int FORM, typename TO, int N>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                  const int* v0, const int* v1, float xs,
-                                                                 const DenseScales& ws) {
-  float v[4];
+                                                                 const DenseScales<N>& ws) {
+  float v[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     v[i] = float(v0[i]) * xs * ws.w0[i];
     if constexpr (FORM == kDenseIntGated) v[i] = v[i] * dense_sigmoid(v[i]) * (float(v1[i]) * xs * ws.w1[i]);
   }
-  dense_store<TO>(p.c, m * p.ldc + n, v, cnt);
+  dense_store<TO, N>(p.c, m * p.ldc + n, v, cnt);
 }
 // the same with everything read on the spot
 template <int FORM, typename E, typename TO, typename S>
 __device__ __attribute__((always_inline)) inline void dense_finish(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                    const S* v0, const S* v1) {
   if constexpr (dense_int(FORM)) {
-    DenseScales ws;
+    DenseScales<4> ws;
     ws.fetch<dense_two_b(FORM)>(p, n);
-    dense_emit<FORM, TO>(p, m, n, cnt, v0, v1, gload<float>(p.xs + m), ws);
+    dense_emit<FORM, TO, 4>(p, m, n, cnt, v0, v1, gload<float>(p.xs + m), ws);
   } else {
-    DenseWith<FORM, E> with;
+    DenseWith<FORM, E, 4> with;
     if constexpr (FORM == kDenseGrad) with.fetch(p, m, n, cnt);
-    dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1, with);
+    dense_emit<FORM, E, TO, 4>(p, m, n, cnt, v0, v1, with);
   }
 }
 #endif

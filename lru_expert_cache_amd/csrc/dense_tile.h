@@ -139,7 +139,7 @@ struct TileKernel {
   typedef TileOperand<BR, true, HN, NW, ES> OB;
   // LDS: two of each unit: A lo, A hi, B lo, B hi
   static constexpr int kLds = 2 * (2 * OA::kUnit + 2 * OB::kUnit);
-  static_assert(!BR || NF % 2 == 0, "B rows are handed out to pairs of fragments");
+  static_assert(NF % 2 == 0, "B rows are handed out to pairs of fragments");
   static_assert(AR == BR || ES == 2, "8-bit operands lie along K");
 
   static __device__ __attribute__((always_inline)) inline int at_a(int par, int half) { return (par * 2 + half) * OA::kUnit; }
@@ -158,9 +158,11 @@ struct TileKernel {
     const int r = lane & 15, row = is_b ? 8 * (r >> 2) + (r & 3) : r;
     return uint32_t((row0 + row) * kTileKB + (((4 * ks + (lane >> 4)) ^ (r >> 1)) * 16));
   }
+  // B fragments come in pairs there too: fragment t of a pair takes the columns
+  // 8 c + 4 t .. + 3, c = 0..3 (its reads then meet each bank twice)
   template <int R>
-  static __device__ __attribute__((always_inline)) inline uint32_t addr_cols(int row0, int lane) {
-    const int i = lane & 15, m = row0 + (i & 3) * 4, k = 8 * (lane >> 4) + (i >> 2);
+  static __device__ __attribute__((always_inline)) inline uint32_t addr_cols(int row0, int lane, bool pairs) {
+    const int i = lane & 15, m = row0 + (i & 3) * (pairs ? 8 : 4), k = 8 * (lane >> 4) + (i >> 2);
     return uint32_t(k * (R * 2) + (((m >> 3) ^ tile_key_cols<R>(k)) * 16) + (m & 7) * 2);
   }
   static __device__ __attribute__((always_inline)) inline u32x4 lds_rows(uint32_t at) {
@@ -300,11 +302,11 @@ struct TileKernel {
     uint32_t addr_a[kAddrA], addr_b[kAddrB];
 #pragma unroll
     for (int i = 0; i < kAddrA; ++i)
-      addr_a[i] = lds0 + (AR ? addr_rows(wm * MF * 16, lane, i, false) : addr_cols<HM>(wm * MF * 16 + i * 16, lane));
+      addr_a[i] = lds0 + (AR ? addr_rows(wm * MF * 16, lane, i, false) : addr_cols<HM>(wm * MF * 16 + i * 16, lane, false));
 #pragma unroll
     for (int i = 0; i < kAddrB; ++i)
       addr_b[i] = lds0 + 4 * OA::kUnit +
-                  (BR ? addr_rows(wn * NF * 16, lane, i, true) : addr_cols<HN>(wn * NF * 16 + i * 16, lane));
+                  (BR ? addr_rows(wn * NF * 16, lane, i, true) : addr_cols<HN>(wn * NF * 16 + (i / 2) * 32 + i % 2 * 4, lane, true));
     FragA al, ah;
     FragB bx, by;
 
@@ -389,13 +391,10 @@ struct TileKernel {
                                                                       int lane) {
     const DenseProblem& p = l.p[o.problem];
     const int m0 = o.m0, n0 = o.n0, split = o.split;
-    // results: lane l has row m = l % 16 of each A fragment and four columns of each B fragment
-    const int grp4 = lane >> 4;
-    auto column = [&](int y, int j) {
-      return n0 + (TWO ? 0 : y * HN) + wn * NF * 16 + (BR ? (j / 2) * 32 + 8 * grp4 + 4 * (j % 2) : j * 16 + 4 * grp4);
-    };
+    // results: lane l has row m = l % 16 of each A fragment and eight columns of each pair of B fragments
+    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF, PF = NF / 2;
+    auto column = [&](int y, int j) { return n0 + (TWO ? 0 : y * HN) + wn * NF * 16 + j * 32 + 8 * (lane >> 4); };
     auto row = [&](int xi) { return int64_t(m0) + (xi / MF) * HM + wm * MF * 16 + xi % MF * 16 + (lane & 15); };
-    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF;
     if (p.part) {
       // the sums of a part of K: whole groups of four (columns past the end hold zeros)
       typedef typename D::sum Sum;
@@ -408,22 +407,37 @@ struct TileKernel {
 #pragma unroll
           for (int j = 0; j < NF; ++j) {
             const int64_t m = row(xi);
-            const int n = column(y, j);
+            const int n = column(y, j / 2) + j % 2 * 4;
             if (m >= p.m || n >= p.n) continue;
             gstore<Acc>(s + m * ldp + n, acc[xi / MF][y][xi % MF][j]);
             if constexpr (TWO) gstore<Acc>(s + mat + m * ldp + n, acc[xi / MF][1][xi % MF][j]);
           }
       return;
     }
-    // what the sums are combined with is read ahead: the scales at once, gu a row ahead
-    DenseScales ws[YS][NF];
+    // rows of a multiple of eight: whole groups, without a branch around a load
+    if (p.n % 8 == 0)
+      emit<true>(p, acc, row, column);
+    else
+      emit<false>(p, acc, row, column);
+  }
+
+  // What the sums are combined with is read ahead of the stores: the scales at
+  // once, gu some rows ahead (what the registers hold).  WHOLE: columns come in
+  // whole groups of eight; reads outside the matrix are moved to its last row
+  // and group.
+  template <bool WHOLE, typename ROW, typename COLUMN>
+  static __device__ __attribute__((always_inline)) inline void emit(const DenseProblem& p, const Acc (&acc)[2][2][MF][NF],
+                                                                    ROW row, COLUMN column) {
+    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF, PF = NF / 2;
+    DenseScales<8> ws[YS][PF];
     float xs[kRows];
-    DenseWith<FORM, E> with[2][YS][NF];
+    constexpr int kAhead = kRows <= 4 ? 3 : 1;
+    DenseWith<FORM, E, 8> with[kAhead + 1][YS][PF];
     if constexpr (dense_int(FORM)) {
 #pragma unroll
       for (int y = 0; y < YS; ++y)
 #pragma unroll
-        for (int j = 0; j < NF; ++j) ws[y][j].template fetch<TWO>(p, column(y, j));
+        for (int j = 0; j < PF; ++j) ws[y][j].template fetch<TWO>(p, column(y, j));
 #pragma unroll
       for (int xi = 0; xi < kRows; ++xi) xs[xi] = gload<float>(p.xs + min(row(xi), int64_t(p.m) - 1));
     }
@@ -432,28 +446,35 @@ struct TileKernel {
 #pragma unroll
         for (int y = 0; y < YS; ++y)
 #pragma unroll
-          for (int j = 0; j < NF; ++j)
-            with[xi & 1][y][j].fetch(p, row(xi), column(y, j), row(xi) < p.m ? min(p.n - column(y, j), 4) : 0);
+          for (int j = 0; j < PF; ++j)
+            if constexpr (WHOLE)
+              with[xi % (kAhead + 1)][y][j].fetch(p, min(row(xi), int64_t(p.m) - 1), min(column(y, j), p.n - 8));
+            else
+              with[xi % (kAhead + 1)][y][j].fetch(p, row(xi), column(y, j), row(xi) < p.m ? min(p.n - column(y, j), 8) : 0);
       }
     };
-    fetch(0);
+#pragma unroll
+    for (int xi = 0; xi < kAhead; ++xi) fetch(xi);
 #pragma unroll
     for (int xi = 0; xi < kRows; ++xi) {
-      if (xi + 1 < kRows) fetch(xi + 1);
+      if (xi + kAhead < kRows) fetch(xi + kAhead);
       const int64_t m = row(xi);
 #pragma unroll
       for (int y = 0; y < YS; ++y)
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-          const int n = column(y, j), cnt = min(p.n - n, 4);
-          if (m >= p.m || cnt <= 0) continue;
-          typename D::sum v0[4], v1[4];
+        for (int j = 0; j < PF; ++j) {
+          const int n = column(y, j), cnt = WHOLE ? 8 : min(p.n - n, 8);
+          typename D::sum v0[8], v1[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v0[q] = acc[xi / MF][y][xi % MF][j][q], v1[q] = acc[xi / MF][1][xi % MF][j][q];
+          for (int q = 0; q < 8; ++q) {
+            v0[q] = acc[xi / MF][y][xi % MF][2 * j + q / 4][q % 4];
+            v1[q] = acc[xi / MF][1][xi % MF][2 * j + q / 4][q % 4];
+          }
+          if (m >= p.m || n >= p.n) continue;
           if constexpr (dense_int(FORM))
-            dense_emit<FORM, TO>(p, m, n, cnt, v0, v1, xs[xi], ws[y][j]);
+            dense_emit<FORM, TO, 8>(p, m, n, cnt, v0, v1, xs[xi], ws[y][j]);
           else
-            dense_emit<FORM, E, TO>(p, m, n, cnt, v0, v1, with[xi & 1][y][j]);
+            dense_emit<FORM, E, TO, 8>(p, m, n, cnt, v0, v1, with[xi % (kAhead + 1)][y][j]);
         }
     }
   }
