@@ -145,7 +145,9 @@ int64_t parts_bytes(DenseForm form, std::initializer_list<DenseShape> shapes) {
 }
 
 // One launch (two when K is cut into parts): up to three products of one form.
-int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems, uint8_t* part, hipStream_t s) {
+// clear: queue counters that a tiled launch sets to zero.
+int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems, uint8_t* part, hipStream_t s,
+        uint32_t* clear = nullptr) {
   DenseLaunch l{};
   DenseShape shapes[kDenseMaxProblems];
   bool tiled = true;
@@ -165,6 +167,7 @@ int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems,
   }
   const DensePlan plan = dense_plan(form, shapes, l.count);
   l.splits = plan.splits;
+  l.clear = clear;
   for (int i = 0; i < l.count && plan.splits > 1; ++i) {
     l.p[i].part = part;
     part += up(dense_part_bytes(form, shapes[i], plan.splits), kAlign);
@@ -177,6 +180,7 @@ int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems,
 struct FfnWork {
   int64_t ldi;  // elements between rows of h, and half of a row of dgu
   uint8_t *h, *dgu, *part;
+  uint32_t* queue;
   int64_t bytes;
 };
 FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
@@ -188,6 +192,7 @@ FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
   int64_t part;
   if (backward) {
     w.dgu = c.take(int64_t(d.tokens) * w.ldi * 4);
+    w.queue = reinterpret_cast<uint32_t*>(c.take(kDenseQueue * 4));
     part = std::max({parts_bytes(kDenseGrad, {{T, I, H, 1}}), parts_bytes(kDenseCols, {{T, H, I, 2}}),
                      parts_bytes(kDenseOuter, {{I, H, T, 1}, {I, H, T, 1}, {H, I, T, 1}})});
   } else {
@@ -330,6 +335,19 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
                                    {grads ? dw_down : any, 2, "dw_down"}, {T ? work : any, T ? 16 : 2, "work"}}))
       return rc;
 
+    DenseProblem cols{};
+    DenseProblem outer[3];
+    if (dx) {
+      cols = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2);
+      cols.a[1] = w.dgu + 2 * w.ldi;
+      cols.b[1] = u8(w_up);
+      cols.segs = 2;
+    }
+    if (grads) {
+      outer[0] = product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2);
+      outer[1] = product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2);
+      outer[2] = product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2);
+    }
     if (T > 0) {
       DenseProblem p = product(dy, d.ld_y, w_down, d.ld_w_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2);
       p.gu = const_cast<uint8_t*>(u8(gu));
@@ -338,21 +356,29 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       p.dgu = w.dgu;
       p.lddgu = 2 * w.ldi;
       p.off_du = w.ldi;
-      if (const int rc = run(kDenseGrad, d.dtype, {p}, w.part, s)) return rc;
+      // dx and the weight gradients in one launch, where all can be tiled
+      int pair = 0;
+      if (dx && grads && dense_tileable(kDenseGrad, p) && dense_tileable(kDenseCols, cols) &&
+          dense_tileable(kDenseOuter, outer[0]) && dense_tileable(kDenseOuter, outer[1]) &&
+          dense_tileable(kDenseOuter, outer[2]))
+        pair = dense_plan_pair({shape(outer[0]), shape(outer[1]), shape(outer[2])}, shape(cols));
+      if (const int rc = run(kDenseGrad, d.dtype, {p}, w.part, s, pair ? w.queue : nullptr)) return rc;
+      if (pair) {
+        DensePair l{};
+        for (int i = 0; i < 3; ++i) l.outer.p[i] = outer[i];
+        l.outer.count = 3;
+        l.cols.p[0] = cols;
+        l.cols.count = 1;
+        l.outer.splits = l.cols.splits = 1;
+        l.queue = w.queue;
+        FT_HIP_CHECK(launch_dense_pair(d.dtype, pair, l, s));
+        return FT_OK;
+      }
     }
-    if (T > 0 && dx) {
-      DenseProblem p = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2);
-      p.a[1] = w.dgu + 2 * w.ldi;
-      p.b[1] = u8(w_up);
-      p.segs = 2;
-      if (const int rc = run(kDenseCols, d.dtype, {p}, w.part, s)) return rc;
-    }
+    if (T > 0 && dx)
+      if (const int rc = run(kDenseCols, d.dtype, {cols}, w.part, s)) return rc;
     if (!grads) return FT_OK;
-    return run(kDenseOuter, d.dtype,
-               {product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2),
-                product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2),
-                product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2)},
-               w.part, s);
+    return run(kDenseOuter, d.dtype, {outer[0], outer[1], outer[2]}, w.part, s);
   });
 }
 

@@ -58,6 +58,18 @@ struct DenseLaunch {
   int32_t count;
   int32_t splits;        // parts that K is cut into (tiled kernels)
   int32_t tiles;         // of all problems (set by the launchers)
+  uint32_t* clear;       // kDenseQueue counters that the tiled kernels set to zero, or null
+};
+
+// The backward pass's last products in one launch: the weight gradients
+// (kDenseOuter, not cut into parts) and dx (kDenseCols) share the workgroups,
+// which take tiles from one queue per XCD, the longer ones (the weight
+// gradients') first.  The queue counters must be zero at the start: the launch
+// before, of dh, clears them.  Which workgroup takes a tile changes no result.
+constexpr int kDenseQueue = 8;
+struct DensePair {
+  DenseLaunch outer, cols;
+  uint32_t* queue;
 };
 
 // How a product (or up to three of one form) is run on the tiled kernels:
@@ -71,6 +83,8 @@ struct DenseShape {
   int32_t m, n, k, segs;
 };
 DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count);
+// the tile of a DensePair, or 0 where separate launches are quicker
+int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols);
 int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits);
 
 // dense_any.hip: any size, stride and alignment.  dtype: FT_DT_* of the
@@ -82,6 +96,9 @@ bool dense_tileable(DenseForm form, const DenseProblem& p);
 hipError_t launch_dense_tile(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s);
 hipError_t launch_dense_tile_bf16(DenseForm form, int tile, const DenseLaunch& l, hipStream_t s);
 hipError_t launch_dense_tile_f16(DenseForm form, int tile, const DenseLaunch& l, hipStream_t s);
+hipError_t launch_dense_pair(int dtype, int tile, const DensePair& l, hipStream_t s);
+hipError_t launch_dense_pair_bf16(int tile, const DensePair& l, hipStream_t s);
+hipError_t launch_dense_pair_f16(int tile, const DensePair& l, hipStream_t s);
 hipError_t launch_dense_tile_int(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s);
 
 // dense_few.hip: tileable products of up to kDenseFewRows tokens, both operands along K

@@ -39,44 +39,101 @@ int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits) {
 // 4096 x 2048 x 768: 18.6 against 26.5).  Cutting K costs a second launch and
 // the parts' way to memory and back (77 x 2048 into 768: 23 us in one part,
 // 11 in eight; 4096 x 768 into 2048: 18.6 in one, 39 in two).
-DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count) {
-  constexpr int kCus = 256, kMaxSplits = 32;
-  constexpr double kStart = 4.0, kJoin = 5.0, kJoinBytes = 3.5e6;  // bytes of a part per us, written and read
-  const bool i8 = dense_int(form);
-  // a step of a 256 x 256 tile with few and with all CUs busy; of a 128 x 128
-  // one alone on its CU likewise, of a pair of them, and of a pair at the power
-  // limit; what a tile takes beside its steps
-  const double few256 = i8 ? 1.0 : 1.15, all256 = i8 ? 1.35 : 1.55, tile256 = i8 ? 9.0 : 3.0;
-  const double few128 = 0.36, all128 = i8 ? 0.6 : 0.52, pair128 = i8 ? 0.9 : 0.75, hot128 = i8 ? 1.1 : 1.0, tile128 = 1.5;
+namespace {
+
+constexpr int kCus = 256;
+constexpr double kStart = 4.0;
+
+struct Pace {
+  double few256, all256, tile256;  // a step of a 256 x 256 tile with few and with all CUs busy; a tile beside its steps
+  double few128, all128, pair128, hot128, tile128;  // 128 x 128 alone on its CU; two; two at the power limit
+};
+Pace pace(DenseForm form) {
+  return dense_int(form) ? Pace{1.0, 1.35, 9.0, 0.36, 0.6, 0.9, 1.1, 1.5} : Pace{1.15, 1.55, 3.0, 0.36, 0.52, 0.75, 1.0, 1.5};
+}
+double between(double few, double all, int64_t wgs) { return few + (all - few) * std::min(1.0, double(wgs) / kCus); }
+
+int64_t tiles_of(DenseForm form, const DenseShape& s, int tile) {
+  return parts(s.m, tile) * parts(s.n, dense_two_b(form) ? tile / 2 : tile);
+}
+int64_t steps_of(DenseForm form, const DenseShape& s) { return parts(s.k, 128 / dense_elem(form)) * s.segs; }
+
+// wgs workgroups of `per` steps each
+double tiles_time(DenseForm form, int tile, int64_t wgs, int64_t per) {
+  const Pace p = pace(form);
+  const int64_t each = parts(wgs, kCus);  // a CU's tiles
+  if (tile == 256) return kStart + double(each) * (p.tile256 + per * between(p.few256, p.all256, wgs));
+  double t = kStart + double(each / 2) * (p.tile128 + per * (each <= 8 ? p.pair128 : p.hot128));
+  if (each % 2) t += p.tile128 + per * between(p.few128, p.all128, wgs);
+  return t;
+}
+
+DensePlan plan_of(DenseForm form, const DenseShape* shapes, int count, double* time) {
+  constexpr int kMaxSplits = 32;
+  constexpr double kJoin = 5.0, kJoinBytes = 3.5e6;  // bytes of a part per us, written and read
   const double epilogue = form == kDenseGrad ? 6.0 : 0.0;  // its reads of gu, in one part
-  const int ke = 128 / dense_elem(form);
   DensePlan best{128, 1};
-  double best_t = 1e30;
+  *time = 1e30;
   for (int tile : {256, 128}) {
     int64_t tiles = 0, steps = 0, bytes = 0;
     for (int i = 0; i < count; ++i) {
-      const DenseShape& s = shapes[i];
-      tiles += parts(s.m, tile) * parts(s.n, dense_two_b(form) ? tile / 2 : tile);
-      steps = std::max(steps, parts(s.k, ke) * s.segs);
-      bytes += dense_part_bytes(form, s, 2) / 2;
+      tiles += tiles_of(form, shapes[i], tile);
+      steps = std::max(steps, steps_of(form, shapes[i]));
+      bytes += dense_part_bytes(form, shapes[i], 2) / 2;
     }
     const int most = int(std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, steps / 2)));
     for (int splits = 1; splits <= most; ++splits) {
-      const int64_t wgs = tiles * splits, per = parts(steps, splits);
-      const double busy = std::min(1.0, double(wgs) / kCus);
-      const int64_t each = parts(wgs, kCus);  // a CU's tiles
-      double t = kStart;
-      if (tile == 256) {
-        t += double(each) * (tile256 + per * (few256 + (all256 - few256) * busy));
-      } else {
-        t += double(each / 2) * (tile128 + per * (each <= 8 ? pair128 : hot128));
-        if (each % 2) t += tile128 + per * (few128 + (all128 - few128) * busy);
-      }
+      double t = tiles_time(form, tile, tiles * splits, parts(steps, splits));
       t += splits > 1 ? kJoin + double(splits) * double(bytes) / kJoinBytes : epilogue;
-      if (t < best_t) best_t = t, best = {tile, splits};
+      if (t < *time) *time = t, best = {tile, splits};
     }
   }
   return best;
+}
+
+}  // namespace
+
+DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count) {
+  double t;
+  return plan_of(form, shapes, count, &t);
+}
+
+// One queue of both keeps the CUs busy to the end: its time is the work over
+// the places, but at least one longest tile.  Only products that are not cut
+// alone either are run so: what a gradient comes to does not depend on which
+// others are asked for.
+int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols) {
+  double apart_outer, apart_cols;
+  if (plan_of(kDenseOuter, outer, 3, &apart_outer).splits != 1 ||
+      plan_of(kDenseCols, &cols, 1, &apart_cols).splits != 1)
+    return 0;
+  int best = 0;
+  double best_t = apart_outer + apart_cols;
+  const Pace p = pace(kDenseOuter);
+  for (int tile : {256, 128}) {
+    int64_t wgs = 0, work = 0, longest = 0;
+    auto add = [&](DenseForm form, const DenseShape& s) {
+      const int64_t n = tiles_of(form, s, tile), steps = std::max<int64_t>(2, steps_of(form, s));
+      wgs += n;
+      work += n * steps;
+      if (n) longest = std::max(longest, steps);
+    };
+    for (const DenseShape& s : outer) add(kDenseOuter, s);
+    add(kDenseCols, cols);
+    const double over = tile == 256 ? p.tile256 : p.tile128;
+    const int places = tile == 256 ? kCus : 2 * kCus;
+    const double alone = tile == 256 ? between(p.few256, p.all256, wgs) : between(p.few128, p.all128, wgs);
+    const double all = tile == 256 ? p.all256 : wgs <= 8 * kCus ? p.pair128 : p.hot128;
+    // half a longest tile for the uneven end
+    const double t = kStart + std::max(over + longest * alone,
+                                       (double(work) * all + double(wgs) * over) / places + (wgs > places ? longest * all / 2 : 0.0));
+    if (t < best_t) best_t = t, best = tile;
+  }
+  return best;
+}
+
+hipError_t launch_dense_pair(int dtype, int tile, const DensePair& l, hipStream_t s) {
+  return dtype == FT_DT_F16 ? launch_dense_pair_f16(tile, l, s) : launch_dense_pair_bf16(tile, l, s);
 }
 
 hipError_t launch_dense_tile(DenseForm form, int dtype, int tile, const DenseLaunch& l, hipStream_t s) {

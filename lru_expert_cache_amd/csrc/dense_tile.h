@@ -238,16 +238,17 @@ struct TileKernel {
     return o;
   }
 
-  static __device__ __attribute__((always_inline)) inline void run(const DenseLaunch& l, uint8_t* lds) {
-    // workgroups are dealt to the eight XCDs in turn by their number: XCD x
-    // takes the contiguous range x of the tiles, so the tiles it works on at a
-    // time share rows of A and of B in its L2; a workgroup takes every
-    // (grid / 8)th tile of the range
-    const int total = l.tiles * l.splits, xcd = int(blockIdx.x) & 7, stride = int(gridDim.x) >> 3;
-    const int end = int(int64_t(total) * (xcd + 1) / 8);
-    int item = int(int64_t(total) * xcd / 8) + (int(blockIdx.x) >> 3);
-    if (item >= end) return;
+  // XCD x (workgroups are dealt to the eight in turn by their number) takes
+  // the contiguous range x of the items, so the tiles it works on at a time
+  // share rows of A and of B in its L2.
+  static __device__ __attribute__((always_inline)) inline int range(const DenseLaunch& l, int xcd) {
+    return int(int64_t(l.tiles) * l.splits * xcd / 8);
+  }
 
+  // Runs items `item`, next(item), ... below `end`; returns the first that is not.
+  template <typename NEXT>
+  static __device__ __attribute__((always_inline)) inline int run(const DenseLaunch& l, uint8_t* lds, int item, int end,
+                                                                  NEXT next) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int wm = w % WM, wn = w / WM;
@@ -362,8 +363,9 @@ struct TileKernel {
     fill(1, 1);
 
     for (;;) {
-      const bool last = item + stride >= end;
-      Place nxt = last ? cur : place(l, item + stride);
+      item = next(item);
+      const bool last = item >= end;
+      Place nxt = last ? cur : place(l, item);
       if (last) nxt.count = 0;
 #pragma unroll
       for (int x = 0; x < 4; ++x)
@@ -381,9 +383,9 @@ struct TileKernel {
       finish(l, cur, acc, wm, wn, lane);
       if (last) break;
       cur = nxt;
-      item += stride;
     }
     __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the end
+    return item;
   }
 
   static __device__ __attribute__((always_inline)) inline void finish(const DenseLaunch& l, const Place& o,
@@ -481,18 +483,67 @@ struct TileKernel {
 };
 
 template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_dense_tile(DenseLaunch l) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_dense_tile(DenseLaunch l) {
   typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[K::kLds];
-  K::run(l, lds);
+  if (l.clear && blockIdx.x == 0 && threadIdx.x < kDenseQueue) gstore<uint32_t>(l.clear + threadIdx.x, 0u);
+  // a workgroup takes every (grid / 8)th item of its XCD's range
+  const int xcd = int(blockIdx.x) & 7, stride = int(gridDim.x) >> 3;
+  const int item = K::range(l, xcd) + (int(blockIdx.x) >> 3), end = K::range(l, xcd + 1);
+  if (item < end) K::run(l, lds, item, end, [&](int at) { return at + stride; });
+}
+
+template <typename D, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_dense_pair(DensePair l) {
+  typedef typename D::elem E;
+  typedef TileKernel<D, kDenseOuter, E, TM, TN, WM, WN> O;
+  typedef TileKernel<D, kDenseCols, E, TM, TN, WM, WN> C;
+  static_assert(O::kLds == C::kLds, "one LDS layout");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[O::kLds];
+  __shared__ int taken;
+  // items of this XCD: the weight gradients' tiles, then dx's
+  const int xcd = int(blockIdx.x) & 7, o0 = O::range(l.outer, xcd), no = O::range(l.outer, xcd + 1) - o0;
+  const int c0 = C::range(l.cols, xcd), nc = C::range(l.cols, xcd + 1) - c0;
+  const int first = int(gridDim.x) >> 3;  // the items that workgroups start with
+  auto next = [&](int) {
+    __syncthreads();  // everyone has read the one before
+    if (threadIdx.x == 0) taken = first + int(atomicAdd(l.queue + xcd, 1u));
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(taken);
+  };
+  int item = int(blockIdx.x) >> 3;
+  if (item < no) item = O::run(l.outer, lds, o0 + item, o0 + no, [&](int at) { return o0 + next(at); }) - o0;
+  if (item < no + nc) {
+    __syncthreads();  // the weight gradients' LDS reads are over
+    C::run(l.cols, lds, c0 + item - no, c0 + nc, [&](int at) { return c0 - no + next(at); });
+  }
+}
+
+template <int FORM, int TM, int TN>
+int64_t count_tiles(const DenseLaunch& l) {
+  constexpr int NOUT = dense_two_b(FORM) ? TN / 2 : TN;
+  int64_t tiles = 0;
+  for (int i = 0; i < l.count; ++i) tiles += int64_t((l.p[i].m + TM - 1) / TM) * ((l.p[i].n + NOUT - 1) / NOUT);
+  return tiles;
+}
+
+template <typename D, int TM, int TN, int WM, int WN>
+hipError_t launch_pair(DensePair l, hipStream_t s) {
+  const int64_t to = count_tiles<kDenseOuter, TM, TN>(l.outer), tc = count_tiles<kDenseCols, TM, TN>(l.cols);
+  if (to + tc > (1 << 30) || l.outer.splits != 1 || l.cols.splits != 1) return hipErrorInvalidValue;
+  l.outer.tiles = int32_t(to);
+  l.cols.tiles = int32_t(tc);
+  // each XCD's range is rounded, so the most of one is a tile more than its share
+  const int64_t most = 256 * (TM >= 256 ? 1 : 2);
+  const uint32_t grid = uint32_t(std::min(most, ((to + 7) / 8 + (tc + 7) / 8) * 8));
+  hipLaunchKernelGGL((k_dense_pair<D, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
+  return hipGetLastError();
 }
 
 template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
 hipError_t launch_tile(DenseLaunch l, hipStream_t s) {
   typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
-  int64_t tiles = 0;
-  for (int i = 0; i < l.count; ++i)
-    tiles += int64_t((l.p[i].m + TM - 1) / TM) * ((l.p[i].n + K::NOUT - 1) / K::NOUT);
+  const int64_t tiles = count_tiles<FORM, TM, TN>(l);
   if (tiles == 0) return hipSuccess;
   if (tiles * l.splits > (1 << 30)) return hipErrorInvalidValue;
   l.tiles = int32_t(tiles);
