@@ -534,7 +534,7 @@ hipError_t launch_pair(DensePair l, hipStream_t s) {
   l.outer.tiles = int32_t(to);
   l.cols.tiles = int32_t(tc);
   // each XCD's range is rounded, so the most of one is a tile more than its share
-  const int64_t most = 256 * (TM >= 256 ? 1 : 2);
+  const int64_t most = 256 * (TM + TN > 256 ? 1 : 2);
   const uint32_t grid = uint32_t(std::min(most, ((to + 7) / 8 + (tc + 7) / 8) * 8));
   hipLaunchKernelGGL((k_dense_pair<D, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
   return hipGetLastError();
