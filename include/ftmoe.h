@@ -426,10 +426,11 @@ int ft_moe_debug_read(ft_moe_pool *p, int32_t what, void *dst, int64_t bytes);
  *
  * Weights are [out][in] row-major as in an expert blob.  A leading dimension
  * (ld_*) is the distance between two rows in elements; 0 means rows follow
- * each other (the width itself).  Any size and stride is taken; operands
- * whose base addresses and row strides are multiples of 16 bytes (and whose
- * widths along K are whole 16-byte pieces) run the fast kernels, others a
- * general one several times slower.
+ * each other (the width itself).  Any size and stride is taken.  Operands
+ * with rows of whole 16-byte pieces at 16-byte distances are read where they
+ * lie; others (weights too) are copied into `work` at each call first.  A base
+ * address that is no multiple of 16 bytes, where a copy is not needed
+ * otherwise, runs a general kernel several times slower.
  *
  * Every call enqueues its work on `hip_stream` (NULL = the null stream of the
  * current device) and returns; nothing is read after that on the host and

@@ -176,22 +176,60 @@ int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems,
   return FT_OK;
 }
 
+// A call's operands that the tiled kernels cannot take as they lie, copied into
+// scratch memory.  Whether one is copied depends on sizes and row distances
+// only (the scratch memory is sized before addresses are known); a base
+// address off the 16-byte grid leaves its product to the general kernel.
+struct Packs {
+  DensePackLaunch l{};
+  Carve* c;
+  bool odd(int64_t width, int64_t ld, int64_t es) const { return width * es % 16 || ld * es % 16; }
+  // a matrix: where it then lies, and its rows' distance; one that the call does not read keeps its place only
+  const void* matrix(const void* src, int64_t rows, int64_t width, int64_t& ld, int64_t es, bool& whole, bool read = true) {
+    whole = false;
+    if (!odd(width, ld, es)) return src;
+    const int64_t to = up(width * es, 128);
+    uint8_t* dst = c->take(rows * to);
+    add({u8(src), dst, ld * es, to, width * es, to, read ? rows : 0});
+    ld = to / es;
+    whole = true;
+    return dst;
+  }
+  // zeros behind the rows of a matrix of the call's own, up to a whole piece; whether there are any.  The piece that
+  // the rows end in is cleared before its values are written.
+  bool behind(uint8_t* base, int64_t rows, int64_t width, int64_t ld, int64_t es) {
+    if (width * es % 16 == 0) return false;
+    const int64_t from = width * es / 16 * 16;
+    add({nullptr, base + from, 0, ld * es, 0, 16, rows});
+    return true;
+  }
+  void add(const DensePack& p) { l.p[l.count++] = p; }
+};
+
 // ------------------------------------------------------------ gated block
 struct FfnWork {
   int64_t ldi;  // elements between rows of h, and half of a row of dgu
   uint8_t *h, *dgu, *part;
   uint32_t* queue;
+  // the operands as the products take them
+  const void *x, *dy, *wg, *wu, *wd;
+  int64_t ld_x, ld_y, ld_in, ld_out;
+  bool whole_x, whole_y, whole_in, whole_out, whole_i;
+  DensePackLaunch packs;
   int64_t bytes;
 };
-FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
+// read_x, read_in: whether the call reads x, and w_gate and w_up
+FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base, const void* x = nullptr, const void* dy = nullptr,
+                 const void* wg = nullptr, const void* wu = nullptr, const void* wd = nullptr, bool read_x = true,
+                 bool read_in = true) {
   FfnWork w{};
   Carve c{static_cast<uint8_t*>(base)};
-  w.ldi = up(d.inter, 64);
-  w.h = c.take(int64_t(d.tokens) * w.ldi * 2);
   const int T = d.tokens, H = d.hidden, I = d.inter;
+  w.ldi = up(I, 64);
+  w.h = c.take(int64_t(T) * w.ldi * 2);
   int64_t part;
   if (backward) {
-    w.dgu = c.take(int64_t(d.tokens) * w.ldi * 4);
+    w.dgu = c.take(int64_t(T) * w.ldi * 4);
     w.queue = reinterpret_cast<uint32_t*>(c.take(kDenseQueue * 4));
     part = std::max({parts_bytes(kDenseGrad, {{T, I, H, 1}}), parts_bytes(kDenseCols, {{T, H, I, 2}}),
                      parts_bytes(kDenseOuter, {{I, H, T, 1}, {I, H, T, 1}, {H, I, T, 1}})});
@@ -199,6 +237,26 @@ FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base) {
     part = std::max(parts_bytes(kDenseGated, {{T, I, H, 1}}), parts_bytes(kDenseRows, {{T, H, I, 1}}));
   }
   w.part = c.take(part);
+  Packs k;
+  k.c = &c;
+  w.ld_x = d.ld_x;
+  w.ld_y = d.ld_y;
+  w.ld_in = d.ld_w_in;
+  w.ld_out = d.ld_w_out;
+  if (T > 0) {
+    int64_t ld_up = d.ld_w_in;
+    w.x = k.matrix(x, T, H, w.ld_x, 2, w.whole_x, read_x);
+    w.wg = k.matrix(wg, I, H, w.ld_in, 2, w.whole_in, read_in);
+    w.wu = k.matrix(wu, I, H, ld_up, 2, w.whole_in, read_in);
+    w.wd = k.matrix(wd, H, I, w.ld_out, 2, w.whole_out);
+    if (backward) w.dy = k.matrix(dy, T, H, w.ld_y, 2, w.whole_y);
+    w.whole_i = k.behind(w.h, T, I, w.ldi, 2);
+    if (backward) {
+      k.behind(w.dgu, T, I, 2 * w.ldi, 2);
+      k.behind(w.dgu + 2 * w.ldi, T, I, 2 * w.ldi, 2);
+    }
+  }
+  w.packs = k.l;
   w.bytes = c.used;
   return w;
 }
@@ -229,15 +287,20 @@ struct IntWork {
   int8_t *xq, *hq;
   float *xs, *hs, *h;
   uint8_t* part;
+  const void *wg, *wu, *wd;
+  int64_t ld_in, ld_out;
+  bool whole_x, whole_h, whole_in, whole_out;
+  DensePackLaunch packs;
   int64_t bytes;
 };
-IntWork int_work(const ft_moe_gated_ffn& d, void* base) {
+IntWork int_work(const ft_moe_gated_ffn& d, void* base, const void* wg = nullptr, const void* wu = nullptr,
+                 const void* wd = nullptr) {
   IntWork w{};
   Carve c{static_cast<uint8_t*>(base)};
-  const int64_t T = d.tokens;
-  w.ldx = up(d.hidden, 128);
-  w.ldh = up(d.inter, 128);
-  w.ldf = up(d.inter, 32);
+  const int64_t T = d.tokens, H = d.hidden, I = d.inter;
+  w.ldx = up(H, 128);
+  w.ldh = up(I, 128);
+  w.ldf = up(I, 32);
   w.xq = reinterpret_cast<int8_t*>(c.take(T * w.ldx));
   w.xs = reinterpret_cast<float*>(c.take(T * 4));
   w.h = reinterpret_cast<float*>(c.take(T * w.ldf * 4));
@@ -245,6 +308,44 @@ IntWork int_work(const ft_moe_gated_ffn& d, void* base) {
   w.hs = reinterpret_cast<float*>(c.take(T * 4));
   w.part = c.take(std::max(parts_bytes(kDenseIntGated, {{d.tokens, d.inter, d.hidden, 1}}),
                            parts_bytes(kDenseInt, {{d.tokens, d.hidden, d.inter, 1}})));
+  Packs k;
+  k.c = &c;
+  w.ld_in = d.ld_w_in;
+  w.ld_out = d.ld_w_out;
+  if (T > 0) {
+    int64_t ld_up = d.ld_w_in;
+    w.wg = k.matrix(wg, I, H, w.ld_in, 1, w.whole_in);
+    w.wu = k.matrix(wu, I, H, ld_up, 1, w.whole_in);
+    w.wd = k.matrix(wd, H, I, w.ld_out, 1, w.whole_out);
+    w.whole_x = k.behind(reinterpret_cast<uint8_t*>(w.xq), T, H, w.ldx, 1);
+    w.whole_h = k.behind(reinterpret_cast<uint8_t*>(w.hq), T, I, w.ldh, 1);
+  }
+  w.packs = k.l;
+  w.bytes = c.used;
+  return w;
+}
+// the product alone: its operands as it takes them
+struct ProductWork {
+  const void *x, *w;
+  int64_t ld_x, ld_w;
+  bool whole_x, whole_w;
+  uint8_t* part;
+  DensePackLaunch packs;
+  int64_t bytes;
+};
+ProductWork product_work(const ft_moe_int_product& d, void* base, const void* x = nullptr, const void* wt = nullptr) {
+  ProductWork w{};
+  Carve c{static_cast<uint8_t*>(base)};
+  w.part = c.take(parts_bytes(kDenseInt, {{d.tokens, d.out, d.in, 1}}));
+  Packs k;
+  k.c = &c;
+  w.ld_x = d.ld_x;
+  w.ld_w = d.ld_w;
+  if (d.tokens > 0) {
+    w.x = k.matrix(x, d.tokens, d.in, w.ld_x, 1, w.whole_x);
+    w.w = k.matrix(wt, d.out, d.in, w.ld_w, 1, w.whole_w);
+  }
+  w.packs = k.l;
   w.bytes = c.used;
   return w;
 }
@@ -286,7 +387,7 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
     ft_moe_gated_ffn d;
     if (const int rc = check_ffn(desc, d)) return rc;
     if (d.tokens == 0) return FT_OK;
-    const FfnWork w = ffn_work(d, false, work);
+    const FfnWork w = ffn_work(d, false, work, x, nullptr, w_gate, w_up, w_down);
     if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
     if (same(y, {x, w_gate, w_up, w_down, gu, work}) || same(gu, {x, w_gate, w_up, w_down, work}))
       return bad("an output is also another argument");
@@ -296,13 +397,18 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
                                    {y, 2, "y"}, {gu ? gu : y, 2, "gu"}, {work, 16, "work"}}))
       return rc;
 
-    DenseProblem p = product(x, d.ld_x, w_gate, d.ld_w_in, d.tokens, d.inter, d.hidden, w.h, w.ldi, 2);
-    p.b[1] = u8(w_up);
+    FT_HIP_CHECK(launch_dense_pack(w.packs, s));
+    DenseProblem p = product(w.x, w.ld_x, w.wg, w.ld_in, d.tokens, d.inter, d.hidden, w.h, w.ldi, 2);
+    p.b[1] = u8(w.wu);
+    p.a_whole = w.whole_x;
+    p.b_whole = w.whole_in;
     p.gu = u8(gu);
     p.ldgu = d.ld_gu;
     p.off_u = d.inter;
     if (const int rc = run(kDenseGated, d.dtype, {p}, w.part, s)) return rc;
-    p = product(w.h, w.ldi, w_down, d.ld_w_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2);
+    p = product(w.h, w.ldi, w.wd, w.ld_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2);
+    p.a_whole = w.whole_i;
+    p.b_whole = w.whole_out;
     return run(kDenseRows, d.dtype, {p}, w.part, s);
   });
 }
@@ -316,7 +422,7 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
     const bool grads = dw_gate || dw_up || dw_down;
     if (grads && !(dw_gate && dw_up && dw_down)) return bad("weight gradients are given together or not at all");
     if (!grads && (!dx || d.tokens == 0)) return FT_OK;
-    const FfnWork w = ffn_work(d, true, work);
+    const FfnWork w = ffn_work(d, true, work, x, dy, w_gate, w_up, w_down, grads, dx != nullptr);
     if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
     for (const void* o : {(const void*)dx, (const void*)dw_gate, (const void*)dw_up, (const void*)dw_down, (const void*)work})
       if (same(o, {x, w_gate, w_up, w_down, gu, dy})) return bad("an output is also another argument");
@@ -338,18 +444,26 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
     DenseProblem cols{};
     DenseProblem outer[3];
     if (dx) {
-      cols = product(w.dgu, 2 * w.ldi, w_gate, d.ld_w_in, T, H, I, dx, d.ld_x, 2);
+      cols = product(w.dgu, 2 * w.ldi, w.wg, w.ld_in, T, H, I, dx, d.ld_x, 2);
       cols.a[1] = w.dgu + 2 * w.ldi;
-      cols.b[1] = u8(w_up);
+      cols.b[1] = u8(w.wu);
       cols.segs = 2;
+      cols.a_whole = w.whole_i;
+      cols.b_whole = w.whole_in;
     }
     if (grads) {
-      outer[0] = product(w.dgu, 2 * w.ldi, x, d.ld_x, I, H, T, dw_gate, d.ld_w_in, 2);
-      outer[1] = product(w.dgu + 2 * w.ldi, 2 * w.ldi, x, d.ld_x, I, H, T, dw_up, d.ld_w_in, 2);
-      outer[2] = product(dy, d.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2);
+      outer[0] = product(w.dgu, 2 * w.ldi, w.x, w.ld_x, I, H, T, dw_gate, d.ld_w_in, 2);
+      outer[1] = product(w.dgu + 2 * w.ldi, 2 * w.ldi, w.x, w.ld_x, I, H, T, dw_up, d.ld_w_in, 2);
+      outer[2] = product(w.dy, w.ld_y, w.h, w.ldi, H, I, T, dw_down, d.ld_w_out, 2);
+      outer[0].a_whole = outer[1].a_whole = outer[2].b_whole = w.whole_i;
+      outer[0].b_whole = outer[1].b_whole = w.whole_x;
+      outer[2].a_whole = w.whole_y;
     }
     if (T > 0) {
-      DenseProblem p = product(dy, d.ld_y, w_down, d.ld_w_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2);
+      FT_HIP_CHECK(launch_dense_pack(w.packs, s));
+      DenseProblem p = product(w.dy, w.ld_y, w.wd, w.ld_out, T, I, H, grads ? w.h : nullptr, w.ldi, 2);
+      p.a_whole = w.whole_y;
+      p.b_whole = w.whole_out;
       p.gu = const_cast<uint8_t*>(u8(gu));
       p.ldgu = d.ld_gu;
       p.off_u = I;
@@ -407,7 +521,7 @@ int ft_moe_int_matmul_work(const ft_moe_int_product* d, int64_t* bytes) {
     ft_moe_int_product o;
     if (const int rc = check_product(d, o)) return rc;
     if (!bytes) return bad("bytes is NULL");
-    *bytes = parts_bytes(kDenseInt, {{o.tokens, o.out, o.in, 1}});
+    *bytes = product_work(o, nullptr).bytes;
     return FT_OK;
   });
 }
@@ -418,7 +532,8 @@ int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const flo
     ft_moe_int_product d;
     if (const int rc = check_product(desc, d)) return rc;
     if (d.tokens == 0) return FT_OK;
-    const int64_t need = parts_bytes(kDenseInt, {{d.tokens, d.out, d.in, 1}});
+    const ProductWork k = product_work(d, work, x, w);
+    const int64_t need = k.bytes;
     if (const int rc = check_work(work, work_bytes, need)) return rc;
     if (same(y, {x, x_scale, w, w_scale, work})) return bad("an output is also another argument");
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
@@ -427,10 +542,13 @@ int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const flo
     if (const int rc = g.enter(s, {{x, 1, "x"}, {x_scale, 4, "x_scale"}, {w, 1, "w"}, {w_scale, 4, "w_scale"}, {y, es, "y"},
                                    {need ? work : y, need ? 16 : es, "work"}}))
       return rc;
-    DenseProblem p = product(x, d.ld_x, w, d.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1);
+    FT_HIP_CHECK(launch_dense_pack(k.packs, s));
+    DenseProblem p = product(k.x, k.ld_x, k.w, k.ld_w, d.tokens, d.out, d.in, y, d.ld_y, 1);
+    p.a_whole = k.whole_x;
+    p.b_whole = k.whole_w;
     p.xs = x_scale;
     p.ws[0] = p.ws[1] = w_scale;
-    return run(kDenseInt, d.out_dtype, {p}, u8(work), s);
+    return run(kDenseInt, d.out_dtype, {p}, k.part, s);
   });
 }
 
@@ -451,7 +569,7 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
     ft_moe_gated_ffn d;
     if (const int rc = check_int_ffn(desc, d)) return rc;
     if (d.tokens == 0) return FT_OK;
-    const IntWork w = int_work(d, work);
+    const IntWork w = int_work(d, work, w_gate, w_up, w_down);
     if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
     if (same(y, {x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale, work}) ||
         same(work, {x, w_gate, gate_scale, w_up, up_scale, w_down, down_scale}))
@@ -463,15 +581,20 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
                                    {y, 2, "y"}, {work, 16, "work"}}))
       return rc;
     const int T = d.tokens, H = d.hidden, I = d.inter;
+    FT_HIP_CHECK(launch_dense_pack(w.packs, s));
     FT_HIP_CHECK(launch_int_quantize(d.dtype, T, H, x, d.ld_x, w.xq, w.ldx, w.xs, s));
-    DenseProblem p = product(w.xq, w.ldx, w_gate, d.ld_w_in, T, I, H, w.h, w.ldf, 1);
-    p.b[1] = u8(w_up);
+    DenseProblem p = product(w.xq, w.ldx, w.wg, w.ld_in, T, I, H, w.h, w.ldf, 1);
+    p.b[1] = u8(w.wu);
+    p.a_whole = w.whole_x;
+    p.b_whole = w.whole_in;
     p.xs = w.xs;
     p.ws[0] = gate_scale;
     p.ws[1] = up_scale;
     if (const int rc = run(kDenseIntGated, FT_DT_F32, {p}, w.part, s)) return rc;
     FT_HIP_CHECK(launch_int_quantize(FT_DT_F32, T, I, w.h, w.ldf, w.hq, w.ldh, w.hs, s));
-    p = product(w.hq, w.ldh, w_down, d.ld_w_out, T, H, I, y, d.ld_y, 1);
+    p = product(w.hq, w.ldh, w.wd, w.ld_out, T, H, I, y, d.ld_y, 1);
+    p.a_whole = w.whole_h;
+    p.b_whole = w.whole_out;
     p.xs = w.hs;
     p.ws[0] = p.ws[1] = down_scale;
     return run(kDenseInt, d.dtype, {p}, w.part, s);

@@ -50,6 +50,7 @@ struct DenseProblem {
   int64_t lddgu, off_du;
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
+  bool a_whole, b_whole; // this operand's rows are zeros up to a whole 16-byte piece
   uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };
 constexpr int kDenseMaxProblems = 3;
@@ -104,6 +105,21 @@ hipError_t launch_dense_tile_int(DenseForm form, int dtype, int tile, const Dens
 // dense_few.hip: tileable products of up to kDenseFewRows tokens, both operands along K
 constexpr int kDenseFewRows = 64;
 hipError_t launch_dense_few(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s);
+
+// dense_pack.hip: rows of `bytes` bytes copied to dst rows of dst_bytes (a
+// multiple of 16, at 16-byte addresses), zeros behind them; src is not read when bytes is 0
+struct DensePack {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t src_ld, dst_ld, bytes, dst_bytes, rows;
+  int32_t lanes;  // set by the launch
+};
+constexpr int kDenseMaxPacks = 8;  // a backward pass: x, dy, three weights, h, dg, du
+struct DensePackLaunch {
+  DensePack p[kDenseMaxPacks];
+  int32_t count;
+};
+hipError_t launch_dense_pack(const DensePackLaunch& l, hipStream_t s);
 
 // int_quant.hip: rows of x (FT_DT_*) to 8-bit codes and scales
 hipError_t launch_int_quantize(int dtype, int32_t rows, int32_t cols, const void* x, int64_t ld_x, int8_t* codes,

@@ -13,15 +13,15 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 
-// The tiled kernels load whole 16-byte pieces and hold a unit's offsets in 31
-// bits: 128 rows of an operand along K, 64 (8 bit: 128) of one across it.
+// The tiled kernels load whole 16-byte pieces (a piece that K or the columns
+// end in has to be there, with zeros) and hold a unit's offsets in 31 bits: 128
+// rows of an operand along K, 64 (8 bit: 128) of one across it.
 bool dense_tileable(DenseForm form, const DenseProblem& p) {
   const int64_t es = dense_elem(form);
   if (!on16(p.a[0]) || !on16(p.a[1]) || !on16(p.b[0]) || !on16(p.b[1]) || p.lda % 16 || p.ldb % 16) return false;
   if (p.lda >= (1 << 23) || p.ldb >= (1 << 23)) return false;
-  if ((dense_a_rows(form) || dense_b_rows(form)) && int64_t(p.k) * es % 16) return false;
-  if (!dense_a_rows(form) && int64_t(p.m) * es % 16) return false;
-  if (!dense_b_rows(form) && int64_t(p.n) * es % 16) return false;
+  if ((dense_a_rows(form) ? p.k : p.m) * es % 16 && !p.a_whole) return false;
+  if ((dense_b_rows(form) ? p.k : p.n) * es % 16 && !p.b_whole) return false;
   return true;
 }
 

@@ -133,3 +133,19 @@ def test_struct_layouts():
         assert c[(n, "size")] == ctypes.sizeof(t), n
         for f, _ in t._fields_:
             assert c[(n, f)] == getattr(t, f).offset, (n, f)
+
+
+@pytest.mark.parametrize("hidden,inter", [(17, 19), (2721, 1043), (16, 19), (17, 16), (1, 1)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_scratch_memory_holds_copies_of_rows_that_are_no_whole_pieces(hidden, inter, backward):
+    """Rows that are not multiples of 16 bytes are copied to rows that are: the scratch memory has room for them."""
+    for tokens in (1, 33, 500):
+        odd = ft.ft_moe_gated_ffn_work(_ffn(tokens=tokens, hidden=hidden, inter=inter), backward)
+        up = lambda v: -(-v // 64) * 64
+        h, i = up(hidden), up(inter)
+        own = tokens * i * 2 * (3 if backward else 1)
+        copies = (tokens * h * (2 if backward else 1) + 2 * inter * h) * 2 if hidden % 8 else 0
+        copies += hidden * i * 2 if inter % 8 else 0
+        assert odd >= own + copies
+        assert ft.ft_moe_int_gated_ffn_work(_ffn(tokens=tokens, hidden=hidden, inter=inter)) >= tokens * (hidden + 5 * inter)
+    assert ft.ft_moe_gated_ffn_work(_ffn(tokens=0, hidden=hidden, inter=inter), backward) >= 0
