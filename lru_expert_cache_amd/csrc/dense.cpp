@@ -176,6 +176,26 @@ int run(DenseForm form, int dtype, std::initializer_list<DenseProblem> problems,
   return FT_OK;
 }
 
+// An 8-bit product whose tokens lie at x (ld_x elements of type dtype apart)
+// and are quantised to p's a and xs: by the product itself where it can, in a
+// launch of its own otherwise.
+int run_quantized(DenseForm form, int out_dtype, DenseProblem p, int dtype, const void* x, int64_t ld_x, uint8_t* part,
+                  hipStream_t s) {
+  if (dense_few_quantizes(p.m, p.k) && dense_tileable(form, p)) {
+    p.a[0] = p.a[1] = u8(x);
+    p.lda = ld_x * (dtype == FT_DT_F32 ? 4 : 2);
+    p.tokens = dtype;
+    DenseLaunch l{};
+    l.p[0] = p;
+    l.count = l.splits = 1;
+    FT_HIP_CHECK(launch_dense_few(form, out_dtype, l, s));
+    return FT_OK;
+  }
+  FT_HIP_CHECK(launch_int_quantize(dtype, p.m, p.k, x, ld_x, const_cast<int8_t*>(reinterpret_cast<const int8_t*>(p.a[0])),
+                                   p.lda, const_cast<float*>(p.xs), s));
+  return run(form, out_dtype, {p}, part, s);
+}
+
 // A call's operands that the tiled kernels cannot take as they lie, copied into
 // scratch memory.  Whether one is copied depends on sizes and row distances
 // only (the scratch memory is sized before addresses are known); a base
@@ -582,7 +602,6 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
       return rc;
     const int T = d.tokens, H = d.hidden, I = d.inter;
     FT_HIP_CHECK(launch_dense_pack(w.packs, s));
-    FT_HIP_CHECK(launch_int_quantize(d.dtype, T, H, x, d.ld_x, w.xq, w.ldx, w.xs, s));
     DenseProblem p = product(w.xq, w.ldx, w.wg, w.ld_in, T, I, H, w.h, w.ldf, 1);
     p.b[1] = u8(w.wu);
     p.a_whole = w.whole_x;
@@ -590,14 +609,13 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn* desc, const void* x, const int8
     p.xs = w.xs;
     p.ws[0] = gate_scale;
     p.ws[1] = up_scale;
-    if (const int rc = run(kDenseIntGated, FT_DT_F32, {p}, w.part, s)) return rc;
-    FT_HIP_CHECK(launch_int_quantize(FT_DT_F32, T, I, w.h, w.ldf, w.hq, w.ldh, w.hs, s));
+    if (const int rc = run_quantized(kDenseIntGated, FT_DT_F32, p, d.dtype, x, d.ld_x, w.part, s)) return rc;
     p = product(w.hq, w.ldh, w.wd, w.ld_out, T, H, I, y, d.ld_y, 1);
     p.a_whole = w.whole_h;
     p.b_whole = w.whole_out;
     p.xs = w.hs;
     p.ws[0] = p.ws[1] = down_scale;
-    return run(kDenseInt, d.dtype, {p}, w.part, s);
+    return run_quantized(kDenseInt, d.dtype, p, FT_DT_F32, w.h, w.ldf, w.part, s);
   });
 }
 

@@ -50,6 +50,7 @@ struct DenseProblem {
   int64_t lddgu, off_du;
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
+  int32_t tokens;        // 8-bit forms, few tokens: a's type (FT_DT_*) where it is yet to be quantised
   bool a_whole, b_whole; // this operand's rows are zeros up to a whole 16-byte piece
   uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };
@@ -104,6 +105,8 @@ hipError_t launch_dense_tile_int(DenseForm form, int dtype, int tile, const Dens
 
 // dense_few.hip: tileable products of up to kDenseFewRows tokens, both operands along K
 constexpr int kDenseFewRows = 64;
+// 8-bit forms: whether it can quantise m tokens of k elements itself
+bool dense_few_quantizes(int m, int k);
 hipError_t launch_dense_few(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s);
 
 // dense_pack.hip: rows of `bytes` bytes copied to dst rows of dst_bytes (a

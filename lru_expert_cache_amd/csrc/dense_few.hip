@@ -8,8 +8,8 @@
 // lines, with a row's 16-byte pieces permuted so that the fragment reads (lane
 // l: row l % 16, bytes 16 (l / 16) .. of a 64-byte step) meet no bank twice.
 // Two stages are in flight while one is multiplied.  Lanes outside the
-// matrices write zeros, and turns past the end of K are such loads too, so
-// every wave counts the same loads.  The waves' sums meet in LDS and are added
+// matrices write zeros, as a wave's turn past the end of K does, so every wave
+// counts the same loads.  The waves' sums meet in LDS and are added
 // in the order of the waves.  No second launch, no scratch memory.
 //
 // Loading fragments straight into registers instead touches 16 lines per
@@ -21,29 +21,106 @@
 // workgroups then fit the CUs in one round, else 2, which reads the tokens
 // half as often: N 6144, K 2048, 16 tokens 6.8 us against 10.0; N 2048 (gated),
 // K 6144 10.3 against 9.7.
+//
+// 8-bit forms quantise up to 16 tokens themselves while the codes fit 16 KB:
+// every workgroup reads all the tokens and forms the same codes, which saves a
+// launch.  The whole 8-bit block, H 2048, I 768, one token: 9.6 us, with launches
+// of their own 14.9; H 7168, I 2048, one token 13.9 and 17.2, 8 tokens 17.2 and
+// 17.8.  With 32 KB of codes 16 tokens of the latter took 19.3 us against 18.0.
 #include "dense_tile.h"
+#include "int_quant.h"
 
 namespace ftmoe {
 
 namespace {
 
+// Tokens that the kernel quantises itself (TX: their type): R of them (a power
+// of two up to 16), their codes in LDS as R rows of 128 bytes a unit.  A row
+// belongs to 512 / R threads, which keep kTokenPieces pieces of it each.
+constexpr int kTokenCodes = 16384;  // bytes, see above
+template <typename TX>
+constexpr int kTokenPieces = kTokenCodes / 512 / RowPiece<TX>::N;
+
+template <typename TX>
+struct TokenCodes {
+  int shift;  // log2 R
+  __device__ __attribute__((always_inline)) inline explicit TokenCodes(int m) : shift(m > 1 ? 32 - __clz(m - 1) : 0) {}
+  // the codes of unit u's row r, 16 bytes at piece c of its 128
+  __device__ __attribute__((always_inline)) inline uint32_t at(int u, int r, int c) const {
+    return uint32_t(((u << shift) + r) * kTileKB + ((c ^ ((r >> 1) & 7)) * 16));
+  }
+  // meanwhile() runs once the tokens are there
+  template <typename F>
+  __device__ __attribute__((always_inline)) inline void fill(const DenseProblem& p, uint8_t* codes, uint32_t* top,
+                                                             float* scale, F meanwhile) const {
+    constexpr int N = RowPiece<TX>::N, G = kTokenPieces<TX>;
+    const int tid = threadIdx.x, per = 512 >> shift, r = tid >> (9 - shift), j = tid & (per - 1);
+    const int pieces = (p.k + kTileKB - 1) / kTileKB * kTileKB / N;
+    RowPiece<TX> v[G], end;
+    RowMax<TX> most;
+    // rows past the last token stay zeros
+    const int cols = r < p.m ? p.k : 0, whole = p.k / N;
+    const TX* x = reinterpret_cast<const TX*>(p.a[0] + min(r, p.m - 1) * p.lda);
+    const bool last = whole * N < cols && j == 0;  // has the piece that the row ends in
+#pragma unroll
+    for (int g = 0; g < G; ++g) v[g].load(x, (j + g * per) * N, cols);
+    if (last) {
+      end.load_last(x, cols);
+      most.add(end);
+    }
+    if (tid < 16) top[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < G; ++g) most.add(v[g]);
+    uint32_t mx = most.bits();
+    asm volatile("" : "+v"(mx)::"memory");
+    meanwhile();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = max(mx, uint32_t(__shfl_xor(int(mx), o)));
+    if ((tid & 31) == 0) atomicMax(top + r, mx);  // the largest, whatever the order
+    __syncthreads();
+    const RowScale q(top[r]);
+    if (j == 0) scale[r] = q.scale;
+    auto put = [&](int c, const RowPiece<TX>& t) {
+      const int e = c * N;
+      uint32_t b[N / 4];
+      q.codes(t, b);
+      uint32_t* to = reinterpret_cast<uint32_t*>(codes + at(e / kTileKB, r, e % kTileKB / 16) + e % 16);
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) to[i] = b[i];
+    };
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int c = j + g * per;
+      if (c < pieces && (c != whole || whole * N == cols)) put(c, v[g]);
+    }
+    if (last) put(whole, end);
+    __syncthreads();
+  }
+};
+
 // FT: weight fragments of 16 rows (a gated form: both matrices together); XI:
-// load instructions of 8 tokens
-template <typename D, int FORM, typename TO, int FT, int XI, int kWaves>
+// load instructions of 8 tokens, 0: the tokens have type TX and are quantised here
+template <typename D, int FORM, typename TO, int FT, int XI, int kWaves, typename TX = int8_t>
 __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
   typedef typename D::elem E;
   typedef typename D::acc4 Acc;
   typedef typename D::sum Sum;
   constexpr bool TWO = dense_two_b(FORM);
   constexpr int F = FT * (TWO ? 8 : 16);     // output columns
-  constexpr int MT = (XI + 1) / 2;           // token fragments of 16
-  constexpr int S = 3;                       // LDS stages of a wave
+  constexpr bool QUANT = XI == 0;
+  static_assert(!QUANT || kWaves == 8, "512 threads share the tokens");
+  constexpr int MT = QUANT ? 1 : (XI + 1) / 2;  // token fragments of 16
+  constexpr int S = QUANT && FT == 1 ? 6 : 3;   // LDS stages of a wave
   constexpr int kLoads = 2 * FT + XI;        // per stage
-  constexpr int kStage = (FT + MT) * 2048;
+  constexpr int kStage = (FT + (QUANT ? 0 : MT)) * 2048;
   constexpr int kLd = FT * 16 + 4;           // sums of a token, padded
   constexpr int kSums = kWaves * MT * 16 * kLd * 4;
   constexpr int kLds = kWaves * S * kStage > kSums ? kWaves * S * kStage : kSums;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t codes[QUANT ? kTokenCodes : 16];
+  __shared__ uint32_t top[16];
+  __shared__ float scale[16];
 
   const DenseProblem& p = l.p[0];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -76,10 +153,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
       tile_load16(buf, dst + q * 1024, piece * 16 < left ? uint32_t(row0 + r8) * uint32_t(ld) + piece * 16 : kOutside);
     }
   };
-  auto wait = [&]() {  // this round's loads have landed, the round before has been read
+  auto wait = [&](int round) {  // this round's loads have landed, the round before has been read
     asm volatile("" ::: "memory");
     constexpr int n = (S - 2) * kLoads;
-    __builtin_amdgcn_s_waitcnt((n & 0xF) | (n >> 4 << 14) | 0x70);
+    if (round + S - 1 <= rounds)
+      __builtin_amdgcn_s_waitcnt((n & 0xF) | (n >> 4 << 14) | 0x70);
+    else
+      __builtin_amdgcn_s_waitcnt(0x0070);
     asm volatile("" ::: "memory");
   };
 
@@ -91,19 +171,36 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
   uint32_t at[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) at[s] = base + (lane & 15) * kTileKB + (((4 * s + (lane >> 4)) ^ ((lane >> 1) & 7)) * 16);
+  constexpr int kGroups = F / 4;  // of columns; a thread ends with group threadIdx.x % kGroups
+  DenseScales<4> ws;
+  if constexpr (dense_int(FORM)) ws.template fetch<TWO>(p, n0 + int(threadIdx.x) % kGroups * 4);
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(s, s);
+  for (int s = 0; s < 2; ++s)
+    if (s < rounds) issue(s, s);
+  const TokenCodes<TX> tokens(p.m);
+  if constexpr (QUANT)  // the tokens' loads wait for all before them, so not all weights' are before them
+    tokens.fill(p, codes, top, scale, [&]() {
+#pragma unroll
+      for (int s = 2; s < S - 1; ++s)
+        if (s < rounds) issue(s, s);
+    });
+  const uint32_t codes0 = uint32_t(uintptr_t((FT_L3 uint8_t*)codes));
   int stage = 0, fill = S - 1;
   for (int i = 0; i < rounds; ++i) {
-    wait();
-    issue(i + S - 1, fill);
+    wait(i);
+    if (i + S - 1 < rounds) issue(i + S - 1, fill);
     u32x4 fw[FT][2], fx[MT][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int f = 0; f < FT; ++f) fw[f][s] = *(FT_L3 const u32x4*)(at[s] + stage * kStage + f * 2048);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) fx[t][s] = *(FT_L3 const u32x4*)(at[s] + stage * kStage + (FT + t) * 2048);
+      for (int t = 0; t < MT; ++t)
+        if constexpr (QUANT)  // past the last unit the weights are zeros
+          fx[t][s] = *(FT_L3 const u32x4*)(codes0 + tokens.at(min(w + i * kWaves, units - 1),
+                                                              (lane & 15) & ((1 << tokens.shift) - 1), 4 * s + (lane >> 4)));
+        else
+          fx[t][s] = *(FT_L3 const u32x4*)(at[s] + stage * kStage + (FT + t) * 2048);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -114,8 +211,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
     stage = stage + 1 == S ? 0 : stage + 1;
     fill = fill + 1 == S ? 0 : fill + 1;
   }
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);  // the loads past the end
   __syncthreads();
   Sum* const part = reinterpret_cast<Sum*>(lds);  // [wave][token][kLd]
 #pragma unroll
@@ -126,7 +221,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
   __syncthreads();
 
   // a thread per token and four columns
-  constexpr int kGroups = F / 4;
   for (int g = threadIdx.x; g < MT * 16 * kGroups; g += 64 * kWaves) {
     const int m = g / kGroups, q = g % kGroups;
     if (m >= p.m) continue;
@@ -144,24 +238,34 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
     Sum s0[4], s1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) s0[i] = v0[i], s1[i] = v1[i];
-    if (cnt > 0) dense_finish<FORM, E, TO>(p, m, n, cnt, s0, s1);
+    if (cnt <= 0) continue;
+    if constexpr (dense_int(FORM))
+      dense_emit<FORM, TO, 4>(p, m, n, cnt, s0, s1, QUANT ? scale[m] : gload<float>(p.xs + m), ws);
+    else
+      dense_finish<FORM, E, TO>(p, m, n, cnt, s0, s1);
   }
 }
 
-template <typename D, int FORM, typename TO, int XI>
+template <typename D, int FORM, typename TO, int XI, typename TX = int8_t>
 hipError_t launch_xi(const DenseLaunch& l, hipStream_t s) {
   constexpr int kWaves = XI <= 2 ? 8 : 4, F = dense_two_b(FORM) ? 8 : 16, kCus = 256;
   const int wgs = (l.p[0].n + F - 1) / F;
   if (wgs <= kCus)
-    hipLaunchKernelGGL((k_dense_few<D, FORM, TO, 1, XI, kWaves>), dim3(wgs), dim3(64 * kWaves), 0, s, l);
+    hipLaunchKernelGGL((k_dense_few<D, FORM, TO, 1, XI, kWaves, TX>), dim3(wgs), dim3(64 * kWaves), 0, s, l);
   else
-    hipLaunchKernelGGL((k_dense_few<D, FORM, TO, 2, XI, kWaves>), dim3((wgs + 1) / 2), dim3(64 * kWaves), 0, s, l);
+    hipLaunchKernelGGL((k_dense_few<D, FORM, TO, 2, XI, kWaves, TX>), dim3((wgs + 1) / 2), dim3(64 * kWaves), 0, s, l);
   return hipGetLastError();
 }
 
 template <typename D, int FORM, typename TO>
 hipError_t launch(const DenseLaunch& l, hipStream_t s) {
   const int m = l.p[0].m;
+  if constexpr (dense_int(FORM)) {
+    // x as the caller has it; h in fp32
+    if (l.p[0].tokens && FORM == kDenseInt) return launch_xi<D, FORM, TO, 0, float>(l, s);
+    if (l.p[0].tokens == FT_DT_F16) return launch_xi<D, FORM, TO, 0, _Float16>(l, s);
+    if (l.p[0].tokens) return launch_xi<D, FORM, TO, 0, __bf16>(l, s);
+  }
   if (m <= 8) return launch_xi<D, FORM, TO, 1>(l, s);
   if (m <= 16) return launch_xi<D, FORM, TO, 2>(l, s);
   if (m <= 32) return launch_xi<D, FORM, TO, 4>(l, s);
@@ -170,8 +274,15 @@ hipError_t launch(const DenseLaunch& l, hipStream_t s) {
 
 }  // namespace
 
+bool dense_few_quantizes(int m, int k) {
+  int rows = 1;
+  while (rows < m) rows *= 2;
+  return m <= 16 && int64_t(rows) * ((k + kTileKB - 1) / kTileKB * kTileKB) <= kTokenCodes;
+}
+
 hipError_t launch_dense_few(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s) {
   if (l.count != 1 || l.p[0].m > kDenseFewRows) return hipErrorInvalidValue;
+  if (l.p[0].tokens && !dense_few_quantizes(l.p[0].m, l.p[0].k)) return hipErrorInvalidValue;
   if (form == kDenseIntGated) return launch<DenseI8, kDenseIntGated, float>(l, s);
   if (form == kDenseInt) {
     if (dtype == FT_DT_F32) return launch<DenseI8, kDenseInt, float>(l, s);

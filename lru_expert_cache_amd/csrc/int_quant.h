@@ -20,16 +20,18 @@ struct RowPiece {
   static constexpr int N = 16 / int(sizeof(E));
   typedef E elems __attribute__((ext_vector_type(N)));
   elems v;
-  // from column c; beyond the row's end, zeros
+  // from column c, whole if it is there, else zeros
   __device__ __attribute__((always_inline)) inline void load(const E* x, int c, int cols) {
     typedef elems __attribute__((aligned(1))) any;
-    const int cnt = cols - c;
-    if (cnt >= N) {
-      v = gload<any>(x + c);
-    } else {
+    v = elems{};
+    if (c + N <= cols) v = gload<any>(x + c);
+  }
+  // the piece that the row ends in, with zeros behind.  One thread's work, and apart
+  // from the above: code for single elements at each piece took longer to fetch than to run.
+  __device__ __attribute__((always_inline)) inline void load_last(const E* x, int cols) {
+    const int c = cols / N * N;
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = i < cnt ? gload<E>(x + c + i) : E(0);
-    }
+    for (int i = 0; i < N; ++i) v[i] = c + i < cols ? gload<E>(x + c + i) : E(0);
   }
 };
 

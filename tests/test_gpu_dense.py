@@ -355,3 +355,91 @@ def test_gradients_of_frozen_or_first_blocks():
     """Nothing asked for is nothing done."""
     f = dc.Ffn(4, 32, 16)
     assert ft.ft_moe_gated_ffn_backward(f.desc, None, f.wg, f.wu, f.wd, f.saved(), f.dy) == ft.FT_OK
+
+
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+@pytest.mark.parametrize("H,I", [(1024, 768), (136, 1000), (2048, 96), (45, 23), (1, 1)])
+def test_int_block_rows_do_not_depend_on_their_number(H, I, type_):
+    """Few tokens are quantised by the products themselves, more by launches of their own: the sums are exact and the
+    codes correctly rounded, so a token's result has the same bits in either."""
+    f, codes, d = _int_block(40, H, I, type_)
+    f.x[1] = 0
+    f.x[2] *= 2.0**-14
+    f.x[5, H // 2] = float("nan")
+    y = _run_int_block(f, codes, d)
+    assert bool(y[5].isnan().all()) and bool((y[1] == 0).all())
+    x = f.x
+    for T in (1, 2, 3, 6, 8, 13, 16):
+        for first in (0, 7):
+            f.T, f.x = T, x[first:first + T]
+            some = ft.make_gated_ffn(f.dt, T, H, I, ld_w_in=d.ld_w_in, ld_w_out=d.ld_w_out)
+            got = _run_int_block(f, codes, some)
+            assert torch.equal(got.view(torch.int16), y[first:first + T].view(torch.int16)), (T, first)
+
+
+@pytest.mark.parametrize("size", [(4096, 2048, 768), (2049, 1024, 2048), (1500, 1000, 1016), (1300, 777, 901), (300, 512, 256)])
+def test_gradients_do_not_depend_on_which_are_asked_for(size):
+    """dx and the weight gradients may share a launch: the same bits as each alone, and again at each call."""
+    f = dc.Ffn(*size, "fp16")
+    gu = f.saved()
+    work = f.work(True)
+    both = f.backward(gu, work=work)
+    dx = f.backward(gu, want_dw=False, work=work)[0]
+    dw = f.backward(gu, want_dx=False, work=work)[1:]
+    assert all(torch.equal(a, b) for a, b in zip((dx, *dw), both))
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(f.backward(gu, work=work), both))
+
+
+def test_gradients_with_the_same_tensor_twice():
+    """x and dy in one buffer, and one matrix for both gates, are inputs like any others."""
+    f = dc.Ffn(37, 45, 45)
+    gu = f.saved()
+    f.dy, f.wu = f.x, f.wg
+    for want in (dict(), dict(want_dw=False), dict(want_dx=False)):
+        got, ref = f.backward(gu, **want), f.backward_reference(gu)
+        if want.get("want_dx", True):
+            dc.check(got[0], ref[0], "dx")
+        if want.get("want_dw", True):
+            for g, r in zip(got[1:], ref[1:]):
+                dc.check(g, r)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with scratch memory of its own, do not disturb each other."""
+    fs = [dc.Ffn(1200, 1024, 512, seed=i) for i in range(2)]
+    gus = [f.saved() for f in fs]
+    want = [(f.forward()[0], *f.backward(gu)) for f, gu in zip(fs, gus)]
+    streams, works = [torch.cuda.Stream() for _ in fs], [(f.work(False), f.work(True)) for f in fs]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for f, gu, s, (w1, w2) in zip(fs, gus, streams, works):
+            o = [torch.empty_like(v) for v in want[0]]
+            torch.cuda.current_stream().synchronize()
+            ft.ft_moe_gated_ffn_forward(f.desc, f.x, f.wg, f.wu, f.wd, o[0], None, w1, s)
+            ft.ft_moe_gated_ffn_backward(f.desc, f.x, f.wg, f.wu, f.wd, gu, f.dy, *o[1:], w2, s)
+            outs.append(o)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert all(torch.equal(a, b) for a, b in zip(o, want[i % 2]))
+
+
+@pytest.mark.parametrize("off", [1, 3])
+def test_addresses_off_the_grid(off):
+    """Base addresses that are no multiples of 16 bytes, alone or with widths that are none either."""
+    for T, H, I in ((3, 64, 48), (70, 64, 48), (70, 61, 43)):
+        f = dc.Ffn(T, H, I)
+        for name in ("x", "wg", "wd", "dy"):
+            g = dc.Ffn(T, H, I)
+            m = getattr(g, name)
+            flat = torch.empty(m.numel() + 16, dtype=m.dtype, device="cuda")
+            moved = flat[off:off + m.numel()].view(m.shape)
+            moved.copy_(m)
+            setattr(g, name, moved)
+            y, gu = g.forward()
+            (ry, rgu) = g.forward_reference()
+            dc.check(y, ry, "y")
+            dc.check(gu, rgu, "gu")
+            for a, r in zip(g.backward(gu), g.backward_reference(gu)):
+                dc.check(a, r, name)
