@@ -30,13 +30,16 @@ int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits) {
   return int64_t(splits) * (dense_two_b(form) ? 2 : 1) * s.m * parts(s.n, 4) * 16;
 }
 
-// Estimated times in microseconds, fitted to sweeps of tiles and parts over 10
-// sizes of each form.  A 256 x 256 workgroup has a CU to itself; a K step takes
-// it longer the more CUs are busy (they share power and the L2s).  128 x 128
-// ones run two to a CU, and read the operands twice as often: slower than 256
-// x 256 once the card is at its power limit (8192^3: 1025 us against 838), but
-// quicker where they fill the CUs better (1531 x 7168 x 2048: 46 against 50;
-// 4096 x 2048 x 768: 18.6 against 26.5).  Cutting K costs a second launch and
+// Estimated times in microseconds, fitted to 39 products and blocks of normal
+// random numbers, each with either tile alone (within 10%; the choice is within
+// 6% of the better tile).  A 256 x 256 workgroup has a CU to itself, 128 x 128
+// ones run two to a CU and read the operands twice as often; a K step takes
+// longer the more of the card's places are taken over the launch, which shares
+// power and the L2s.  So 256 x 256 is quicker where
+// it fills the card (forward of 8192 tokens, H 7168, I 2048: 530 us against
+// 696; 8-bit 4096 x 6144 x 6144 133 against 146), 128 x 128 where it does that
+// better (4096 tokens, H 2048, I 768: 45 against 64; 8-bit 1024 x 6144 x 6144 48
+// against 62).  Cutting K costs a second launch and
 // the parts' way to memory and back (77 x 2048 into 768: 23 us in one part,
 // 11 in eight; 4096 x 768 into 2048: 18.6 in one, 39 in two).
 namespace {
@@ -44,14 +47,16 @@ namespace {
 constexpr int kCus = 256;
 constexpr double kStart = 4.0;
 
+// a tile beside its steps, and a step with few and with all places of the card taken
 struct Pace {
-  double few256, all256, tile256;  // a step of a 256 x 256 tile with few and with all CUs busy; a tile beside its steps
-  double few128, all128, pair128, hot128, tile128;  // 128 x 128 alone on its CU; two; two at the power limit
+  double tile256, few256, all256;
+  double tile128, few128, all128;  // alone on its CU
+  double few2, all2;               // two on a CU, each
 };
 Pace pace(DenseForm form) {
-  return dense_int(form) ? Pace{1.0, 1.35, 9.0, 0.36, 0.6, 0.9, 1.1, 1.5} : Pace{1.15, 1.55, 3.0, 0.36, 0.52, 0.75, 1.0, 1.5};
+  return dense_int(form) ? Pace{5.7, 0.86, 1.45, 1.0, 0.36, 0.58, 0.43, 1.06} : Pace{4.8, 0.82, 1.42, 0.4, 0.31, 0.56, 0.44, 0.98};
 }
-double between(double few, double all, int64_t wgs) { return few + (all - few) * std::min(1.0, double(wgs) / kCus); }
+double between(double few, double all, double taken) { return few + (all - few) * std::min(1.0, taken); }
 
 int64_t tiles_of(DenseForm form, const DenseShape& s, int tile) {
   return parts(s.m, tile) * parts(s.n, dense_two_b(form) ? tile / 2 : tile);
@@ -61,10 +66,15 @@ int64_t steps_of(DenseForm form, const DenseShape& s) { return parts(s.k, 128 / 
 // wgs workgroups of `per` steps each
 double tiles_time(DenseForm form, int tile, int64_t wgs, int64_t per) {
   const Pace p = pace(form);
-  const int64_t each = parts(wgs, kCus);  // a CU's tiles
-  if (tile == 256) return kStart + double(each) * (p.tile256 + per * between(p.few256, p.all256, wgs));
-  double t = kStart + double(each / 2) * (p.tile128 + per * (each <= 8 ? p.pair128 : p.hot128));
-  if (each % 2) t += p.tile128 + per * between(p.few128, p.all128, wgs);
+  if (tile == 256) {
+    const int64_t each = parts(wgs, kCus);
+    return kStart + double(each) * (p.tile256 + per * between(p.few256, p.all256, double(wgs) / double(each * kCus)));
+  }
+  // rounds of two a CU, the last one of one where that holds the rest
+  const int64_t whole = wgs / (2 * kCus), rest = wgs % (2 * kCus);
+  const double two = between(p.few2, p.all2, double(wgs) / double(parts(wgs, 2 * kCus) * 2 * kCus));
+  double t = kStart + double(whole) * (p.tile128 + per * two);
+  if (rest) t += p.tile128 + per * (rest <= kCus ? between(p.few128, p.all128, double(rest) / kCus) : two);
   return t;
 }
 
@@ -122,11 +132,12 @@ int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols) {
     add(kDenseCols, cols);
     const double over = tile == 256 ? p.tile256 : p.tile128;
     const int places = tile == 256 ? kCus : 2 * kCus;
-    const double alone = tile == 256 ? between(p.few256, p.all256, wgs) : between(p.few128, p.all128, wgs);
-    const double all = tile == 256 ? p.all256 : wgs <= 8 * kCus ? p.pair128 : p.hot128;
-    // half a longest tile for the uneven end
-    const double t = kStart + std::max(over + longest * alone,
-                                       (double(work) * all + double(wgs) * over) / places + (wgs > places ? longest * all / 2 : 0.0));
+    const double taken = double(wgs) / places;
+    const double alone = tile == 256 ? between(p.few256, p.all256, taken) : between(p.few128, p.all128, 2 * taken);
+    const double all = tile == 256 ? alone : between(p.few2, p.all2, taken);
+    // the end is uneven by part of a tile of dx, which come last
+    const double end = wgs > places ? steps_of(kDenseCols, cols) * all / 4 : 0.0;
+    const double t = kStart + std::max(over + longest * alone, (double(work) * all + double(wgs) * over) / places + end);
     if (t < best_t) best_t = t, best = tile;
   }
   return best;

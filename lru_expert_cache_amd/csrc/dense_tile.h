@@ -14,8 +14,8 @@
 // their use.  One barrier per half step makes a half's loads visible (vmcnt of
 // everything older than the two latest halves) and frees the slots read in
 // the half before.  Reads and loads are spread between the matrix
-// instructions.  With one slot's worth less in flight the loop ran 10% slower;
-// with the reads of a step in K order (slots free only at its end) 15%.
+// instructions.  With the reads of a step in K order, whose slots are free only
+// at its end, 8192^3 ran at 1.09 to 1.14 PFLOP/s, so at 1.24 (32x32 instructions).
 //
 // Loads.  buffer_load ... lds moves 16 bytes per lane straight into LDS, lane
 // i at + 16 i of a uniform address: 1 KB per instruction.  An operand along K
@@ -40,7 +40,8 @@
 // drops to 1.9 GHz with them busy 75% of the cycles.  The 16x16 instructions
 // ran 6% faster than the 32x32 ones (which draw more: 1.65 GHz), eight waves
 // 36% faster than four of 128 x 128.  8192^3, sustained: bf16 1.32 PFLOP/s,
-// 8 bit 2.16; K across both operands 1.23.
+// 8 bit 2.16; K across both operands 1.23.  8192 tokens, H 7168, I 2048: forward
+// with g and u kept 573 us (1.26 PFLOP/s), backward 1097 us (1.32).
 #pragma once
 #include <algorithm>
 #include <type_traits>

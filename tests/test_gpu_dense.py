@@ -443,3 +443,30 @@ def test_addresses_off_the_grid(off):
             dc.check(gu, rgu, "gu")
             for a, r in zip(g.backward(gu), g.backward_reference(gu)):
                 dc.check(a, r, name)
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_offsets_past_32_bits(T):
+    """A weight matrix of more than 4 GB, and rows of tokens and results whose distances pass 4 GB together: the last
+    rows and columns."""
+    K, N, far = 8192, 600_000, 2000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    w = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand(N, generator=g, device="cuda") + 0.5
+    x = torch.randint(-128, 128, (T, K), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.rand(T, generator=g, device="cuda") + 0.5
+    y = torch.empty(T, N, device="cuda")
+    d = ft.make_int_matmul(T, K, N, ft.FT_DT_F32)
+    ft.ft_moe_int_matmul(d, x, xs, w, ws, y, torch.empty(ft.ft_moe_int_matmul_work(d), dtype=torch.uint8, device="cuda"))
+    for part in (slice(0, far), slice(N - far, N)):
+        dc.check(y[:, part], dc.int_product_reference(x, xs, w[part], ws[part], torch.float32), "y")
+    del w, y
+    step = (1 << 31) // T // 64 * 64 + 64  # elements: T rows of results pass 8 GB
+    xw = torch.empty(T * step, dtype=torch.int8, device="cuda").view(T, step)[:, :K]
+    xw.copy_(x)
+    w = torch.randint(-128, 128, (far, K), generator=g, device="cuda", dtype=torch.int8)
+    yw = torch.empty(T * step, dtype=torch.float32, device="cuda").view(T, step)[:, :far]
+    d = ft.make_int_matmul(T, K, far, ft.FT_DT_F32, ld_x=step, ld_y=step)
+    ft.ft_moe_int_matmul(d, xw, xs, w, ws, yw, torch.empty(ft.ft_moe_int_matmul_work(d), dtype=torch.uint8, device="cuda"))
+    dc.check(yw, dc.int_product_reference(x, xs, w, ws[:far], torch.float32), "y")
