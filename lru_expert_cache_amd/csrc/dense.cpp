@@ -10,7 +10,7 @@ using namespace ftmoe;
 namespace {
 
 constexpr int32_t kMaxDim = (1 << 24) - 1;  // tokens and widths
-constexpr int32_t kMaxIntK = 131071;        // 127 * 127 * K < 2^31
+constexpr int32_t kMaxIntK = 131071;        // 128 * 128 * K < 2^31
 constexpr int64_t kAlign = 256;             // parts of the scratch memory
 
 template <typename F>
@@ -409,7 +409,8 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
     if (d.tokens == 0) return FT_OK;
     const FfnWork w = ffn_work(d, false, work, x, nullptr, w_gate, w_up, w_down);
     if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
-    if (same(y, {x, w_gate, w_up, w_down, gu, work}) || same(gu, {x, w_gate, w_up, w_down, work}))
+    if (same(y, {x, w_gate, w_up, w_down, gu, work}) || same(gu, {x, w_gate, w_up, w_down, work}) ||
+        same(work, {x, w_gate, w_up, w_down}))
       return bad("an output is also another argument");
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
     DeviceGuard g;
@@ -555,7 +556,8 @@ int ft_moe_int_matmul(const ft_moe_int_product* desc, const int8_t* x, const flo
     const ProductWork k = product_work(d, work, x, w);
     const int64_t need = k.bytes;
     if (const int rc = check_work(work, work_bytes, need)) return rc;
-    if (same(y, {x, x_scale, w, w_scale, work})) return bad("an output is also another argument");
+    if (same(y, {x, x_scale, w, w_scale, work}) || (need && same(work, {x, x_scale, w, w_scale})))
+      return bad("an output is also another argument");
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const int64_t es = size_of(d.out_dtype);
     DeviceGuard g;

@@ -91,7 +91,9 @@ DensePlan plan_of(DenseForm form, const DenseShape* shapes, int count, double* t
       steps = std::max(steps, steps_of(form, shapes[i]));
       bytes += dense_part_bytes(form, shapes[i], 2) / 2;
     }
-    const int most = int(std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, steps / 2)));
+    // more parts than fill the card a few times over only cost their way to memory
+    const int64_t useful = 1 + parts(4 * kCus, std::max<int64_t>(1, tiles));
+    const int most = int(std::min({int64_t(kMaxSplits), useful, std::max<int64_t>(1, steps / 2)}));
     for (int splits = 1; splits <= most; ++splits) {
       double t = tiles_time(form, tile, tiles * splits, parts(steps, splits));
       t += splits > 1 ? kJoin + double(splits) * double(bytes) / kJoinBytes : epilogue;

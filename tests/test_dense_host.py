@@ -149,3 +149,15 @@ def test_scratch_memory_holds_copies_of_rows_that_are_no_whole_pieces(hidden, in
         assert odd >= own + copies
         assert ft.ft_moe_int_gated_ffn_work(_ffn(tokens=tokens, hidden=hidden, inter=inter)) >= tokens * (hidden + 5 * inter)
     assert ft.ft_moe_gated_ffn_work(_ffn(tokens=0, hidden=hidden, inter=inter), backward) >= 0
+
+
+def test_scratch_memory_that_is_an_input():
+    d, w = _ffn(), _Buf(1 << 20)
+    for at in range(4):
+        p = [A, 2 * A, 3 * A, 4 * A]
+        p[at] = w.at
+        _refused(ft.ft_moe_gated_ffn_forward, d, *p, 5 * A, None, w)
+    m = ft.make_int_matmul(2, 17, 16, ft.FT_DT_BF16)  # rows that are copied
+    assert ft.ft_moe_int_matmul_work(m) > 0
+    _refused(ft.ft_moe_int_matmul, m, w.at, 2 * A, 3 * A, 4 * A, 5 * A, w)
+    _refused(ft.ft_moe_int_matmul, m, A, 2 * A, w.at, 4 * A, 5 * A, w)

@@ -470,3 +470,37 @@ def test_offsets_past_32_bits(T):
     d = ft.make_int_matmul(T, K, far, ft.FT_DT_F32, ld_x=step, ld_y=step)
     ft.ft_moe_int_matmul(d, xw, xs, w, ws, yw, torch.empty(ft.ft_moe_int_matmul_work(d), dtype=torch.uint8, device="cuda"))
     dc.check(yw, dc.int_product_reference(x, xs, w, ws[:far], torch.float32), "y")
+
+
+@pytest.mark.parametrize("size", [(4096, 2048, 768), (1300, 777, 901)])
+def test_backward_graph_replays(size):
+    """A captured backward pass whose gradients share a launch (its work queue is cleared in the graph), and one whose
+    operands are copied first: every replay, with eager calls on the same scratch memory between, gives the eager bits."""
+    f = dc.Ffn(*size)
+    T, H, I = size
+    gu, work, s = f.saved(), f.work(True), torch.cuda.Stream()
+    outs = [torch.empty(T, H, dtype=f.t, device="cuda"), *(torch.empty(I, H, dtype=f.t, device="cuda") for _ in range(2)),
+            torch.empty(H, I, dtype=f.t, device="cuda")]
+
+    def call(stream):
+        ft.ft_moe_gated_ffn_backward(f.desc, f.x, f.wg, f.wu, f.wd, gu, f.dy, *outs, work, stream)
+
+    torch.cuda.synchronize()
+    call(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call(torch.cuda.current_stream())
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    for _ in range(4):
+        f.dy.copy_(torch.randn(T, H, generator=g, device="cuda").to(f.t))
+        call(None)
+        torch.cuda.synchronize()
+        want = [v.clone() for v in outs]
+        for v in outs:
+            v.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
