@@ -31,7 +31,7 @@ int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits) {
 }
 
 // Estimated times in microseconds, fitted to 39 products and blocks of normal
-// random numbers, each with either tile alone (within 10%; the choice is within
+// random numbers, each with either tile alone (within 12%; the choice is within
 // 6% of the better tile).  A 256 x 256 workgroup has a CU to itself, 128 x 128
 // ones run two to a CU and read the operands twice as often; a K step takes
 // longer the more of the card's places are taken over the launch, which shares
@@ -54,7 +54,7 @@ struct Pace {
   double few2, all2;               // two on a CU, each
 };
 Pace pace(DenseForm form) {
-  return dense_int(form) ? Pace{5.7, 0.86, 1.45, 1.0, 0.36, 0.58, 0.43, 1.06} : Pace{4.8, 0.82, 1.42, 0.4, 0.31, 0.56, 0.44, 0.98};
+  return dense_int(form) ? Pace{5.5, 0.87, 1.46, 0.7, 0.36, 0.5, 0.43, 1.06} : Pace{5.3, 0.8, 1.41, 0.6, 0.34, 0.56, 0.39, 0.97};
 }
 double between(double few, double all, double taken) { return few + (all - few) * std::min(1.0, taken); }
 
@@ -72,9 +72,9 @@ double tiles_time(DenseForm form, int tile, int64_t wgs, int64_t per) {
   }
   // rounds of two a CU, the last one of one where that holds the rest
   const int64_t whole = wgs / (2 * kCus), rest = wgs % (2 * kCus);
-  const double two = between(p.few2, p.all2, double(wgs) / double(parts(wgs, 2 * kCus) * 2 * kCus));
-  double t = kStart + double(whole) * (p.tile128 + per * two);
-  if (rest) t += p.tile128 + per * (rest <= kCus ? between(p.few128, p.all128, double(rest) / kCus) : two);
+  const double taken = double(rest) / kCus;
+  double t = kStart + double(whole) * (p.tile128 + per * p.all2);
+  if (rest) t += p.tile128 + per * (rest <= kCus ? between(p.few128, p.all128, taken) : between(p.few2, p.all2, taken / 2));
   return t;
 }
 
