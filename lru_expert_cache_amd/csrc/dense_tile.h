@@ -41,7 +41,7 @@
 // ran 6% faster than the 32x32 ones (which draw more: 1.65 GHz), eight waves
 // 36% faster than four of 128 x 128.  8192^3, sustained: bf16 1.32 PFLOP/s,
 // 8 bit 2.16; K across both operands 1.23.  8192 tokens, H 7168, I 2048: forward
-// with g and u kept 573 us (1.26 PFLOP/s), backward 1097 us (1.32).
+// with g and u kept 533 us (1.35 PFLOP/s), backward 1094 us (1.32).
 #pragma once
 #include <algorithm>
 #include <type_traits>
