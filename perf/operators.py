@@ -205,19 +205,21 @@ def _kernels(s):
     if p is None:
         p = s["plan"] = _plan(s)
     ft, kind, d, work = p["ft"], s["kind"], p["d"], p["work"]
+    # the calls' own default is the null stream; the inputs are made, and the results read, on the current one
+    stream = torch.cuda.current_stream()
     if kind in ("product", "linear"):
         if kind == "linear":
-            ft.ft_moe_int_quantize(p["dt"], s["T"], s["K"], s["x"], p["q"], p["xs"], ld_x=s["x"].stride(0))
-        ft.ft_moe_int_matmul(d, p["q"], p["xs"], s["w"], s["ws"], p["y"], work)
+            ft.ft_moe_int_quantize(p["dt"], s["T"], s["K"], s["x"], p["q"], p["xs"], ld_x=s["x"].stride(0), stream=stream)
+        ft.ft_moe_int_matmul(d, p["q"], p["xs"], s["w"], s["ws"], p["y"], work, stream)
         return p["y"]
     if kind == "int_ffn":
-        ft.ft_moe_int_gated_ffn(d, s["x"], s["wg"], s["wgs"], s["wu"], s["wus"], s["wd"], s["wds"], p["y"], work)
+        ft.ft_moe_int_gated_ffn(d, s["x"], s["wg"], s["wgs"], s["wu"], s["wus"], s["wd"], s["wds"], p["y"], work, stream)
         return p["y"]
     if kind == "ffn":
-        ft.ft_moe_gated_ffn_forward(d, s["x"], s["wg"], s["wu"], s["wd"], p["y"], p["gu"], work)
+        ft.ft_moe_gated_ffn_forward(d, s["x"], s["wg"], s["wu"], s["wd"], p["y"], p["gu"], work, stream)
         return (p["y"], p["gu"]) if s["save"] else p["y"]
     o = p["out"]
-    ft.ft_moe_gated_ffn_backward(d, s["x"], s["wg"], s["wu"], s["wd"], s["gu"], s["dy"], o["dx"], o["dwg"], o["dwu"], o["dwd"], work)
+    ft.ft_moe_gated_ffn_backward(d, s["x"], s["wg"], s["wu"], s["wd"], s["gu"], s["dy"], o["dx"], o["dwg"], o["dwu"], o["dwd"], work, stream)
     return o
 
 
