@@ -50,7 +50,8 @@ struct DenseProblem {
   int64_t lddgu, off_du;
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
-  int32_t tokens;        // 8-bit forms, few tokens: a's type (FT_DT_*) where it is yet to be quantised
+  int32_t tokens;        // 8-bit forms, few tokens: a's type where it is yet to be quantised (kDenseInt: FT_DT_F32;
+                         // kDenseIntGated: FT_DT_BF16, FT_DT_F16), else 0
   bool a_whole, b_whole; // this operand's rows are zeros up to a whole 16-byte piece
   uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };

@@ -259,13 +259,15 @@ hipError_t launch_xi(const DenseLaunch& l, hipStream_t s) {
 
 template <typename D, int FORM, typename TO>
 hipError_t launch(const DenseLaunch& l, hipStream_t s) {
-  const int m = l.p[0].m;
-  if constexpr (dense_int(FORM)) {
-    // x as the caller has it; h in fp32
-    if (l.p[0].tokens && FORM == kDenseInt) return launch_xi<D, FORM, TO, 0, float>(l, s);
-    if (l.p[0].tokens == FT_DT_F16) return launch_xi<D, FORM, TO, 0, _Float16>(l, s);
-    if (l.p[0].tokens) return launch_xi<D, FORM, TO, 0, __bf16>(l, s);
+  const int m = l.p[0].m, tokens = l.p[0].tokens;
+  // rows to quantise: x as the caller has it; h in fp32
+  if constexpr (FORM == kDenseIntGated) {
+    if (tokens == FT_DT_F16) return launch_xi<D, FORM, TO, 0, _Float16>(l, s);
+    if (tokens == FT_DT_BF16) return launch_xi<D, FORM, TO, 0, __bf16>(l, s);
   }
+  if constexpr (FORM == kDenseInt)
+    if (tokens == FT_DT_F32) return launch_xi<D, FORM, TO, 0, float>(l, s);
+  if (tokens) return hipErrorInvalidValue;
   if (m <= 8) return launch_xi<D, FORM, TO, 1>(l, s);
   if (m <= 16) return launch_xi<D, FORM, TO, 2>(l, s);
   if (m <= 32) return launch_xi<D, FORM, TO, 4>(l, s);
