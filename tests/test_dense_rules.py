@@ -7,6 +7,7 @@ import pytest
 
 import lru_expert_cache_amd as ft
 from lru_expert_cache_amd import build
+from tests import dense_exact as de
 
 # DenseForm
 GATED, ROWS, GRAD, COLS, OUTER, INT, INT_GATED = range(7)
@@ -43,3 +44,29 @@ def test_only_the_token_types_of_a_form_are_quantised(check, form, tokens):
 @pytest.mark.parametrize("form", [GATED, ROWS])
 def test_16_bit_products_quantise_nothing(check, form):
     assert check("few", form, ft.FT_DT_F32) == ["refused"]
+
+
+def test_tiles_of_the_sizes_that_are_compared_bit_for_bit(check):
+    """The plan sends these sizes to 256 x 256 tiles, with K whole and in parts, dx and the weight gradients together and
+    apart: if it changes, sizes that cover those kernels take their place."""
+    def plans(T, H, I):
+        p = {"gated": check("plan", GATED, T, I, H, 1), "rows": check("plan", ROWS, T, H, I, 1), "dh": check("plan", GRAD, T, I, H, 1),
+             "dx": check("plan", COLS, T, H, I, 2), "dw": check("plan", OUTER, I, H, T, 1, I, H, T, 1, H, I, T, 1),
+             "int": check("plan", INT, T, H, I, 1), "int gated": check("plan", INT_GATED, T, I, H, 1)}
+        pair = check("pair", I, H, T, I, H, T, H, I, T, T, H, I)
+        return {n: (int(v[0]), int(v[1])) for n, v in p.items()}, int(pair[0])
+
+    for size in de.TILED[:2]:
+        p, pair = plans(*size)
+        assert set(p.values()) == {(256, 1)} and pair == 256, (size, p, pair)
+    p, pair = plans(*de.TILED[2])
+    assert p["gated"] == p["rows"] == p["dx"] == p["dw"] == (256, 1) and p["dh"][0] == 256 and p["dh"][1] > 1 and pair == 256
+    p, _ = plans(*de.TILED[3])
+    assert p["dx"][0] == 256 and p["dx"][1] > 1
+    p, _ = plans(*de.TILED[4])
+    assert p["dw"][0] == 256 and p["dw"][1] > 1
+    p, pair = plans(*de.TILED[5])
+    assert p["dx"] == p["dw"] == (256, 1) and pair == 0
+    for T, K, N in de.PRODUCTS[3:5]:
+        assert check("plan", INT, T, N, K, 1) == ["256", "1"]
+    assert {check("plan", INT, T, N, K, 1)[0] for T, K, N in de.PRODUCTS if T > 64} == {"128", "256"}
