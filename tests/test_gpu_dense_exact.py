@@ -75,3 +75,83 @@ def test_int_matmul(size, out):
     torch.cuda.synchronize()
     assert dc.untouched(yb, T, N)
     same(y, (dc.mm(q.double(), w.double().T).float() * xs[:, None] * ws[None, :]).to(t), "y")
+
+
+def off_grid(m, off):
+    """The same rows from an address `off` elements past a 16-byte one, as far apart."""
+    ld = m.stride(0) if m.dim() == 2 else 1
+    flat = torch.zeros(m.shape[0] * ld + off + 64, dtype=m.dtype, device=m.device)
+    start = off + (-flat.data_ptr() // m.element_size()) % (16 // m.element_size())
+    return flat.as_strided(m.shape, m.stride(), start).copy_(m)
+
+
+@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("name", ["x", "w"])
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+def test_int_matmul_off_the_grid(T, name, out):
+    """Codes at addresses that are no multiples of 16 bytes, rows of whole pieces and not: the general kernel, in all
+    its output types."""
+    t, dt = dc.TYPES[out]
+    g = de.generator(8)
+    for K, N in ((256, 130), (250, 77)):
+        q, w = (torch.randint(-127, 128, (n, K), generator=g, dtype=torch.int8).cuda() for n in (T, N))
+        xs, ws = (torch.pow(2.0, torch.randint(-12, -6, (n,), generator=g).float()).cuda() for n in (T, N))
+        a = {"x": q, "w": w}
+        a[name] = off_grid(a[name], 3)
+        assert a[name].data_ptr() % 16
+        y, yb = dc.padded(T, N, 5, t)
+        d = ft.make_int_matmul(T, K, N, dt, ld_y=N + 5)
+        work = torch.empty(ft.ft_moe_int_matmul_work(d), dtype=torch.uint8, device="cuda").fill_(0xFF)
+        ft.ft_moe_int_matmul(d, a["x"], xs, a["w"], ws, y, work)
+        torch.cuda.synchronize()
+        assert dc.untouched(yb, T, N)
+        same(y, (dc.mm(q.double(), w.double().T).float() * xs[:, None] * ws[None, :]).to(t), f"y {K} {N}")
+
+
+@pytest.mark.parametrize("size", [(3, 64, 48), (70, 64, 48), (70, 61, 43), (200, 320, 136)])
+@pytest.mark.parametrize("name", ["x", "wg", "wu", "wd", "all"])
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+def test_int_block_off_the_grid(size, name, type_):
+    v = de.IntValues(*size).to("cuda", torch.float64)
+    t, dt = dc.TYPES[type_]
+    T, H, I = size
+    one = torch.ones(I, device="cuda")
+    a = {"x": v.x.to(t), "wg": v.wg.to(torch.int8), "wu": v.wu.to(torch.int8), "wd": v.wd.to(torch.int8)}
+    for n in a if name == "all" else (name,):
+        a[n] = off_grid(a[n], 1)
+        assert a[n].data_ptr() % 16
+    y, yb = dc.padded(T, H, 0, t)
+    d = ft.make_gated_ffn(dt, T, H, I)
+    work = torch.empty(ft.ft_moe_int_gated_ffn_work(d), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    ft.ft_moe_int_gated_ffn(d, a["x"], a["wg"], one, a["wu"], one, a["wd"], v.down, y, work)
+    torch.cuda.synchronize()
+    assert dc.untouched(yb, T, H)
+    same(y, v.forward(t)[0], "y")
+
+
+@pytest.mark.parametrize("size", [(3, 64, 48), (70, 61, 43), (200, 320, 136)])
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+def test_block_off_the_grid(size, type_):
+    """Each operand, results and saved values among them, and then all."""
+    v = de.Values(*size).to("cuda", torch.float64)
+    T, H, I = size
+    t, dt = dc.TYPES[type_]
+    desc = ft.make_gated_ffn(dt, T, H, I)
+    forward = [(m.to(t)) for m in (v.x, v.wg, v.wu, v.wd)]
+    backward = [m.to(t) for m in (v.bx, v.bg, v.bu, v.bd, v.gu, v.dy)]
+    want_f, want_b = v.forward(t)[:2], [m.to(t) for m in v.backward(t)[:4]]
+    new = lambda r, c, off: off_grid(torch.zeros(r, c, dtype=t, device="cuda"), off)  # noqa: E731
+    for at in range(7):
+        a = [off_grid(m, 1) if at in (i, 6) else m for i, m in enumerate(forward)]
+        out = [new(T, n, 3 if at in (4 + i, 6) else 0) for i, n in enumerate((H, 2 * I))]
+        work = torch.empty(ft.ft_moe_gated_ffn_work(desc), dtype=torch.uint8, device="cuda").fill_(0xFF)
+        ft.ft_moe_gated_ffn_forward(desc, *a, *out, work)
+        for got, want, what in zip(out, want_f, ("y", "gu")):
+            same(got, want, f"{what}, {at} off")
+    for at in range(11):
+        a = [off_grid(m, 5) if at in (i, 10) else m for i, m in enumerate(backward)]
+        out = [new(*s, 1 if at in (6 + i, 10) else 0) for i, s in enumerate(((T, H), (I, H), (I, H), (H, I)))]
+        work = torch.empty(ft.ft_moe_gated_ffn_work(desc, True), dtype=torch.uint8, device="cuda").fill_(0xFF)
+        ft.ft_moe_gated_ffn_backward(desc, *a, *out, work)
+        for got, want, what in zip(out, want_b, ("dx", "dwg", "dwu", "dwd")):
+            same(got, want, f"{what}, {at} off")
