@@ -155,3 +155,12 @@ def test_block_off_the_grid(size, type_):
         ft.ft_moe_gated_ffn_backward(desc, *a, *out, work)
         for got, want, what in zip(out, want_b, ("dx", "dwg", "dwu", "dwd")):
             same(got, want, f"{what}, {at} off")
+
+
+def test_one_token_that_holds_a_nan_or_an_infinity():
+    for bad in ("nan", "inf", "-inf"):
+        f = dc.Ffn(1, 256, 192)
+        f.x[0, 3] = float(bad)
+        assert bool((f.wg[:, 3] < 0).any()) and bool((f.wg[:, 3] > 0).any())  # infinite gates of both signs: -inf * 0 is NaN
+        y, gu = f.forward()
+        assert bool(torch.isnan(y).all()) and not bool(torch.isfinite(gu).any()), bad
