@@ -452,7 +452,13 @@ enum { FT_DT_BF16 = 1, FT_DT_F16 = 2, FT_DT_F32 = 3 };
  * x [T][H], Wg and Wu [I][H], Wd [H][I], y [T][H], gu [T][2 I] holding g in
  * columns 0..I-1 and u in I..2I-1.  All tensors have type `dtype` (bf16 or
  * fp16); sums are fp32, and g, u, h and the gradients of g and u are rounded
- * to `dtype` where they are stored.  Sizes up to 2^24 - 1 per dimension. */
+ * to `dtype` where they are stored: h and those gradients are operands of the
+ * next products, which take 16-bit ones.  So in fp16 an |h| from 65520 on is
+ * infinite and makes its token's y infinite or NaN, though y's value may be
+ * finite, as do gradients of g and u in the backward pass; and gradients below
+ * 2^-14 lose bits, those up to 2^-25 all of them (scale dy, as for the fp16
+ * gradients themselves).  bf16 has fp32's range.  Sizes up to 2^24 - 1 per
+ * dimension. */
 typedef struct {
   int32_t dtype;             /* FT_DT_BF16 or FT_DT_F16 */
   int32_t tokens;            /* T >= 0 */

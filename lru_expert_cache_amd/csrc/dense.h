@@ -260,6 +260,10 @@ struct DenseScales {
 // What becomes of the sums of row m, columns n .. n + cnt - 1 (cnt <= N); v1: the second matrix of a gated form.  E: the operands'
 // type, TO: c's type where it differs (8-bit forms).  Rounding: h, g, u, dg
 // and du are rounded once, to the type they are stored in, from fp32 values.
+// That of h, dg and du is chosen: the next product's matrix instructions take
+// 16-bit operands at 16 times fp32's rate, and half the bytes come back.  It
+// costs the result 1.4 times the error of rounding it alone (relative 2-norm
+// 0.0024 in bf16, 0.0017 without), and in fp16 the range beyond 65504.
 template <int FORM, typename E, typename TO, int N>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                  const float* v0, const float* v1,

@@ -164,3 +164,24 @@ def test_one_token_that_holds_a_nan_or_an_infinity():
         assert bool((f.wg[:, 3] < 0).any()) and bool((f.wg[:, 3] > 0).any())  # infinite gates of both signs: -inf * 0 is NaN
         y, gu = f.forward()
         assert bool(torch.isnan(y).all()) and not bool(torch.isfinite(gu).any()), bad
+
+
+def test_range_of_fp16():
+    """h is rounded to the block's type: up to fp16's largest number it gives a finite y; beyond, its token's y is not
+    finite, and the other tokens keep their bits."""
+    T, H, I = 6, 32, 16
+    t, dt = dc.TYPES["fp16"]
+    x, wg, wu, wd = (torch.zeros(n, m, dtype=t, device="cuda") for n, m in ((T, H), (I, H), (I, H), (H, I)))
+    x[:, 0] = 1
+    x[:, 1] = torch.tensor([65.5, 0.5, 65.5, 66.0, 65.5, -66.0])  # u: h = 65500, which rounds to 65504, or 66000
+    wg[:, 0], wu[:, 1] = 1000, 1
+    wd[torch.arange(H), torch.arange(H) % I] = 2.0**-8
+    y, gu = torch.empty(T, H, dtype=t, device="cuda"), torch.empty(T, 2 * I, dtype=t, device="cuda")
+    d = ft.make_gated_ffn(dt, T, H, I)
+    work = torch.empty(ft.ft_moe_gated_ffn_work(d), dtype=torch.uint8, device="cuda")
+    ft.ft_moe_gated_ffn_forward(d, x, wg, wu, wd, y, gu, work)
+    want = torch.tensor([65504.0, 500.0, 65504.0, 0.0, 65504.0, 0.0], device="cuda") * 2.0**-8
+    keep = torch.tensor([0, 1, 2, 4], device="cuda")
+    same(gu, torch.cat([torch.full((T, I), 1000.0), x[:, 1:2].cpu().expand(T, I)], 1).to(t).cuda(), "gu")
+    same(y[keep], want[keep, None].expand(4, H).to(t), "y")
+    assert not bool(torch.isfinite(y[[3, 5]]).any())
