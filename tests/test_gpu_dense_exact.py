@@ -185,3 +185,128 @@ def test_range_of_fp16():
     same(gu, torch.cat([torch.full((T, I), 1000.0), x[:, 1:2].cpu().expand(T, I)], 1).to(t).cuda(), "gu")
     same(y[keep], want[keep, None].expand(4, H).to(t), "y")
     assert not bool(torch.isfinite(y[[3, 5]]).any())
+
+
+def pick(g, density, *shape):
+    """-1, 0 or 1 on the GPU, in bf16 (for matrices too large to make on the CPU)."""
+    r = torch.randint(0, 1 << 14, shape, generator=g, device="cuda", dtype=torch.int16)
+    at = int(density / 2 * (1 << 14))
+    return (r < at).to(torch.bfloat16) - (r >= (1 << 14) - at).to(torch.bfloat16)
+
+
+def gates(g, T, I, on):
+    """g of 32 (a share `on`), else -128; u of 1 or -1: what the backward pass is given."""
+    gu = torch.empty(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+    gu[:, :I] = torch.where(torch.randint(0, 1 << 14, (T, I), generator=g, device="cuda", dtype=torch.int16) < int(on * (1 << 14)), 32.0, -128.0)
+    gu[:, I:] = torch.where(torch.randint(0, 2, (T, I), generator=g, device="cuda", dtype=torch.int16) > 0, 1.0, -1.0)
+    return gu
+
+
+def ends(n, far):
+    return (slice(0, far), slice(n - far, n))
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_weights_past_32_bits(T):
+    """Weight matrices of more than 4 GB, forward and backward: results at both ends, bit for bit."""
+    H, I, far, t = 8192, 270_000, 2000, torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(21)
+    x, dy = pick(g, 0.1, T, H), pick(g, 0.1, T, H)
+    wg, wu, wd = pick(g, 0.1, I, H), pick(g, 0.1, I, H), pick(g, 0.1, H, I)
+    assert wg.numel() * 2 > 1 << 32
+    x[:, 0], wu[:, 0], wd[:, -1], wd[-1] = 1, 0, 1, 1
+    wg[:, 0] = -172  # closed gates, but for one in fifty (the last among them)
+    wg[::50, 0] = wg[-1, 0] = 144
+    d = ft.make_gated_ffn(ft.FT_DT_BF16, T, H, I)
+    work = torch.empty(ft.ft_moe_gated_ffn_work(d), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    y, gu = torch.empty(T, H, dtype=t, device="cuda"), torch.empty(T, 2 * I, dtype=t, device="cuda")
+    ft.ft_moe_gated_ffn_forward(d, x, wg, wu, wd, y, gu, work)
+    for part in ends(I, far):
+        same(gu[:, part], de.product(x.double(), wg[part].double().T, 1).to(t), "g")
+        same(gu[:, I:][:, part], de.product(x.double(), wu[part].double().T, 1).to(t), "u")
+    v, u = gu[:, :I].double(), gu[:, I:].double()
+    assert bool(((v >= 32) & (v <= 256) | (v <= -89) & (v >= -256)).all()) and float(u.abs().max()) <= 112
+    h = torch.where(v > 0, v * u, 0).to(t)
+    for part in ends(H, far):
+        same(y[:, part], de.product(h.double(), wd[part].double().T, 1).to(t), "y")
+    del y, v, u, h, work
+    gu = gates(g, T, I, 0.1)
+    work = torch.empty(ft.ft_moe_gated_ffn_work(d, True), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    dx, dwg, dwu, dwd = (torch.empty_like(m) for m in (x, wg, wu, wd))
+    wg[:, 0] = 1
+    ft.ft_moe_gated_ffn_backward(d, x, wg, wu, wd, gu, dy, dx, dwg, dwu, dwd, work)
+    dh = de.product(dy.double(), wd.double(), 1)
+    assert float(dh.abs().max()) <= 256
+    v, u = gu[:, :I].double(), gu[:, I:].double()
+    s = (v > 0).double()
+    dg, du, h = dh * u * s, dh * v * s, v * s * u
+    sums = de.product(dg, wg.double(), 1) + de.product(du, wu.double(), 32)
+    assert float((dc.mm(dg.abs(), wg.double().abs()) + dc.mm(du.abs(), wu.double().abs())).max()) <= 2**24
+    same(dx, sums.to(t), "dx")
+    for part in ends(I, far):
+        same(dwg[part], de.product(dg[:, part].T, x.double(), 1).to(t), "dwg")
+        same(dwu[part], de.product(du[:, part].T, x.double(), 32).to(t), "dwu")
+    for part in ends(H, far):
+        same(dwd[part], de.product(dy[:, part].double().T, h, 32).to(t), "dwd")
+
+
+def test_tokens_past_32_bits():
+    """So many tokens that every tensor of theirs passes 4 GB: the ends of what has their rows, the weight gradients
+    whole, bit for bit; and the 8-bit block, whose last tokens have the bits that they have alone."""
+    T, H, I, far, t = 2_200_000, 1024, 1000, 2000, torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(22)
+    x, wg, wu, wd = pick(g, 0.1, T, H), pick(g, 0.1, I, H), pick(g, 0.1, I, H), pick(g, 0.3, H, I)
+    assert T * min(H, I) * 2 > 1 << 32
+    x[:, 0], wu[:, 0] = 1, 0
+    wg[:, 0] = -172
+    wg[::4, 0] = 144
+    d = ft.make_gated_ffn(ft.FT_DT_BF16, T, H, I)
+    work = torch.empty(ft.ft_moe_gated_ffn_work(d), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    y, gu = torch.empty(T, H, dtype=t, device="cuda"), torch.empty(T, 2 * I, dtype=t, device="cuda")
+    ft.ft_moe_gated_ffn_forward(d, x, wg, wu, wd, y, gu, work)
+    for part in ends(T, far):
+        v, u = (de.product(x[part].double(), w.double().T, 1) for w in (wg, wu))
+        same(gu[part], torch.cat([v, u], 1).to(t), "gu")
+        assert bool(((v >= 32) & (v <= 256) | (v <= -89) & (v >= -256)).all()) and float(u.abs().max()) <= 112
+        h = torch.where(v > 0, v * u, 0).to(t).double()
+        same(y[part], de.product(h, wd.double().T, 1).to(t), "y")
+    del gu, work
+    # 8 bit: the tokens as their own rows, weights as codes
+    one, down = torch.ones(I, device="cuda"), torch.ones(H, device="cuda")
+    codes = (wg.clamp(-100, 100).to(torch.int8), one, wu.to(torch.int8), one, wd.to(torch.int8), down)
+    y8 = torch.empty(T, H, dtype=t, device="cuda")
+    work = torch.empty(ft.ft_moe_int_gated_ffn_work(d), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    ft.ft_moe_int_gated_ffn(d, x, *codes, y8, work)
+    for part in (slice(0, 100), slice(T - 100, T)):
+        few = ft.make_gated_ffn(ft.FT_DT_BF16, 100, H, I)
+        alone = torch.empty(100, H, dtype=t, device="cuda")
+        ft.ft_moe_int_gated_ffn(few, x[part], *codes, alone, work)
+        same(y8[part], alone, "y, 8 bit")
+    del y8, work
+    dy, gu = y, gates(g, T, I, 0.25)
+    dy.copy_(pick(g, 0.1, T, H))
+    work = torch.empty(ft.ft_moe_gated_ffn_work(d, True), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    dx, dwg, dwu, dwd = (torch.empty_like(m) for m in (x, wg, wu, wd))
+    wg[:, 0] = 1
+    ft.ft_moe_gated_ffn_backward(d, x, wg, wu, wd, gu, dy, dx, dwg, dwu, dwd, work)
+    sums = [torch.zeros(*s, dtype=torch.float64, device="cuda") for s in ((I, H), (I, H), (H, I))]
+    tops = [torch.zeros_like(s) for s in sums]
+    step = 110_000
+    for r in range(0, T, step):
+        part = slice(r, r + step)
+        dh = de.product(dy[part].double(), wd.double(), 1)
+        assert float(dh.abs().max()) <= 256
+        v, u = gu[part, :I].double(), gu[part, I:].double()
+        s = (v > 0).double()
+        dg, du, h = dh * u * s, dh * v * s, v * s * u
+        for total, top, a, b in zip(sums, tops, (dg, du, dy[part].double()), (x[part].double(), x[part].double(), h)):
+            total += dc.mm(a.T, b)
+            top += dc.mm(a.T.abs(), b.abs())
+        if r in (0, T - step):
+            assert float((dc.mm(dg.abs(), wg.double().abs()) + dc.mm(du.abs(), wu.double().abs())).max()) <= 2**24
+            same(dx[part], (dc.mm(dg, wg.double()) + dc.mm(du, wu.double())).to(t), "dx")
+    for got, total, top, unit, what in zip((dwg, dwu, dwd), sums, tops, (1, 32, 32), ("dwg", "dwu", "dwd")):
+        assert float(top.max()) <= 2**24 * unit
+        same(got, total.to(t), what)
