@@ -500,7 +500,9 @@ int ft_moe_int_quantize(int32_t dtype, int32_t rows, int32_t cols, const void *x
 /* Product of 8-bit codes with a scale per token and per output channel:
  *   y[t][n] = x_scale[t] w_scale[n] sum_k x[t][k] w[n][k]
  * The sums are exact 32-bit integers (K up to 131071); y has type out_dtype
- * (bf16, fp16 or fp32). */
+ * (bf16, fp16 or fp32).  The sum is converted to fp32 and multiplied by
+ * x_scale, then by w_scale, each rounded to fp32: scales so far apart that
+ * sum * x_scale alone leaves fp32's range give an infinity or lost bits. */
 typedef struct {
   int32_t out_dtype;         /* FT_DT_* of y */
   int32_t tokens;            /* T >= 0 */

@@ -30,14 +30,16 @@ int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits) {
   return int64_t(splits) * (dense_two_b(form) ? 2 : 1) * s.m * parts(s.n, 4) * 16;
 }
 
-// Estimated times in microseconds, fitted to 39 products and blocks of normal
-// random numbers, each with either tile alone (within 12%; the choice is within
-// 6% of the better tile).  A 256 x 256 workgroup has a CU to itself, 128 x 128
+// Estimated times in microseconds, fitted to 37 products and blocks of normal
+// random numbers, each with either tile alone: within 13% of 71 of the 74 times
+// (three products of 300 to 1500 tokens with K in parts come out a fifth low).
+// The choice is within 1% of the better tile, where the two launches of a block
+// take different ones within 6% of the better of one tile for both.  A 256 x 256 workgroup has a CU to itself, 128 x 128
 // ones run two to a CU and read the operands twice as often; a K step takes
 // longer the more of the card's places are taken over the launch, which shares
 // power and the L2s.  So 256 x 256 is quicker where
 // it fills the card (forward of 8192 tokens, H 7168, I 2048: 530 us against
-// 696; 8-bit 4096 x 6144 x 6144 133 against 146), 128 x 128 where it does that
+// 696; 8-bit 4096 x 6144 x 6144 131 against 142), 128 x 128 where it does that
 // better (4096 tokens, H 2048, I 768: 45 against 64; 8-bit 1024 x 6144 x 6144 48
 // against 62).  Cutting K costs a second launch and
 // the parts' way to memory and back (77 x 2048 into 768: 23 us in one part,

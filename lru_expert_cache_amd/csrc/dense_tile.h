@@ -27,7 +27,9 @@
 // Bank conflicts.  Units cannot be padded (the loads write contiguously), so
 // the 16-byte pieces of a row are permuted instead, on the side of the source
 // addresses: row r holds piece c at place c ^ key(r), key(r) distinct for the
-// rows that one LDS cycle reads (SQ_LDS_BANK_CONFLICT counts none).
+// rows that one LDS cycle reads.  SQ_LDS_BANK_CONFLICT counts none for operands
+// along K; across K the reads of B meet each bank twice (8192 tokens, H 7168, I
+// 2048: 7.4 M cycles of all CUs in dh, 36.8 M in dx and the weight gradients).
 //
 // Operands.  Lane l of a 16x16 matrix instruction needs row l % 16, K bytes
 // 16 (l / 16) .. + 15 of a 64-byte step.  Along K that is one 16-byte LDS
@@ -41,7 +43,9 @@
 // ran 6% faster than the 32x32 ones (which draw more: 1.65 GHz), eight waves
 // 36% faster than four of 128 x 128.  8192^3, sustained: bf16 1.32 PFLOP/s,
 // 8 bit 2.16; K across both operands 1.23.  8192 tokens, H 7168, I 2048: forward
-// with g and u kept 533 us (1.35 PFLOP/s), backward 1094 us (1.32).
+// with g and u kept 532 us (1.36 PFLOP/s), backward 1087 us (1.33).  The 256 x 256
+// kernels take all 256 registers of a lane and spill some: 20 to 22 in dh, 10 in
+// dx with the weight gradients, 1 to 9 in the others; the 128 x 128 ones none.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -395,7 +399,7 @@ struct TileKernel {
     const DenseProblem& p = l.p[o.problem];
     const int m0 = o.m0, n0 = o.n0, split = o.split;
     // results: lane l has row m = l % 16 of each A fragment and eight columns of each pair of B fragments
-    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF, PF = NF / 2;
+    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF;
     auto column = [&](int y, int j) { return n0 + (TWO ? 0 : y * HN) + wn * NF * 16 + j * 32 + 8 * (lane >> 4); };
     auto row = [&](int xi) { return int64_t(m0) + (xi / MF) * HM + wm * MF * 16 + xi % MF * 16 + (lane & 15); };
     if (p.part) {
