@@ -453,7 +453,10 @@ enum { FT_DT_BF16 = 1, FT_DT_F16 = 2, FT_DT_F32 = 3 };
  * columns 0..I-1 and u in I..2I-1.  All tensors have type `dtype` (bf16 or
  * fp16); sums are fp32, and g, u, h and the gradients of g and u are rounded
  * to `dtype` where they are stored: h and those gradients are operands of the
- * next products, which take 16-bit ones.  So in fp16 an |h| from 65520 on is
+ * next products, which take 16-bit ones.  Up to 16 tokens' h in the forward pass
+ * and up to 64 tokens' h and gradients in the backward pass the products also
+ * take what that rounding left off: such results are rounded once.  With more
+ * tokens it adds about as much as the result's own rounding, in squares.  In fp16 an |h| from 65520 on is
  * infinite and makes its token's y infinite or NaN, though y's value may be
  * finite, as do gradients of g and u in the backward pass; and gradients below
  * 2^-14 lose bits, those up to 2^-25 all of them (scale dy, as for the fp16

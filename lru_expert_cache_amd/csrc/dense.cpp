@@ -230,6 +230,8 @@ struct Packs {
 struct FfnWork {
   int64_t ldi;  // elements between rows of h, and half of a row of dgu
   uint8_t *h, *dgu, *part;
+  int32_t lo;   // rows from an h, dg or du to what its rounding left off, 0 with more than a few tokens
+  int64_t rows; // of h and dgu
   uint32_t* queue;
   // the operands as the products take them
   const void *x, *dy, *wg, *wu, *wd;
@@ -246,13 +248,16 @@ FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base, const voi
   Carve c{static_cast<uint8_t*>(base)};
   const int T = d.tokens, H = d.hidden, I = d.inter;
   w.ldi = up(I, 64);
-  w.h = c.take(int64_t(T) * w.ldi * 2);
+  w.lo = dense_lo(T, backward);
+  w.rows = int64_t(T) + w.lo;
+  w.h = c.take(w.rows * w.ldi * 2);
   int64_t part;
   if (backward) {
-    w.dgu = c.take(int64_t(T) * w.ldi * 4);
+    w.dgu = c.take(w.rows * w.ldi * 4);
     w.queue = reinterpret_cast<uint32_t*>(c.take(kDenseQueue * 4));
+    const int segs = w.lo ? 2 : 1;
     part = std::max({parts_bytes(kDenseGrad, {{T, I, H, 1}}), parts_bytes(kDenseCols, {{T, H, I, 2}}),
-                     parts_bytes(kDenseOuter, {{I, H, T, 1}, {I, H, T, 1}, {H, I, T, 1}})});
+                     parts_bytes(kDenseOuter, {{I, H, T, segs}, {I, H, T, segs}, {H, I, T, segs}})});
   } else {
     part = std::max(parts_bytes(kDenseGated, {{T, I, H, 1}}), parts_bytes(kDenseRows, {{T, H, I, 1}}));
   }
@@ -270,10 +275,10 @@ FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base, const voi
     w.wu = k.matrix(wu, I, H, ld_up, 2, w.whole_in, read_in);
     w.wd = k.matrix(wd, H, I, w.ld_out, 2, w.whole_out);
     if (backward) w.dy = k.matrix(dy, T, H, w.ld_y, 2, w.whole_y);
-    w.whole_i = k.behind(w.h, T, I, w.ldi, 2);
+    w.whole_i = k.behind(w.h, w.rows, I, w.ldi, 2);
     if (backward) {
-      k.behind(w.dgu, T, I, 2 * w.ldi, 2);
-      k.behind(w.dgu + 2 * w.ldi, T, I, 2 * w.ldi, 2);
+      k.behind(w.dgu, w.rows, I, 2 * w.ldi, 2);
+      k.behind(w.dgu + 2 * w.ldi, w.rows, I, 2 * w.ldi, 2);
     }
   }
   w.packs = k.l;
@@ -426,8 +431,10 @@ int ft_moe_gated_ffn_forward(const ft_moe_gated_ffn* desc, const void* x, const 
     p.gu = u8(gu);
     p.ldgu = d.ld_gu;
     p.off_u = d.inter;
+    p.c_lo = w.lo;
     if (const int rc = run(kDenseGated, d.dtype, {p}, w.part, s)) return rc;
     p = product(w.h, w.ldi, w.wd, w.ld_out, d.tokens, d.hidden, d.inter, y, d.ld_y, 2);
+    p.a_lo = w.lo;
     p.a_whole = w.whole_i;
     p.b_whole = w.whole_out;
     return run(kDenseRows, d.dtype, {p}, w.part, s);
@@ -469,6 +476,7 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       cols.a[1] = w.dgu + 2 * w.ldi;
       cols.b[1] = u8(w.wu);
       cols.segs = 2;
+      cols.a_lo = w.lo;
       cols.a_whole = w.whole_i;
       cols.b_whole = w.whole_in;
     }
@@ -479,6 +487,12 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       outer[0].a_whole = outer[1].a_whole = outer[2].b_whole = w.whole_i;
       outer[0].b_whole = outer[1].b_whole = w.whole_x;
       outer[2].a_whole = w.whole_y;
+      if (w.lo) {  // what the rounding left off: a second K segment
+        outer[0].segs = outer[1].segs = outer[2].segs = 2;
+        outer[0].a[1] = outer[0].a[0] + w.lo * outer[0].lda;
+        outer[1].a[1] = outer[1].a[0] + w.lo * outer[1].lda;
+        outer[2].b[1] = outer[2].b[0] + w.lo * outer[2].ldb;
+      }
     }
     if (T > 0) {
       FT_HIP_CHECK(launch_dense_pack(w.packs, s));
@@ -491,12 +505,13 @@ int ft_moe_gated_ffn_backward(const ft_moe_gated_ffn* desc, const void* x, const
       p.dgu = w.dgu;
       p.lddgu = 2 * w.ldi;
       p.off_du = w.ldi;
+      p.c_lo = w.lo;
       // dx and the weight gradients in one launch, where all can be tiled
       int pair = 0;
       if (dx && grads && dense_tileable(kDenseGrad, p) && dense_tileable(kDenseCols, cols) &&
           dense_tileable(kDenseOuter, outer[0]) && dense_tileable(kDenseOuter, outer[1]) &&
           dense_tileable(kDenseOuter, outer[2]))
-        pair = dense_plan_pair({shape(outer[0]), shape(outer[1]), shape(outer[2])}, shape(cols));
+        pair = dense_plan_pair({shape(outer[0]), shape(outer[1]), shape(outer[2])}, shape(cols), w.lo != 0);
       if (const int rc = run(kDenseGrad, d.dtype, {p}, w.part, s, pair ? w.queue : nullptr)) return rc;
       if (pair) {
         DensePair l{};

@@ -48,6 +48,8 @@ struct DenseProblem {
   int64_t ldgu, off_u;   // u's first column in gu
   uint8_t* dgu;          // kDenseGrad: written
   int64_t lddgu, off_du;
+  int32_t c_lo;          // kDenseGated, kDenseGrad: rows from a rounded h, dg, du to what its rounding left off; 0: not kept
+  int32_t a_lo;          // rows from A's values to what their rounding left off, which is added; 0: A has one part
   const float* xs;       // 8-bit forms: scale per row, per column (of each matrix)
   const float* ws[2];
   int32_t tokens;        // 8-bit forms, few tokens: a's type where it is yet to be quantised (kDenseInt: FT_DT_F32;
@@ -56,6 +58,19 @@ struct DenseProblem {
   uint8_t* part;         // split K: 32-bit sums [split][matrix][m][n rounded up to 4], else null
 };
 constexpr int kDenseMaxProblems = 3;
+// h, dg and du are rounded to 16 bits for the next products.  Over many tokens
+// and columns that adds up to 1.4 times the result's own rounding; with few it
+// scatters (1 token, I 128 to 768: over 1.5 times for a quarter of the inputs,
+// 2.6 at worst).  Up to these numbers of tokens the products take both 16-bit
+// parts of such a value, in places that would stay empty: the forward pass in
+// the second eight of a fragment's 16 rows (9 to 16 tokens: in a second
+// fragment), dx in the second 64 of a tile's 128, the weight gradients in a
+// second K step that the first is paired with anyway.
+constexpr int kDenseLoForward = 16, kDenseLoBackward = 64;
+// rows from a value to its rest
+constexpr int dense_lo(int tokens, bool backward) {
+  return tokens == 0 || tokens > (backward ? kDenseLoBackward : kDenseLoForward) ? 0 : backward ? 64 : tokens <= 8 ? 8 : 16;
+}
 struct DenseLaunch {
   DenseProblem p[kDenseMaxProblems];
   int32_t count;
@@ -86,8 +101,8 @@ struct DenseShape {
   int32_t m, n, k, segs;
 };
 DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count);
-// the tile of a DensePair, or 0 where separate launches are quicker
-int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols);
+// the tile of a DensePair, or 0 where separate launches are quicker; only128: 256 x 256 is not there for it
+int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols, bool only128 = false);
 int64_t dense_part_bytes(DenseForm form, const DenseShape& s, int splits);
 
 // dense_any.hip: any size, stride and alignment.  dtype: FT_DT_* of the
@@ -263,8 +278,22 @@ struct DenseScales {
 // That of h, dg and du is chosen: the next product's matrix instructions take
 // 16-bit operands at 16 times fp32's rate, and half the bytes come back.  It
 // costs the result 1.4 times the error of rounding it alone (relative 2-norm
-// 0.0024 in bf16, 0.0017 without), and in fp16 the range beyond 65504.
-template <int FORM, typename E, typename TO, int N>
+// 0.0024 in bf16, 0.0017 without), and in fp16 the range beyond 65504; few
+// tokens keep what it left off (kDenseLoForward).
+// LO: what the rounding of h, dg and du left off is stored too where c_lo asks
+// for it.
+// (the rest, rounded to E; 0 beside infinities and NaN)
+template <typename E, int N>
+__device__ __attribute__((always_inline)) inline void dense_store_rest(uint8_t* base, int64_t at, const float* v, int cnt) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float hi = float(E(v[i]));
+    r[i] = __builtin_isfinite(hi) ? v[i] - hi : 0.0f;
+  }
+  dense_store<E, N>(base, at, r, cnt);
+}
+template <int FORM, typename E, typename TO, int N, bool LO>
 __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProblem& p, int64_t m, int n, int cnt,
                                                                  const float* v0, const float* v1,
                                                                  const DenseWith<FORM, E, N>& with) {
@@ -275,6 +304,7 @@ __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProb
 #pragma unroll
     for (int i = 0; i < N; ++i) h[i] = v0[i] * dense_sigmoid(v0[i]) * v1[i];
     dense_store<TO, N>(p.c, m * p.ldc + n, h, cnt);
+    if (LO && p.c_lo) dense_store_rest<TO, N>(p.c, (m + p.c_lo) * p.ldc + n, h, cnt);
     if (p.gu) {
       dense_store<TO, N>(p.gu, m * p.ldgu + n, v0, cnt);
       dense_store<TO, N>(p.gu, m * p.ldgu + p.off_u + n, v1, cnt);
@@ -293,6 +323,11 @@ __device__ __attribute__((always_inline)) inline void dense_emit(const DenseProb
     dense_store<E, N>(p.dgu, m * p.lddgu + n, dg, cnt);
     dense_store<E, N>(p.dgu, m * p.lddgu + p.off_du + n, du, cnt);
     if (p.c) dense_store<E, N>(p.c, m * p.ldc + n, h, cnt);
+    if (LO && p.c_lo) {
+      dense_store_rest<E, N>(p.dgu, (m + p.c_lo) * p.lddgu + n, dg, cnt);
+      dense_store_rest<E, N>(p.dgu, (m + p.c_lo) * p.lddgu + p.off_du + n, du, cnt);
+      if (p.c) dense_store_rest<E, N>(p.c, (m + p.c_lo) * p.ldc + n, h, cnt);
+    }
   }
 }
 // the 8-bit forms: the int32 sums are exact; their conversion and the scales round in fp32
@@ -319,7 +354,7 @@ __device__ __attribute__((always_inline)) inline void dense_finish(const DensePr
   } else {
     DenseWith<FORM, E, 4> with;
     if constexpr (FORM == kDenseGrad) with.fetch(p, m, n, cnt);
-    dense_emit<FORM, E, TO, 4>(p, m, n, cnt, v0, v1, with);
+    dense_emit<FORM, E, TO, 4, true>(p, m, n, cnt, v0, v1, with);
   }
 }
 #endif

@@ -97,12 +97,13 @@ __global__ __launch_bounds__(256) void k_dense_any(DenseLaunch l) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[j][i] = 0;
 
-  const int per = (p.k + KS - 1) / KS, steps = per * p.segs;
+  // K segments of A's values, then of what their rounding left off
+  const int per = (p.k + KS - 1) / KS, steps = per * p.segs * (p.a_lo ? 2 : 1);
   AnyPiece<E, AR> pa;
   AnyPiece<E, BR> pb[NB];
   auto load = [&](int step) {
-    const int seg = step >= per, k0 = (step - seg * per) * KS;
-    pa.load(p.a[seg], p.lda, m0, p.m, k0, p.k);
+    const int at = step / per, lo = at >= p.segs, seg = at - lo * p.segs, k0 = (step - at * per) * KS;
+    pa.load(p.a[seg] + (lo ? p.a_lo * p.lda : 0), p.lda, m0, p.m, k0, p.k);
 #pragma unroll
     for (int j = 0; j < NB; ++j) pb[j].load(p.b[NB == 2 ? j : seg], p.ldb, n0, p.n, k0, p.k);
   };

@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
   const int rounds = (units + kWaves - 1) / kWaves;
   const int64_t lda = p.lda, ldb = p.ldb;
   const uint8_t *const a0 = p.a[0], *const b0 = p.b[0] + n0 * ldb, *const b1 = p.b[1] + n0 * ldb;
-  const int64_t a_bytes = p.m * lda, b_bytes = int64_t(p.n - n0) * ldb;
+  const int64_t a_bytes = (p.m + p.a_lo) * lda, b_bytes = int64_t(p.n - n0) * ldb;
 
   // load instruction q: 8 rows of 128 bytes; the pieces of row r are permuted by r / 2
   const int r8 = lane >> 3;
@@ -211,6 +211,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_dense_few(DenseLaunch l) {
     stage = stage + 1 == S ? 0 : stage + 1;
     fill = fill + 1 == S ? 0 : fill + 1;
   }
+  if constexpr (FORM == kDenseRows && (XI == 2 || XI == 4))
+    if (p.a_lo) {  // (uniform) the sums of what A's rounding left off, 8 rows (XI 4: 16) behind
+#pragma unroll
+      for (int f = 0; f < FT; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[f][0][i] += XI == 2 ? __shfl_xor(acc[f][0][i], 8) : acc[f][MT - 1][i];
+    }
   __syncthreads();
   Sum* const part = reinterpret_cast<Sum*>(lds);  // [wave][token][kLd]
 #pragma unroll
@@ -259,7 +266,7 @@ hipError_t launch_xi(const DenseLaunch& l, hipStream_t s) {
 
 template <typename D, int FORM, typename TO>
 hipError_t launch(const DenseLaunch& l, hipStream_t s) {
-  const int m = l.p[0].m, tokens = l.p[0].tokens;
+  const int tokens = l.p[0].tokens;
   // rows to quantise: x as the caller has it; h in fp32
   if constexpr (FORM == kDenseIntGated) {
     if (tokens == FT_DT_F16) return launch_xi<D, FORM, TO, 0, _Float16>(l, s);
@@ -268,9 +275,10 @@ hipError_t launch(const DenseLaunch& l, hipStream_t s) {
   if constexpr (FORM == kDenseInt)
     if (tokens == FT_DT_F32) return launch_xi<D, FORM, TO, 0, float>(l, s);
   if (tokens) return hipErrorInvalidValue;
-  if (m <= 8) return launch_xi<D, FORM, TO, 1>(l, s);
-  if (m <= 16) return launch_xi<D, FORM, TO, 2>(l, s);
-  if (m <= 32) return launch_xi<D, FORM, TO, 4>(l, s);
+  const int rows = l.p[0].a_lo ? 2 * l.p[0].a_lo : l.p[0].m;
+  if (rows <= 8) return launch_xi<D, FORM, TO, 1>(l, s);
+  if (rows <= 16) return launch_xi<D, FORM, TO, 2>(l, s);
+  if (rows <= 32) return launch_xi<D, FORM, TO, 4>(l, s);
   return launch_xi<D, FORM, TO, 8>(l, s);
 }
 
@@ -284,6 +292,7 @@ bool dense_few_quantizes(int m, int k) {
 
 hipError_t launch_dense_few(DenseForm form, int dtype, const DenseLaunch& l, hipStream_t s) {
   if (l.count != 1 || l.p[0].m > kDenseFewRows) return hipErrorInvalidValue;
+  if (l.p[0].a_lo && (form != kDenseRows || l.p[0].m > l.p[0].a_lo || (l.p[0].a_lo != 8 && l.p[0].a_lo != 16))) return hipErrorInvalidValue;
   if (l.p[0].tokens && !dense_few_quantizes(l.p[0].m, l.p[0].k)) return hipErrorInvalidValue;
   if (form == kDenseIntGated) return launch<DenseI8, kDenseIntGated, float>(l, s);
   if (form == kDenseInt) {

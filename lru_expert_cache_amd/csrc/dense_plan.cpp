@@ -88,11 +88,14 @@ DensePlan plan_of(DenseForm form, const DenseShape* shapes, int count, double* t
   *time = 1e30;
   for (int tile : {256, 128}) {
     int64_t tiles = 0, steps = 0, bytes = 0;
+    int32_t rows = 0;
     for (int i = 0; i < count; ++i) {
+      rows = std::max(rows, shapes[i].m);
       tiles += tiles_of(form, shapes[i], tile);
       steps = std::max(steps, steps_of(form, shapes[i]));
       bytes += dense_part_bytes(form, shapes[i], 2) / 2;
     }
+    if (tile == 256 && rows <= 128) continue;  // half of each tile would stay empty
     // more parts than fill the card a few times over only cost their way to memory
     const int64_t useful = 1 + parts(4 * kCus, std::max<int64_t>(1, tiles));
     const int most = int(std::min({int64_t(kMaxSplits), useful, std::max<int64_t>(1, steps / 2)}));
@@ -116,7 +119,7 @@ DensePlan dense_plan(DenseForm form, const DenseShape* shapes, int count) {
 // the places, but at least one longest tile.  Only products that are not cut
 // alone either are run so: what a gradient comes to does not depend on which
 // others are asked for.
-int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols) {
+int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols, bool only128) {
   double apart_outer, apart_cols;
   if (plan_of(kDenseOuter, outer, 3, &apart_outer).splits != 1 ||
       plan_of(kDenseCols, &cols, 1, &apart_cols).splits != 1)
@@ -125,6 +128,7 @@ int dense_plan_pair(const DenseShape (&outer)[3], const DenseShape& cols) {
   double best_t = apart_outer + apart_cols;
   const Pace p = pace(kDenseOuter);
   for (int tile : {256, 128}) {
+    if (tile == 256 && only128) continue;
     int64_t wgs = 0, work = 0, longest = 0;
     auto add = [&](DenseForm form, const DenseShape& s) {
       const int64_t n = tiles_of(form, s, tile), steps = std::max<int64_t>(2, steps_of(form, s));

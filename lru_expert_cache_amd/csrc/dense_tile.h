@@ -130,7 +130,7 @@ struct TileOperand {
   }
 };
 
-template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN, bool LO = false>
 struct TileKernel {
   typedef typename D::elem E;
   typedef typename D::acc4 Acc;
@@ -140,6 +140,10 @@ struct TileKernel {
   static constexpr int MF = HM / WM / 16, NF = HN / WN / 16; // fragments of a wave per unit
   static constexpr int KS = kTileKB / 64;                    // matrix instructions along K per step
   static constexpr int NOUT = TWO ? HN : TN;                 // output columns of a tile
+  // A's second half holds what the rounding of the first half's rows left off: the same
+  // lanes end with the sums of both, which are added
+  static constexpr bool kFold = LO && FORM == kDenseCols;
+  static constexpr int kRows = kFold ? MF : 2 * MF;          // rows of a lane's results
   typedef TileOperand<AR, false, HM, NW, ES> OA;
   typedef TileOperand<BR, true, HN, NW, ES> OB;
   // LDS: two of each unit: A lo, A hi, B lo, B hi
@@ -227,7 +231,7 @@ struct TileKernel {
     o.n0 = in / gh * NOUT;
     o.lda = p.lda;
     o.ldb = p.ldb;
-    o.rows_a = p.m - o.m0;
+    o.rows_a = (kFold ? p.m + HM : p.m) - o.m0;
     o.rows_b = p.n - o.n0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -385,6 +389,12 @@ struct TileKernel {
       }
       step(std::integral_constant<int, 0>(), bx, by, nxt, 0);
       step(std::integral_constant<int, 1>(), by, bx, nxt, 1);
+      if constexpr (kFold) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int i = 0; i < MF * NF; ++i) acc[0][y][i / NF][i % NF] += acc[1][y][i / NF][i % NF];
+      }
       finish(l, cur, acc, wm, wn, lane);
       if (last) break;
       cur = nxt;
@@ -399,7 +409,7 @@ struct TileKernel {
     const DenseProblem& p = l.p[o.problem];
     const int m0 = o.m0, n0 = o.n0, split = o.split;
     // results: lane l has row m = l % 16 of each A fragment and eight columns of each pair of B fragments
-    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF;
+    constexpr int YS = TWO ? 1 : 2;
     auto column = [&](int y, int j) { return n0 + (TWO ? 0 : y * HN) + wn * NF * 16 + j * 32 + 8 * (lane >> 4); };
     auto row = [&](int xi) { return int64_t(m0) + (xi / MF) * HM + wm * MF * 16 + xi % MF * 16 + (lane & 15); };
     if (p.part) {
@@ -435,7 +445,7 @@ struct TileKernel {
   template <bool WHOLE, typename ROW, typename COLUMN>
   static __device__ __attribute__((always_inline)) inline void emit(const DenseProblem& p, const Acc (&acc)[2][2][MF][NF],
                                                                     ROW row, COLUMN column) {
-    constexpr int YS = TWO ? 1 : 2, kRows = 2 * MF, PF = NF / 2;
+    constexpr int YS = TWO ? 1 : 2, PF = NF / 2;
     DenseScales<8> ws[YS][PF];
     float xs[kRows];
     constexpr int kAhead = kRows <= 4 ? 3 : 1;
@@ -481,15 +491,15 @@ struct TileKernel {
           if constexpr (dense_int(FORM))
             dense_emit<FORM, TO, 8>(p, m, n, cnt, v0, v1, xs[xi], ws[y][j]);
           else
-            dense_emit<FORM, E, TO, 8>(p, m, n, cnt, v0, v1, with[xi % (kAhead + 1)][y][j]);
+            dense_emit<FORM, E, TO, 8, LO>(p, m, n, cnt, v0, v1, with[xi % (kAhead + 1)][y][j]);
         }
     }
   }
 };
 
-template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN, bool LO>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_dense_tile(DenseLaunch l) {
-  typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
+  typedef TileKernel<D, FORM, TO, TM, TN, WM, WN, LO> K;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[K::kLds];
   if (l.clear && blockIdx.x == 0 && threadIdx.x < kDenseQueue) gstore<uint32_t>(l.clear + threadIdx.x, 0u);
   // a workgroup takes every (grid / 8)th item of its XCD's range
@@ -498,11 +508,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_dense_tile(DenseLaunch l) {
   if (item < end) K::run(l, lds, item, end, [&](int at) { return at + stride; });
 }
 
-template <typename D, int TM, int TN, int WM, int WN>
+template <typename D, int TM, int TN, int WM, int WN, bool LO>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_dense_pair(DensePair l) {
   typedef typename D::elem E;
   typedef TileKernel<D, kDenseOuter, E, TM, TN, WM, WN> O;
-  typedef TileKernel<D, kDenseCols, E, TM, TN, WM, WN> C;
+  typedef TileKernel<D, kDenseCols, E, TM, TN, WM, WN, LO> C;
   static_assert(O::kLds == C::kLds, "one LDS layout");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[O::kLds];
   __shared__ int taken;
@@ -532,7 +542,7 @@ int64_t count_tiles(const DenseLaunch& l) {
   return tiles;
 }
 
-template <typename D, int TM, int TN, int WM, int WN>
+template <typename D, int TM, int TN, int WM, int WN, bool LO = false>
 hipError_t launch_pair(DensePair l, hipStream_t s) {
   const int64_t to = count_tiles<kDenseOuter, TM, TN>(l.outer), tc = count_tiles<kDenseCols, TM, TN>(l.cols);
   if (to + tc > (1 << 30) || l.outer.splits != 1 || l.cols.splits != 1) return hipErrorInvalidValue;
@@ -541,11 +551,19 @@ hipError_t launch_pair(DensePair l, hipStream_t s) {
   // each XCD's range is rounded, so the most of one is a tile more than its share
   const int64_t most = 256 * (TM + TN > 256 ? 1 : 2);
   const uint32_t grid = uint32_t(std::min(most, ((to + 7) / 8 + (tc + 7) / 8) * 8));
-  hipLaunchKernelGGL((k_dense_pair<D, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
+  hipLaunchKernelGGL((k_dense_pair<D, TM, TN, WM, WN, LO>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
   return hipGetLastError();
 }
 
-template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN>
+template <typename D>
+hipError_t launch_pairs(int tile, const DensePair& l, hipStream_t s) {
+  const DenseProblem& dx = l.cols.p[0];
+  if (!dx.a_lo) return tile == 256 ? launch_pair<D, 256, 256, 2, 4>(l, s) : launch_pair<D, 128, 128, 2, 2>(l, s);
+  if (tile != 128 || dx.m > 64 || dx.a_lo != 64) return hipErrorInvalidValue;
+  return launch_pair<D, 128, 128, 2, 2, true>(l, s);
+}
+
+template <typename D, int FORM, typename TO, int TM, int TN, int WM, int WN, bool LO = false>
 hipError_t launch_tile(DenseLaunch l, hipStream_t s) {
   typedef TileKernel<D, FORM, TO, TM, TN, WM, WN> K;
   const int64_t tiles = count_tiles<FORM, TM, TN>(l);
@@ -555,7 +573,7 @@ hipError_t launch_tile(DenseLaunch l, hipStream_t s) {
   // as many workgroups as run at a time: one per CU, or two of the small ones
   const int64_t most = 256 * (K::kLds <= 65536 ? 2 : 1);
   const uint32_t grid = uint32_t(std::min(most, (tiles * l.splits + 7) / 8 * 8));
-  hipLaunchKernelGGL((k_dense_tile<D, FORM, TO, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
+  hipLaunchKernelGGL((k_dense_tile<D, FORM, TO, TM, TN, WM, WN, LO>), dim3(grid), dim3(64 * WM * WN), 0, s, l);
   return hipGetLastError();
 }
 
@@ -596,8 +614,13 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseLaunch l) {
 
 template <typename D, int FORM, typename TO>
 hipError_t launch_tiles(int tile, const DenseLaunch& l, hipStream_t s) {
-  const hipError_t e = tile == 256 ? launch_tile<D, FORM, TO, 256, 256, 2, 4>(l, s)
-                                   : launch_tile<D, FORM, TO, 128, 128, 2, 2>(l, s);
+  hipError_t e = hipErrorInvalidValue;
+  const DenseProblem& p = l.p[0];
+  if (!p.c_lo && !p.a_lo)
+    e = tile == 256 ? launch_tile<D, FORM, TO, 256, 256, 2, 4>(l, s) : launch_tile<D, FORM, TO, 128, 128, 2, 2>(l, s);
+  else if constexpr (FORM == kDenseGrad || FORM == kDenseCols)  // few tokens: kernels of their own, for the others' registers
+    if (tile == 128 && l.count == 1 && p.m <= 64 && p.a_lo == (FORM == kDenseCols ? 64 : 0))
+      e = launch_tile<D, FORM, TO, 128, 128, 2, 2, true>(l, s);
   if (e != hipSuccess || l.splits == 1) return e;
   int64_t most = 0;
   for (int i = 0; i < l.count; ++i) most = std::max(most, int64_t(l.p[i].m) * ((l.p[i].n + 3) / 4));

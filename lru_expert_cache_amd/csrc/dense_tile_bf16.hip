@@ -17,7 +17,7 @@ hipError_t launch_dense_tile_bf16(DenseForm form, int tile, const DenseLaunch& l
 }
 
 hipError_t launch_dense_pair_bf16(int tile, const DensePair& l, hipStream_t s) {
-  return tile == 256 ? launch_pair<DenseBf16, 256, 256, 2, 4>(l, s) : launch_pair<DenseBf16, 128, 128, 2, 2>(l, s);
+  return launch_pairs<DenseBf16>(tile, l, s);
 }
 
 }  // namespace ftmoe

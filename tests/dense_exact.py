@@ -8,7 +8,9 @@ taken by magnitude: a 32-bit sum is exact in any order (`product` asserts it).
 Gates are 18 or more, where 1 + e^-g rounds to 1 and the sigmoid is 1; below
 -89, where e^-g overflows and it is 0; or 0, where it is 1/2: those reciprocals
 are exact.  What is left are the operators' own roundings to their type, which
-happen once and at known places.
+happen once and at known places: of the results, and of h and its gradients
+where there are more than LO_FORWARD or LO_BACKWARD tokens.  Up to these the
+values have up to 16 bits, so that both parts of them are needed.
 
 Inputs are made on the CPU, so that tests without a GPU can look at the same
 ones; references are plain products in the type `wide` on the inputs' device."""
@@ -19,13 +21,14 @@ import lru_expert_cache_amd as ft
 from tests import dense_case as dc
 
 # (tokens, hidden, inter): what the plan makes of those in TILED is pinned by the tests of the rules
-SMALL = [(1, 2048, 768), (9, 264, 136), (33, 1000, 250), (64, 448, 320), (77, 2048, 768), (300, 777, 901), (513, 136, 72)]
+SMALL = [(1, 2048, 768), (8, 264, 136), (9, 264, 136), (16, 512, 1000), (17, 264, 136), (33, 1000, 250), (64, 448, 320), (65, 320, 120), (77, 2048, 768), (300, 777, 901), (513, 136, 72)]
 TILED = [(7990, 1983, 2043),  # 256 x 256 tiles in every form; odd widths, odd counts of K steps along H and T
          (8001, 2000, 1979),  # the same; an odd count along I, columns of H in whole groups of eight
          (4000, 7000, 2000),  # everything in whole groups; K of dh in parts
          (4097, 4000, 4100),  # K of dx in parts
          (8001, 1027, 2043),  # K of the weight gradients in parts
          (4090, 3901, 3907)]  # dx and the weight gradients in launches of their own, K whole
+LO_FORWARD, LO_BACKWARD = 16, 64
 PRODUCTS = [(5, 333, 77), (64, 2048, 257), (130, 1040, 333), (8001, 2003, 1921), (4090, 4083, 3901), (4096, 6144, 1024)]
 
 
@@ -72,8 +75,10 @@ class Values:
         self.wd /= 32
         # backward: gates and ups of their own, as a caller's gu holds them; dh like the sums above
         self.gu = torch.empty(T, 2 * I)
-        self.gu[:, :I] = torch.tensor([32.0, 32.0, 0.0, -128.0])[torch.randint(4, (T, I), generator=g)]
-        self.gu[:, I:] = torch.tensor([1.0, -1.0, 2.0, -2.0, 0.0])[torch.randint(5, (T, I), generator=g)]
+        few = T <= LO_BACKWARD
+        self.gu[:, :I] = torch.tensor([25.0, 37.0, 0.0, -128.0] if few else [32.0, 32.0, 0.0, -128.0])[torch.randint(4, (T, I), generator=g)]
+        ups = torch.arange(-31.0, 32.0) if few else torch.tensor([1.0, -1.0, 2.0, -2.0, 0.0])
+        self.gu[:, I:] = ups[torch.randint(len(ups), (T, I), generator=g)]
         self.dy, self.bd = pick(g, T, H, p), pick(g, H, I, p)
         self.bx, self.bg, self.bu = pick(g, T, H, 0.3) / 8, pick(g, I, H, 0.3), pick(g, I, H, 0.3) / 4
         for at in ((slice(None), I - 1), (-1, slice(0, I))):  # the last term of dx, of the weight gradients
@@ -91,7 +96,8 @@ class Values:
         """y and gu rounded to t, and what they are made of."""
         g, u = product(self.x, self.wg.T, 1), product(self.x, self.wu.T, 1)
         assert bool(((g >= 32) & (g <= 256) | (g <= -89) & (g >= -256)).all()) and float(u.abs().max()) <= 112
-        h = torch.where(g > 0, g * u, 0).to(t).to(g.dtype)
+        h = torch.where(g > 0, g * u, 0)
+        h = h if self.T <= LO_FORWARD else h.to(t).to(g.dtype)
         y = product(h, self.wd.T, 2**-5)
         return y.to(t), torch.cat([g, u], 1).to(t), h, y
 
@@ -105,9 +111,12 @@ class Values:
         dh = product(self.dy, self.bd, 1)
         assert float(dh.abs().max()) <= 112  # dg in halves, du in 32nds: eight bits each
         dg, du, h = self.dgu(dh)
-        assert all(torch.equal(v, v.to(torch.bfloat16).to(v.dtype)) for v in (dg, du, h))
+        for v in (dg, du, h):
+            hi = v.to(torch.bfloat16).to(v.dtype)
+            lo = (v - hi).to(torch.bfloat16).to(v.dtype)
+            assert torch.equal(v, hi + lo if self.T <= LO_BACKWARD else hi)
         dx = product(torch.cat([dg, du], 1), torch.cat([self.bg, self.bu], 0), 0.5)
-        return dx, product(dg.T, self.bx, 2**-4), product(du.T, self.bx, 4), product(self.dy.T, h, 1), (dg, du, h)
+        return dx, product(dg.T, self.bx, 2**-4), product(du.T, self.bx, 2**-3), product(self.dy.T, h, 1), (dg, du, h)
 
 
 class Block(dc.Ffn):

@@ -27,6 +27,8 @@ def test_forward_inputs(size):
     for t in (torch.bfloat16, torch.float16):
         assert bool(torch.isfinite(sums.to(t)).all())
         assert shows(sums, h[:, -1:] @ v.wd[:, -1:].T, t) > SHOWS
+        if T <= de.LO_FORWARD:  # and what a rounding of h would leave off
+            assert shows(sums, sums - h.to(t).float() @ v.wd.T, t) > 0.05 or t == torch.float16
 
 
 @pytest.mark.parametrize("size", SIZES)
@@ -45,6 +47,11 @@ def test_backward_inputs(size):
         assert shows(dwu, du[-1:].T @ v.bx[-1:], t) > SHOWS
         assert shows(dwd, v.dy[-1:].T @ h[-1:], t) > SHOWS * float((v.dy[-1] != 0).float().mean())
         assert shows(dwu[some], less.T @ v.bx, t) > SHOWS
+        # and what a rounding of dg, du and h would leave off (one token has too few terms for it),
+        if v.T <= de.LO_BACKWARD and t == torch.bfloat16:
+            for m, rounded in ((dx, (dg.to(t).float() @ v.bg) + (du.to(t).float() @ v.bu)), (dwg, dg.to(t).float().T @ v.bx),
+                               (dwu, du.to(t).float().T @ v.bx), (dwd, v.dy.T @ h.to(t).float()))[:0 if v.T == 1 else 4]:
+                assert shows(m, m - rounded, t) > 0.01
 
 
 @pytest.mark.parametrize("size", de.SMALL + de.TILED[:2])

@@ -166,25 +166,26 @@ def test_one_token_that_holds_a_nan_or_an_infinity():
         assert bool(torch.isnan(y).all()) and not bool(torch.isfinite(gu).any()), bad
 
 
-def test_range_of_fp16():
-    """h is rounded to the block's type: up to fp16's largest number it gives a finite y; beyond, its token's y is not
+@pytest.mark.parametrize("T", [6, 18])
+def test_range_of_fp16(T):
+    """h is rounded to the block's type (a few tokens' keep what that leaves off): up to fp16's largest number it gives a finite y; beyond, its token's y is not
     finite, and the other tokens keep their bits."""
-    T, H, I = 6, 32, 16
+    H, I, n = 32, 16, T // 6
     t, dt = dc.TYPES["fp16"]
     x, wg, wu, wd = (torch.zeros(n, m, dtype=t, device="cuda") for n, m in ((T, H), (I, H), (I, H), (H, I)))
     x[:, 0] = 1
-    x[:, 1] = torch.tensor([65.5, 0.5, 65.5, 66.0, 65.5, -66.0])  # u: h = 65500, which rounds to 65504, or 66000
+    x[:, 1] = torch.tensor([65.5, 0.5, 65.5, 66.0, 65.5, -66.0] * n)  # u: h = 65500, which rounds to 65504, or 66000
     wg[:, 0], wu[:, 1] = 1000, 1
     wd[torch.arange(H), torch.arange(H) % I] = 2.0**-8
     y, gu = torch.empty(T, H, dtype=t, device="cuda"), torch.empty(T, 2 * I, dtype=t, device="cuda")
     d = ft.make_gated_ffn(dt, T, H, I)
     work = torch.empty(ft.ft_moe_gated_ffn_work(d), dtype=torch.uint8, device="cuda")
     ft.ft_moe_gated_ffn_forward(d, x, wg, wu, wd, y, gu, work)
-    want = torch.tensor([65504.0, 500.0, 65504.0, 0.0, 65504.0, 0.0], device="cuda") * 2.0**-8
-    keep = torch.tensor([0, 1, 2, 4], device="cuda")
+    want = torch.tensor([65504.0, 500.0, 65504.0, 0.0, 65504.0, 0.0] * n, device="cuda") * 2.0**-8
+    keep = want > 0
     same(gu, torch.cat([torch.full((T, I), 1000.0), x[:, 1:2].cpu().expand(T, I)], 1).to(t).cuda(), "gu")
-    same(y[keep], want[keep, None].expand(4, H).to(t), "y")
-    assert not bool(torch.isfinite(y[[3, 5]]).any())
+    same(y[keep], want[keep, None].expand(-1, H).to(t), "y")
+    assert not bool(torch.isfinite(y[~keep]).any())
 
 
 def pick(g, density, *shape):
@@ -227,7 +228,8 @@ def test_weights_past_32_bits(T):
         same(gu[:, I:][:, part], de.product(x.double(), wu[part].double().T, 1).to(t), "u")
     v, u = gu[:, :I].double(), gu[:, I:].double()
     assert bool(((v >= 32) & (v <= 256) | (v <= -89) & (v >= -256)).all()) and float(u.abs().max()) <= 112
-    h = torch.where(v > 0, v * u, 0).to(t)
+    h = torch.where(v > 0, v * u, 0)
+    h = h if T <= de.LO_FORWARD else h.to(t)
     for part in ends(H, far):
         same(y[:, part], de.product(h.double(), wd[part].double().T, 1).to(t), "y")
     del y, v, u, h, work
@@ -310,3 +312,61 @@ def test_tokens_past_32_bits():
     for got, total, top, unit, what in zip((dwg, dwu, dwd), sums, tops, (1, 32, 32), ("dwg", "dwu", "dwd")):
         assert float(top.max()) <= 2**24 * unit
         same(got, total.to(t), what)
+
+
+def few(T, H, I, type_, seed, off=0):
+    """Normal numbers, all operands `off` elements past a 16-byte address."""
+    f = dc.Ffn(T, H, I, type_, seed=seed)
+    for n in ("x", "wg", "wu", "wd", "dy") if off else ():
+        setattr(f, n, off_grid(getattr(f, n), off))
+    return f
+
+
+FEW = [(1, 256, 128, 0), (1, 512, 768, 0), (3, 129, 67, 0), (8, 320, 136, 0), (8, 200, 128, 3), (2, 64, 1, 0), (9, 256, 128, 0), (16, 320, 200, 0), (13, 129, 67, 0), (16, 72, 61, 1)]
+
+
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+@pytest.mark.parametrize("size", FEW)
+def test_few_tokens_are_rounded_once_forward(size, type_):
+    """y of up to 16 tokens is off by its own rounding and what 32-bit sums lose: h keeps both its 16-bit parts, so that
+    it is off by half a unit of half a unit (and half the smallest number)."""
+    for seed in range(5):
+        f = few(*size[:3], type_, seed, size[3])
+        y, _ = f.forward()
+        x, wg, wu, wd = (v.double() for v in (f.x, f.wg, f.wu, f.wd))
+        e, z = dc.half_ulp(f.t), dc.tiny(f.t)
+        g, u = dc.mm(x, wg.T), dc.mm(x, wu.T)
+        eg, eu, s = dc.sum_error(x, wg.T, f.H), dc.sum_error(x, wu.T, f.H), torch.sigmoid(g)
+        h = g * s * u
+        eh = 2 * (1.1 * eg * u.abs() + (g * s).abs() * eu) + h.abs() * (dc.sigmoid_error(g) + e * e + 4 * dc.U32) + z
+        v = dc.mm(h, wd.T)
+        dc.check(y, (v, (dc.mm(eh, wd.abs().T) + 2 * dc.sum_error(h, wd.T, 2 * f.I)) * 1.01 + e * v.abs() + z), f"y {seed}")
+
+
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+@pytest.mark.parametrize("size", FEW + [(33, 130, 72, 0), (64, 256, 200, 0), (64, 72, 61, 1)])
+def test_few_tokens_are_rounded_once_backward(size, type_):
+    """The same of the gradients of up to 64 tokens: of dg, du and h."""
+    for seed in range(3):
+        f = few(*size[:3], type_, seed, size[3])
+        gu = f.saved()
+        got = f.backward(gu)
+        x, wg, wu, wd, dy = (v.double() for v in (f.x, f.wg, f.wu, f.wd, f.dy))
+        e, z, I, T = dc.half_ulp(f.t), dc.tiny(f.t), f.I, f.T
+        g, u = gu[:, :I].double(), gu[:, I:].double()
+        s, se = torch.sigmoid(g), dc.sigmoid_error(g)
+        dh, edh = dc.mm(dy, wd), dc.sum_error(dy, wd, f.H)
+        h = g * s * u
+        eh = h.abs() * (se + 4 * dc.U32 + e * e) + z
+        fg = u * s * (1 + g * (1 - s))
+        efg = u.abs() * s * ((1 + g.abs()) * (2 * se + 8 * dc.U32))
+        dg, du = dh * fg, dh * g * s
+        edg = 2 * (edh * fg.abs() + dh.abs() * efg) + e * e * dg.abs() + z
+        edu = 2 * (edh * (g * s).abs() + dh.abs() * (g * s).abs() * (se + 4 * dc.U32)) + e * e * du.abs() + z
+        both, w = torch.cat([dg, du], 1), torch.cat([wg, wu], 0)
+        want = ((dc.mm(both, w), dc.mm(torch.cat([edg, edu], 1), w.abs()) + 2 * dc.sum_error(both, w, 4 * I)),
+                (dc.mm(dg.T, x), dc.mm(edg.T, x.abs()) + 2 * dc.sum_error(dg.T, x, 2 * T)),
+                (dc.mm(du.T, x), dc.mm(edu.T, x.abs()) + 2 * dc.sum_error(du.T, x, 2 * T)),
+                (dc.mm(dy.T, h), dc.mm(dy.abs().T, eh) + 2 * dc.sum_error(dy.T, h, 2 * T)))
+        for m, (v, err), name in zip(got, want, ("dx", "dwg", "dwu", "dwd")):
+            dc.check(m, (v, err * 1.01 + e * v.abs() + z), f"{name} {seed}")
