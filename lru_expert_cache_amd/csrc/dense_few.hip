@@ -16,7 +16,12 @@
 // quarter of a wave: 14.0 us against 9.7 for a gated product of 16 tokens, H
 // 6144, I 2048 (50 MB: 5.2 TB/s, a large copy moves 4.9).
 //
-// Eight waves up to 16 tokens, four above (their LDS stages are larger; eight
+// Up to 16 tokens of the 16-bit block's h keep what their rounding left off
+// (a_lo): as many rows again, 8 or 16 behind, whose sums are added before the
+// waves' meet.  Both products of a block, 1 token, H 2048, I 768 6.5 us without,
+// 6.9 with; 16 tokens, H 6144, I 2048 16.2 and 16.9.
+//
+// Eight waves up to 16 rows, four above (their LDS stages are larger; eight
 // with two stages: 14.3 us against 14.1 at 64 tokens).  FT is 1 while the
 // workgroups then fit the CUs in one round, else 2, which reads the tokens
 // half as often: N 6144, K 2048, 16 tokens 6.8 us against 10.0; N 2048 (gated),

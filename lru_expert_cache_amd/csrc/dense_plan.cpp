@@ -95,7 +95,9 @@ DensePlan plan_of(DenseForm form, const DenseShape* shapes, int count, double* t
       steps = std::max(steps, steps_of(form, shapes[i]));
       bytes += dense_part_bytes(form, shapes[i], 2) / 2;
     }
-    if (tile == 256 && rows <= 128) continue;  // half of each tile would stay empty
+    // half of each tile would stay empty (the fit gives such products 128 x 128 anyway; few tokens
+    // whose rests fill the half have no other kernel)
+    if (tile == 256 && rows <= 128) continue;
     // more parts than fill the card a few times over only cost their way to memory
     const int64_t useful = 1 + parts(4 * kCus, std::max<int64_t>(1, tiles));
     const int most = int(std::min({int64_t(kMaxSplits), useful, std::max<int64_t>(1, steps / 2)}));

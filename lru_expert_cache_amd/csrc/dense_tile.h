@@ -141,7 +141,8 @@ struct TileKernel {
   static constexpr int KS = kTileKB / 64;                    // matrix instructions along K per step
   static constexpr int NOUT = TWO ? HN : TN;                 // output columns of a tile
   // A's second half holds what the rounding of the first half's rows left off: the same
-  // lanes end with the sums of both, which are added
+  // lanes end with the sums of both, which are added (64 tokens, H 2048, I 768: backward
+  // 30.8 us, as without; as rows of their own, joined in memory, 32.8)
   static constexpr bool kFold = LO && FORM == kDenseCols;
   static constexpr int kRows = kFold ? MF : 2 * MF;          // rows of a lane's results
   typedef TileOperand<AR, false, HM, NW, ES> OA;
