@@ -1,98 +1,13 @@
 // C entry points of the dense feed-forward operators: argument checks, the
 // layout of the scratch memory, and the sequence of products of each call.
-#include <algorithm>
-#include <initializer_list>
-
 #include "dense.h"
+#include "entry.h"
 
 using namespace ftmoe;
 
 namespace {
 
-constexpr int32_t kMaxDim = (1 << 24) - 1;  // tokens and widths
-constexpr int32_t kMaxIntK = 131071;        // 128 * 128 * K < 2^31
-constexpr int64_t kAlign = 256;             // parts of the scratch memory
-
-template <typename F>
-int guarded(F f) {
-  try {
-    return f();
-  } catch (...) {  // an error message that could not be stored
-    return FT_E_HIP;
-  }
-}
-
-int bad(const char* what) {
-  set_error("%s", what);
-  return FT_E_INVALID;
-}
-
-int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// scratch memory, handed out in order; the same code lays it out (base 0) and uses it
-struct Carve {
-  uint8_t* base;
-  int64_t used = 0;
-  uint8_t* take(int64_t bytes) {
-    uint8_t* p = base + used;
-    used += up(bytes, kAlign);
-    return p;
-  }
-};
-
-struct Arg {
-  const void* p;
-  int64_t align;  // of the element type
-  const char* name;
-};
-
-// Every pointer is there, aligned for its elements and memory of one device,
-// the stream's; that device is made current while the guard lives.
-struct DeviceGuard {
-  int back = -1;
-  ~DeviceGuard() {
-    if (back >= 0) (void)hipSetDevice(back);
-  }
-  int enter(hipStream_t s, std::initializer_list<Arg> args) {
-    for (const Arg& a : args) {
-      if (!a.p) {
-        set_error("%s is NULL", a.name);
-        return FT_E_INVALID;
-      }
-      if (reinterpret_cast<uintptr_t>(a.p) % uintptr_t(a.align)) {
-        set_error("%s is not aligned to %lld bytes", a.name, (long long)a.align);
-        return FT_E_INVALID;
-      }
-    }
-    int cur = 0, dev = 0;
-    FT_HIP_CHECK(hipGetDevice(&cur));
-    dev = cur;
-    if (s) FT_HIP_CHECK(hipStreamGetDevice(s, &dev));
-    for (const Arg& a : args) {
-      hipPointerAttribute_t at;
-      if (hipPointerGetAttributes(&at, a.p) != hipSuccess) {
-        (void)hipGetLastError();
-        at.type = hipMemoryTypeUnregistered;
-      }
-      if ((at.type != hipMemoryTypeDevice && at.type != hipMemoryTypeManaged) || at.device != dev) {
-        set_error("%s is not memory of device %d, the stream's", a.name, dev);
-        return FT_E_INVALID;
-      }
-    }
-    if (dev != cur) {
-      FT_HIP_CHECK(hipSetDevice(dev));
-      back = cur;
-    }
-    return FT_OK;
-  }
-};
-
-bool dim_ok(int64_t v, int64_t lo) { return v >= lo && v <= kMaxDim; }
-// a row distance: 0 = the width; a limit keeps every byte offset within 64 bits
-bool row_ok(int64_t& ld, int64_t width) {
-  if (ld == 0) ld = width;
-  return ld >= width && ld < (int64_t(1) << 32);
-}
+constexpr int32_t kMaxIntK = 131071;  // 128 * 128 * K < 2^31
 
 // checks a block's description and fills in the row distances
 int check_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
@@ -286,12 +201,6 @@ FfnWork ffn_work(const ft_moe_gated_ffn& d, bool backward, void* base, const voi
   return w;
 }
 
-bool same(const void* p, std::initializer_list<const void*> others) {
-  for (const void* o : others)
-    if (p && p == o) return true;
-  return false;
-}
-
 // ------------------------------------------------------------ 8-bit
 int check_product(const ft_moe_int_product* d, ft_moe_int_product& o) {
   if (!d) return bad("NULL description");
@@ -305,8 +214,6 @@ int check_product(const ft_moe_int_product* d, ft_moe_int_product& o) {
     return bad("a row distance (ld_*) is smaller than its row, or 2^32 or more");
   return FT_OK;
 }
-int64_t size_of(int dtype) { return dtype == FT_DT_F32 ? 4 : 2; }
-
 struct IntWork {
   int64_t ldx, ldh, ldf;
   int8_t *xq, *hq;
@@ -378,15 +285,6 @@ int check_int_ffn(const ft_moe_gated_ffn* d, ft_moe_gated_ffn& o) {
   if (const int rc = check_ffn(d, o)) return rc;
   if (o.hidden > kMaxIntK || o.inter > kMaxIntK) {
     set_error("bad sizes: hidden %d, inter %d (8 bit: at most %d)", o.hidden, o.inter, kMaxIntK);
-    return FT_E_INVALID;
-  }
-  return FT_OK;
-}
-
-int check_work(const void* work, int64_t have, int64_t need) {
-  if (have < need || (need > 0 && !work)) {
-    set_error("the call needs %lld bytes of scratch memory, %lld given", (long long)need,
-              (long long)(work ? have : 0));
     return FT_E_INVALID;
   }
   return FT_OK;
