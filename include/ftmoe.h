@@ -526,6 +526,121 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn *d, const void *x, const int8_t 
                          const int8_t *w_up, const float *up_scale, const int8_t *w_down, const float *down_scale,
                          void *y, void *work, int64_t work_bytes, void *hip_stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the blocks: the norm before a block, the adapters beside a
+ * projection, the balance of a router.  The rules of the dense operators
+ * above hold here too: device memory owned by the caller, work enqueued on
+ * hip_stream, no allocation, calls that may be captured, row distances
+ * (ld_*) in elements with 0 for the width itself, any size, stride and
+ * element-aligned address, sums in a fixed order.  What may lie in the same
+ * place is named at each call; any other overlap of an output with an
+ * argument is refused.  `work` is 16-byte aligned.
+ */
+
+/* Root-mean-square norm of a residual stream.
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
+ * x, weight and y have type dtype; the stream's tensors (residual, sum and
+ * their gradients) have residual_dtype.  The norm is taken of the unrounded s:
+ * sum and y are rounded once each.  Sizes up to 2^24 - 1 per dimension. */
+typedef struct {
+  int32_t dtype;          /* FT_DT_* of x, weight, y and their gradients */
+  int32_t residual_dtype; /* of residual, sum, dsum, dresidual: dtype or FT_DT_F32; 0 = dtype */
+  int32_t rows, cols;     /* rows >= 0, cols >= 1 */
+  float eps;              /* >= 0, finite */
+  int64_t ld_x;           /* rows of x and dx */
+  int64_t ld_residual;    /* rows of residual, dsum and dresidual */
+  int64_t ld_sum;         /* rows of sum */
+  int64_t ld_y;           /* rows of y and dy */
+  int64_t ld_codes;       /* rows of codes */
+} ft_moe_rms_norm;
+
+/* residual may be NULL (s = x).  Outputs, each of which may be NULL: sum = s;
+ * y; codes and scale (together): the row's 8-bit codes as ft_moe_int_quantize
+ * defines them, of the unrounded y (scale = fp32(max|y| / 127), codes = y /
+ * scale to the nearest integer, ties to even).  Statistics and codes are
+ * formed in 64 bits: codes and scale are those of the exact y but where it
+ * lies within 2^-40 of a border.  sum and y may each be x or residual (the
+ * same address, type and row distance), not one and the same. */
+int ft_moe_rms_norm_forward(const ft_moe_rms_norm *d, const void *x, const void *residual, const void *weight,
+                            void *sum, void *y, int8_t *codes, float *scale, void *hip_stream);
+
+/* Scratch bytes of a backward call. */
+int ft_moe_rms_norm_work(const ft_moe_rms_norm *d, int64_t *bytes);
+
+/* Gradients, from sum as the forward pass left it:
+ *   r = 1 / sqrt(mean(s^2) + eps), g = dy weight
+ *   ds = r (g - s r^2 mean(g s)) + dsum,  dweight = sum over rows of dy s r
+ * ds is the gradient of x and of residual alike; it is written as dx (dtype)
+ * and dresidual (residual_dtype), either of which may be NULL.  dsum is the
+ * gradient that comes back along the stream, or NULL.  dweight may be NULL; it
+ * is written, not added to, and 0 with no rows.  dx and dresidual may each be
+ * dy, dsum or sum (the same address, type and row distance). */
+int ft_moe_rms_norm_backward(const ft_moe_rms_norm *d, const void *sum, const void *weight, const void *dy,
+                             const void *dsum, void *dx, void *dresidual, void *dweight, void *work,
+                             int64_t work_bytes, void *hip_stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   y[t] = base[t] + scale[i] B[i] (A[i] x[t]),  i = ids[t]
+ * x [T][K], A [n][R][K], B [n][N][R] (adapter i's rows follow adapter i - 1's),
+ * base and y [T][N], ids [T] in any order.  A token whose id is not in
+ * 0..n-1 has no adapter: y[t] = base[t].  A x is held in 32 bits and enters
+ * the second product in two 16-bit parts: y is rounded once.  base is the
+ * projection's result (of ft_moe_int_matmul, say; with FT_DT_F32 nothing of it
+ * was rounded before), or NULL for 0. */
+typedef struct {
+  int32_t dtype;      /* of x, A and B: FT_DT_BF16 or FT_DT_F16 */
+  int32_t base_dtype; /* of base: out_dtype or FT_DT_F32; 0 = out_dtype */
+  int32_t out_dtype;  /* of y: dtype or FT_DT_F32; 0 = dtype */
+  int32_t tokens;     /* T >= 0 */
+  int32_t in, out;    /* K, N: 1..2^24 - 1 */
+  int32_t rank;       /* R: 1..256; adapters of lower ranks are padded with zeros */
+  int32_t adapters;   /* n: 1..65536 */
+  int64_t ld_x, ld_a, ld_b, ld_base, ld_y;
+} ft_moe_adapters;
+int ft_moe_adapters_work(const ft_moe_adapters *d, int64_t *bytes);
+/* scale: [n] fp32, or NULL for 1.  y may be base (the same address, type and
+ * row distance): rows without an adapter are then not touched. */
+int ft_moe_adapters_apply(const ft_moe_adapters *d, const void *x, const int32_t *ids, const void *a, const void *b,
+                          const float *scale, const void *base, void *y, void *work, int64_t work_bytes,
+                          void *hip_stream);
+
+/* A router's balance over a batch of tokens, on its logits z [T][E]:
+ *   p = softmax(z[t]),  sel[t] = the top_k largest logits (larger first, lower
+ *   index on ties: as in ft_moe_layer_forward),  w[t] = their softmax
+ *   c_e = choices of expert e,  V = tokens counted
+ *   loss = weight E / (k V^2) sum_e c_e sum_t p[t][e]
+ * (weight times E sum_e f_e P_e with f_e = c_e / (k V) and P_e the mean
+ * probability; 1 times weight when all experts are alike).  A token is left
+ * out (not counted, sel -1, w 0, gradient 0) when valid[t] is 0 or all its
+ * logits are -inf.  A logit of -inf, or NaN, is never chosen: ranks for which
+ * no other is left hold sel -1 and w 0, and are not counted.  A NaN or +inf in
+ * a token that counts makes loss and that token's gradients NaN. */
+typedef struct {
+  int32_t dtype;     /* FT_DT_* of logits and dlogits */
+  int32_t tokens;    /* T >= 0 */
+  int32_t experts;   /* E: 1..512 */
+  int32_t top_k;     /* k: 1..min(E, 16) */
+  float weight;      /* finite */
+  int64_t ld_logits; /* rows of logits and dlogits */
+} ft_moe_balance;
+/* Scratch bytes of a forward call. */
+int ft_moe_balance_work(const ft_moe_balance *d, int64_t *bytes);
+/* valid: [T] bytes, or NULL for all; sel [T][k] int32, w [T][k] fp32, counts
+ * [E + 1] int32 (c_e, then V), loss [1] fp32. */
+int ft_moe_balance_forward(const ft_moe_balance *d, const void *logits, const uint8_t *valid, int32_t *sel, float *w,
+                           int32_t *counts, float *loss, void *work, int64_t work_bytes, void *hip_stream);
+/* Gradient with respect to the logits of dloss * loss + sum(dw * w):
+ *   dz[e] = dloss p_e (C_e - sum_j C_j p_j) + [e = sel[i]] w[i] (dw[i] - sum_j w[j] dw[j]),
+ *   C_e = weight E c_e / (k V^2)
+ * (c_e and V are constants).  Reads counts as the forward pass left them;
+ * ranks that share a batch add theirs up before, and get the gradient of the
+ * whole batch's loss.  dloss: [1] fp32 in device memory, or NULL for 1.  dw:
+ * [T][k] fp32, or NULL for none (sel and w are then not read and may be
+ * NULL).  dlogits may be logits. */
+int ft_moe_balance_backward(const ft_moe_balance *d, const void *logits, const uint8_t *valid, const int32_t *sel,
+                            const float *w, const int32_t *counts, const float *dw, const float *dloss, void *dlogits,
+                            void *hip_stream);
+
 void ft_moe_destroy_pool(ft_moe_pool *p);
 const char *ft_moe_last_error(void);
 

@@ -40,7 +40,9 @@ EXPORTED = ["ft_moe_init_pool", "ft_moe_layer_forward", "ft_moe_pool_stats", "ft
             "ft_moe_set_hybrid_share_format", "ft_moe_get_hybrid_share", "ft_moe_rebalance",
             "ft_moe_debug_read", "ft_moe_gated_ffn_work", "ft_moe_gated_ffn_forward", "ft_moe_gated_ffn_backward",
             "ft_moe_int_quantize", "ft_moe_int_matmul_work", "ft_moe_int_matmul", "ft_moe_int_gated_ffn_work",
-            "ft_moe_int_gated_ffn"]
+            "ft_moe_int_gated_ffn", "ft_moe_rms_norm_forward", "ft_moe_rms_norm_work", "ft_moe_rms_norm_backward",
+            "ft_moe_adapters_work", "ft_moe_adapters_apply", "ft_moe_balance_work", "ft_moe_balance_forward",
+            "ft_moe_balance_backward"]
 FT_DT_BF16, FT_DT_F16, FT_DT_F32 = 1, 2, 3
 FT_DBG_H_CODES, FT_DBG_H_SCALES, FT_DBG_ROW_SLOT = 0, 1, 2
 
@@ -123,6 +125,25 @@ class ft_moe_int_product(ctypes.Structure):
                 ("ld_y", ctypes.c_int64)]
 
 
+class ft_moe_rms_norm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("eps", ctypes.c_float), ("ld_x", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_sum", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_codes", ctypes.c_int64)]
+
+
+class ft_moe_adapters(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("base_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("in", ctypes.c_int32), ("out", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("adapters", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_a", ctypes.c_int64),
+                ("ld_b", ctypes.c_int64), ("ld_base", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
+
+
+class ft_moe_balance(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("weight", ctypes.c_float), ("ld_logits", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -181,6 +202,7 @@ def lib() -> ctypes.CDLL:
     L.ft_moe_profile_read.restype = ctypes.c_int
     I32, I64 = ctypes.c_int32, ctypes.c_int64
     FFN, PROD, I64P = ctypes.POINTER(ft_moe_gated_ffn), ctypes.POINTER(ft_moe_int_product), ctypes.POINTER(I64)
+    NORM, ADAPT, BAL = (ctypes.POINTER(t) for t in (ft_moe_rms_norm, ft_moe_adapters, ft_moe_balance))
     for name, args in (("ft_moe_gated_ffn_work", [FFN, I32, I64P]),
                        ("ft_moe_gated_ffn_forward", [FFN] + [P] * 7 + [I64, P]),
                        ("ft_moe_gated_ffn_backward", [FFN] + [P] * 11 + [I64, P]),
@@ -188,7 +210,15 @@ def lib() -> ctypes.CDLL:
                        ("ft_moe_int_matmul_work", [PROD, I64P]),
                        ("ft_moe_int_matmul", [PROD] + [P] * 6 + [I64, P]),
                        ("ft_moe_int_gated_ffn_work", [FFN, I64P]),
-                       ("ft_moe_int_gated_ffn", [FFN] + [P] * 9 + [I64, P])):
+                       ("ft_moe_int_gated_ffn", [FFN] + [P] * 9 + [I64, P]),
+                       ("ft_moe_rms_norm_work", [NORM, I64P]),
+                       ("ft_moe_rms_norm_forward", [NORM] + [P] * 8),
+                       ("ft_moe_rms_norm_backward", [NORM] + [P] * 8 + [I64, P]),
+                       ("ft_moe_adapters_work", [ADAPT, I64P]),
+                       ("ft_moe_adapters_apply", [ADAPT] + [P] * 8 + [I64, P]),
+                       ("ft_moe_balance_work", [BAL, I64P]),
+                       ("ft_moe_balance_forward", [BAL] + [P] * 7 + [I64, P]),
+                       ("ft_moe_balance_backward", [BAL] + [P] * 9)):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ctypes.c_int
     L.ft_moe_destroy_pool.argtypes = [P]
@@ -489,3 +519,62 @@ def ft_moe_int_gated_ffn(d: ft_moe_gated_ffn, x, w_gate, gate_scale, w_up, up_sc
     return _check(lib().ft_moe_int_gated_ffn(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(gate_scale), _ptr(w_up),
                                              _ptr(up_scale), _ptr(w_down), _ptr(down_scale), _ptr(y), *_work(work),
                                              _stream(stream)))
+
+
+# ---------------------------------------------------------------- norm, adapters, router balance
+
+
+def make_rms_norm(dtype, rows, cols, eps, residual_dtype=0, ld_x=0, ld_residual=0, ld_sum=0, ld_y=0, ld_codes=0):
+    return ft_moe_rms_norm(int(dtype), int(residual_dtype), int(rows), int(cols), float(eps), int(ld_x),
+                           int(ld_residual), int(ld_sum), int(ld_y), int(ld_codes))
+
+
+def make_adapters(dtype, tokens, in_features, out_features, rank, adapters, base_dtype=0, out_dtype=0, ld_x=0, ld_a=0,
+                  ld_b=0, ld_base=0, ld_y=0):
+    return ft_moe_adapters(int(dtype), int(base_dtype), int(out_dtype), int(tokens), int(in_features),
+                           int(out_features), int(rank), int(adapters), int(ld_x), int(ld_a), int(ld_b), int(ld_base),
+                           int(ld_y))
+
+
+def make_balance(dtype, tokens, experts, top_k, weight, ld_logits=0):
+    return ft_moe_balance(int(dtype), int(tokens), int(experts), int(top_k), float(weight), int(ld_logits))
+
+
+def ft_moe_rms_norm_forward(d: ft_moe_rms_norm, x, residual, weight, sum=None, y=None, codes=None, scale=None,
+                            stream=None) -> int:
+    return _check(lib().ft_moe_rms_norm_forward(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(sum),
+                                                _ptr(y), _ptr(codes), _ptr(scale), _stream(stream)))
+
+
+def ft_moe_rms_norm_work(d: ft_moe_rms_norm) -> int:
+    return _work_bytes(lib().ft_moe_rms_norm_work, ctypes.byref(d))
+
+
+def ft_moe_rms_norm_backward(d: ft_moe_rms_norm, sum, weight, dy, dsum=None, dx=None, dresidual=None, dweight=None,
+                             work=None, stream=None) -> int:
+    return _check(lib().ft_moe_rms_norm_backward(ctypes.byref(d), _ptr(sum), _ptr(weight), _ptr(dy), _ptr(dsum),
+                                                 _ptr(dx), _ptr(dresidual), _ptr(dweight), *_work(work),
+                                                 _stream(stream)))
+
+
+def ft_moe_adapters_work(d: ft_moe_adapters) -> int:
+    return _work_bytes(lib().ft_moe_adapters_work, ctypes.byref(d))
+
+
+def ft_moe_adapters_apply(d: ft_moe_adapters, x, ids, a, b, scale, base, y, work=None, stream=None) -> int:
+    return _check(lib().ft_moe_adapters_apply(ctypes.byref(d), _ptr(x), _ptr(ids), _ptr(a), _ptr(b), _ptr(scale),
+                                              _ptr(base), _ptr(y), *_work(work), _stream(stream)))
+
+
+def ft_moe_balance_work(d: ft_moe_balance) -> int:
+    return _work_bytes(lib().ft_moe_balance_work, ctypes.byref(d))
+
+
+def ft_moe_balance_forward(d: ft_moe_balance, logits, valid, sel, w, counts, loss, work=None, stream=None) -> int:
+    return _check(lib().ft_moe_balance_forward(ctypes.byref(d), _ptr(logits), _ptr(valid), _ptr(sel), _ptr(w),
+                                               _ptr(counts), _ptr(loss), *_work(work), _stream(stream)))
+
+
+def ft_moe_balance_backward(d: ft_moe_balance, logits, valid, sel, w, counts, dw, dloss, dlogits, stream=None) -> int:
+    return _check(lib().ft_moe_balance_backward(ctypes.byref(d), _ptr(logits), _ptr(valid), _ptr(sel), _ptr(w),
+                                                _ptr(counts), _ptr(dw), _ptr(dloss), _ptr(dlogits), _stream(stream)))

@@ -1,0 +1,36 @@
+// Root-mean-square norm with the residual's addition: what its entry points and kernels share.
+#pragma once
+#include "common.h"
+#include "gmem.h"
+
+namespace ftmoe {
+
+struct NormForward {
+  const void *x, *residual, *weight;  // residual: null for 0
+  void *sum, *y;                      // null: not wanted, as the following
+  int8_t* codes;
+  float* scale;
+  int64_t ld_x, ld_residual, ld_sum, ld_y, ld_codes;
+  int32_t rows, cols;
+  double eps;
+};
+
+struct NormBackward {
+  const void *sum, *weight, *dy, *dsum;  // dsum: null for 0
+  void *dx, *dresidual;                  // null: not wanted
+  float* part;                           // [groups][cols]: sums of dy s r over each group's rows, null: not wanted
+  float* stats;                          // rows that no workgroup holds: r and mean(g s r) of each
+  int64_t ld_sum, ld_y, ld_residual, ld_x;
+  int32_t rows, cols, groups;
+  double eps;
+};
+
+// groups of rows whose weight gradients are summed apart
+int norm_groups(int32_t rows, int32_t cols);
+
+hipError_t launch_norm(int dtype, int residual_dtype, const NormForward& a, hipStream_t s);
+hipError_t launch_norm_backward(int dtype, int residual_dtype, const NormBackward& a, hipStream_t s);
+// dweight = the sum of the groups' parts, in order
+hipError_t launch_norm_join(int dtype, const float* part, int32_t groups, int32_t cols, void* dweight, hipStream_t s);
+
+}  // namespace ftmoe

@@ -1,0 +1,137 @@
+// Root-mean-square norm: rows of any width, element by element.
+//
+// Every row is read twice: for its sums, and for its values.
+#include "norm_device.h"
+
+namespace ftmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename X, typename R>
+__global__ __launch_bounds__(kThreads) void k_norm_any(NormForward a) {
+  __shared__ double lds[3 * kThreads / 64];
+  const int64_t row = blockIdx.x;
+  const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
+  const R* residual = a.residual ? static_cast<const R*>(a.residual) + row * a.ld_residual : nullptr;
+  const X* weight = static_cast<const X*>(a.weight);
+  R* sum = a.sum ? static_cast<R*>(a.sum) + row * a.ld_sum : nullptr;
+  X* y = a.y ? static_cast<X*>(a.y) + row * a.ld_y : nullptr;
+  int8_t* codes = a.codes ? a.codes + row * a.ld_codes : nullptr;
+  auto at = [&](int c) { return double(float(gload<X>(x + c))) + (residual ? double(float(gload<R>(residual + c))) : 0.0); };
+
+  NormSums t;
+  for (int c = threadIdx.x; c < a.cols; c += kThreads) t.add(at(c), double(float(gload<X>(weight + c))));
+  t.join<kThreads>(lds);
+  const NormRow r(t, a.cols, a.eps);
+  if (codes && threadIdx.x == 0) a.scale[row] = r.scale;
+  for (int c = threadIdx.x; c < a.cols; c += kThreads) {
+    const double s = at(c), sw = s * double(float(gload<X>(weight + c)));
+    if (sum) gstore<R>(sum + c, R(float(s)));
+    if (y) gstore<X>(y + c, X(float(sw * r.r)));
+    if (codes) gstore<int8_t>(codes + c, int8_t(r.code(sw)));
+  }
+}
+
+template <typename X, typename R>
+__global__ __launch_bounds__(kThreads) void k_norm_stats_any(NormBackward a) {
+  __shared__ double lds[2 * kThreads / 64];
+  const int64_t row = blockIdx.x;
+  const R* sum = static_cast<const R*>(a.sum) + row * a.ld_sum;
+  const X* dy = static_cast<const X*>(a.dy) + row * a.ld_y;
+  const X* weight = static_cast<const X*>(a.weight);
+  NormDots t;
+  for (int c = threadIdx.x; c < a.cols; c += kThreads)
+    t.add(float(gload<R>(sum + c)), float(gload<X>(dy + c)) * float(gload<X>(weight + c)));
+  t.join<kThreads>(lds);
+  const NormSlope k(t, a.cols, a.eps);
+  if (threadIdx.x == 0) {
+    a.stats[2 * row] = k.r;
+    a.stats[2 * row + 1] = k.m;
+  }
+}
+
+// a column for each thread, the rows of a group one after the other
+template <typename X, typename R>
+__global__ __launch_bounds__(kThreads) void k_norm_grad_any(NormBackward a) {
+  const int c = int(blockIdx.x) * kThreads + int(threadIdx.x);
+  if (c >= a.cols) return;
+  const float w = float(gload<X>(static_cast<const X*>(a.weight) + c));
+  float dw = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float s = float(gload<R>(static_cast<const R*>(a.sum) + row * a.ld_sum + c));
+    const float dy = float(gload<X>(static_cast<const X*>(a.dy) + row * a.ld_y + c));
+    const NormSlope k(a.stats[2 * row], a.stats[2 * row + 1]);
+    const float n = s * k.r;
+    float ds = k.ds(dy * w, n);
+    if (a.dsum) ds += float(gload<R>(static_cast<const R*>(a.dsum) + row * a.ld_residual + c));
+    if (a.dx) gstore<X>(static_cast<X*>(a.dx) + row * a.ld_x + c, X(ds));
+    if (a.dresidual) gstore<R>(static_cast<R*>(a.dresidual) + row * a.ld_residual + c, R(ds));
+    dw = fmaf(dy, n, dw);
+  }
+  if (a.part) a.part[int64_t(blockIdx.y) * a.cols + c] = dw;
+}
+
+template <typename X>
+__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int groups, int cols, X* dweight) {
+  __shared__ float lds[16][64];
+  const int lane = threadIdx.x & 63, g0 = threadIdx.x >> 6;
+  const int c = int(blockIdx.x) * 64 + lane;
+  float t = 0.f;
+  if (c < cols)
+    for (int g = g0; g < groups; g += 16) t += part[int64_t(g) * cols + c];
+  lds[g0][lane] = t;
+  __syncthreads();
+  if (g0 == 0 && c < cols) {
+    for (int g = 1; g < 16; ++g) t += lds[g][lane];
+    gstore<X>(dweight + c, X(t));
+  }
+}
+
+}  // namespace
+
+int norm_groups(int32_t rows, int32_t cols) { return rows < 64 ? rows : 64; }
+
+template <typename X, typename R>
+hipError_t launch(const NormForward& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_norm_any<X, R>), dim3(uint32_t(a.rows)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename X, typename R>
+hipError_t launch(const NormBackward& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_norm_stats_any<X, R>), dim3(uint32_t(a.rows)), dim3(kThreads), 0, s, a);
+  const uint32_t across = uint32_t((a.cols + kThreads - 1) / kThreads);
+  hipLaunchKernelGGL((k_norm_grad_any<X, R>), dim3(across, uint32_t(a.groups)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename A>
+hipError_t launch_types(int dtype, int residual_dtype, const A& a, hipStream_t s) {
+  const bool same = dtype == residual_dtype;
+  if (dtype == FT_DT_F32) return launch<float, float>(a, s);
+  if (dtype == FT_DT_F16) return same ? launch<_Float16, _Float16>(a, s) : launch<_Float16, float>(a, s);
+  return same ? launch<__bf16, __bf16>(a, s) : launch<__bf16, float>(a, s);
+}
+
+hipError_t launch_norm(int dtype, int residual_dtype, const NormForward& a, hipStream_t s) {
+  return launch_types(dtype, residual_dtype, a, s);
+}
+hipError_t launch_norm_backward(int dtype, int residual_dtype, const NormBackward& a, hipStream_t s) {
+  return launch_types(dtype, residual_dtype, a, s);
+}
+
+hipError_t launch_norm_join(int dtype, const float* part, int32_t groups, int32_t cols, void* dweight, hipStream_t s) {
+  const dim3 grid(uint32_t((cols + 63) / 64));
+  if (dtype == FT_DT_F32)
+    hipLaunchKernelGGL((k_norm_join<float>), grid, dim3(1024), 0, s, part, groups, cols, static_cast<float*>(dweight));
+  else if (dtype == FT_DT_F16)
+    hipLaunchKernelGGL((k_norm_join<_Float16>), grid, dim3(1024), 0, s, part, groups, cols,
+                       static_cast<_Float16*>(dweight));
+  else
+    hipLaunchKernelGGL((k_norm_join<__bf16>), grid, dim3(1024), 0, s, part, groups, cols, static_cast<__bf16*>(dweight));
+  return hipGetLastError();
+}
+
+}  // namespace ftmoe

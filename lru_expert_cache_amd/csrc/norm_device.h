@@ -1,0 +1,118 @@
+// Sums of a row and what follows from them.
+//
+// Forward: with p = s * weight, y = p r, r = 1 / sqrt(mean(s^2) + eps).  A
+// row's codes are rint(y / scale), and have to be those of the exact y: all of
+// it is formed in 64 bits (s of 16-bit addends and p are then exact), which
+// leaves one y in about 2^40 on the wrong side of a border between two codes,
+// and costs little: the 64-bit units keep up with the memory.
+//
+// Backward: with n = s r and g = dy weight, ds = r (g - n mean(g n)); only the
+// two sums are formed in 64 bits.
+#pragma once
+#include "norm.h"
+
+namespace ftmoe {
+
+__device__ __attribute__((always_inline)) inline double wave_add(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __attribute__((always_inline)) inline double wave_max(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+  return v;
+}
+
+struct NormSums {
+  double squares = 0.0, top = 0.0;
+  double odd = 0.0;  // NaN once a weighted value is infinite or NaN: a maximum alone would pass over it
+  __device__ __attribute__((always_inline)) inline void add(double s, double w) {
+    const double p = s * w;
+    squares = fma(s, s, squares);
+    top = fmax(top, fabs(p));
+    odd = fma(p, 0.0, odd);
+  }
+  // of all threads of the workgroup; lds: three numbers a wave
+  template <int THREADS>
+  __device__ __attribute__((always_inline)) inline void join(double* lds) {
+    squares = wave_add(squares);
+    top = wave_max(top);
+    odd = wave_add(odd);
+    if constexpr (THREADS > 64) {
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        lds[3 * wave] = squares;
+        lds[3 * wave + 1] = top;
+        lds[3 * wave + 2] = odd;
+      }
+      __syncthreads();
+      squares = top = odd = 0.0;
+#pragma unroll
+      for (int i = 0; i < THREADS / 64; ++i) {
+        squares += lds[3 * i];
+        top = fmax(top, lds[3 * i + 1]);
+        odd += lds[3 * i + 2];
+      }
+    }
+  }
+};
+
+struct NormRow {
+  double r;       // y = p r
+  float scale;
+  double q;       // code = rint(p q)
+  bool live;      // else every code is 0
+  __device__ __attribute__((always_inline)) inline NormRow(const NormSums& t, int cols, double eps) {
+    r = 1.0 / sqrt(t.squares / cols + eps);
+    const double top = t.top * r + t.odd;
+    const bool finite = top < __builtin_huge_val();  // not NaN either
+    scale = finite ? float(top / 127.0) : __uint_as_float(0x7FC00000u);
+    live = finite && scale > 0.f;
+    q = live ? r / double(scale) : 0.0;
+  }
+  // scales of few bits (next to the smallest fp32) leave quotients beyond 127
+  __device__ __attribute__((always_inline)) inline int code(double p) const {
+    return live ? min(max(int(rint(p * q)), -127), 127) : 0;
+  }
+};
+
+struct NormDots {
+  double squares = 0.0, dot = 0.0;
+  __device__ __attribute__((always_inline)) inline void add(float s, float g) {
+    squares = fma(double(s), double(s), squares);
+    dot = fma(double(s), double(g), dot);
+  }
+  template <int THREADS>
+  __device__ __attribute__((always_inline)) inline void join(double* lds) {
+    squares = wave_add(squares);
+    dot = wave_add(dot);
+    if constexpr (THREADS > 64) {
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        lds[2 * wave] = squares;
+        lds[2 * wave + 1] = dot;
+      }
+      __syncthreads();
+      squares = dot = 0.0;
+#pragma unroll
+      for (int i = 0; i < THREADS / 64; ++i) {
+        squares += lds[2 * i];
+        dot += lds[2 * i + 1];
+      }
+    }
+  }
+};
+
+struct NormSlope {
+  float r, m;  // of n = s r: ds = r (g - n m), m = mean(g n)
+  __device__ __attribute__((always_inline)) inline NormSlope(float r_, float m_) : r(r_), m(m_) {}
+  __device__ __attribute__((always_inline)) inline NormSlope(const NormDots& t, int cols, double eps) {
+    const double rr = 1.0 / sqrt(t.squares / cols + eps);
+    r = float(rr);
+    m = float(rr * (t.dot / cols));
+  }
+  __device__ __attribute__((always_inline)) inline float ds(float g, float n) const { return r * fmaf(-n, m, g); }
+};
+
+}  // namespace ftmoe
