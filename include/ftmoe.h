@@ -594,7 +594,7 @@ typedef struct {
   int32_t tokens;     /* T >= 0 */
   int32_t in, out;    /* K, N: 1..2^24 - 1 */
   int32_t rank;       /* R: 1..256; adapters of lower ranks are padded with zeros */
-  int32_t adapters;   /* n: 1..65536 */
+  int32_t adapters;   /* n: 1..4096 */
   int64_t ld_x, ld_a, ld_b, ld_base, ld_y;
 } ft_moe_adapters;
 int ft_moe_adapters_work(const ft_moe_adapters *d, int64_t *bytes);

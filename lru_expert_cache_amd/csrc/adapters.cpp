@@ -7,7 +7,7 @@ using namespace ftmoe;
 namespace {
 
 constexpr int32_t kMaxRank = 256;
-constexpr int32_t kMaxAdapters = 65536;
+constexpr int32_t kMaxAdapters = 4096;  // counters of the grouping, in LDS
 
 int check_adapters(const ft_moe_adapters* d, ft_moe_adapters& o) {
   if (!d) return bad("NULL description");
@@ -33,13 +33,24 @@ int check_adapters(const ft_moe_adapters* d, ft_moe_adapters& o) {
 }
 
 struct AdaptersWork {
+  AdapterPlan plan;
   float* h;
+  int32_t *order, *tile_count;
+  AdapterTile* tiles;
+  int32_t ld_h;
   int64_t bytes;
 };
 AdaptersWork adapters_work(const ft_moe_adapters& d, void* base) {
   AdaptersWork w{};
   Carve c{static_cast<uint8_t*>(base)};
-  w.h = reinterpret_cast<float*>(c.take(int64_t(d.tokens) * d.rank * 4));
+  w.plan = adapter_plan(d.tokens, d.in, d.out, d.rank, d.adapters);
+  w.ld_h = int32_t(up(d.rank, 4));
+  w.h = reinterpret_cast<float*>(c.take(int64_t(w.plan.parts) * d.tokens * w.ld_h * 4));
+  if (!w.plan.few) {
+    w.order = reinterpret_cast<int32_t*>(c.take(int64_t(d.tokens) * 4));
+    w.tile_count = reinterpret_cast<int32_t*>(c.take(int64_t(w.plan.windows) * 4));
+    w.tiles = reinterpret_cast<AdapterTile*>(c.take(int64_t(w.plan.windows) * w.plan.tile_cap * int64_t(sizeof(AdapterTile))));
+  }
   w.bytes = c.used;
   return w;
 }
@@ -103,7 +114,19 @@ int ft_moe_adapters_apply(const ft_moe_adapters* desc, const void* x, const int3
     l.rank = d.rank;
     l.count = d.adapters;
     l.in_place = in_place;
-    FT_HIP_CHECK(launch_adapters(d.dtype, d.base_dtype, d.out_dtype, l, s));
+    l.order = w.order;
+    l.tile_count = w.tile_count;
+    l.tiles = w.tiles;
+    l.ld_h = w.ld_h;
+    l.few = w.plan.few;
+    l.sub = w.plan.sub;
+    l.windows = w.plan.windows;
+    l.tile_cap = w.plan.tile_cap;
+    l.parts = w.plan.parts;
+    l.out_blocks = w.plan.out_blocks;
+    if (!l.few) FT_HIP_CHECK(launch_adapters_plan(l, s));
+    FT_HIP_CHECK(launch_adapters_in(d.dtype, l, s));
+    FT_HIP_CHECK(launch_adapters_out(d.dtype, d.base_dtype, d.out_dtype, l, s));
     return FT_OK;
   });
 }

@@ -1,9 +1,28 @@
 // Low-rank adapters beside a projection: what the entry points and kernels share.
+//
+// Two products: h = A x and y = base + scale B h.  Tokens of the same adapter
+// are brought together in tiles of 16, 32 or 64, so that its matrices are read
+// once for a tile and the products run on the matrix cores; a token's own
+// result does not depend on which others share its tile.  h goes through
+// memory in 32 bits: the first product is cut along K over as many workgroups
+// as fill the card, and the second adds their parts, in order.
 #pragma once
 #include "common.h"
 #include "gmem.h"
 
 namespace ftmoe {
+
+// Tokens are grouped within windows of this many.
+constexpr int32_t kAdapterWindow = 8192;
+// Up to this many, each wave finds its tile by itself; else a launch of its own writes down the tiles.
+constexpr int32_t kAdapterFew = 64;
+
+struct AdapterTile {
+  int32_t id;     // adapter, or their number for tokens that have none
+  int32_t first;  // in `order`
+  int32_t count;
+  int32_t unused;
+};
 
 struct Adapters {
   const void* x;
@@ -12,12 +31,26 @@ struct Adapters {
   const float* scale;  // null: 1
   const void* base;    // null: 0
   void* y;
-  float* h;            // [T][R]: A x
+  float* h;            // [parts][T][ld_h]: sums over each part of K
+  int32_t* order;      // [T]: tokens of each tile next to each other
+  AdapterTile* tiles;  // [windows][tile_cap]
+  int32_t* tile_count; // [windows]
   int64_t ld_x, ld_a, ld_b, ld_base, ld_y;
-  int32_t tokens, in, out, rank, count;
-  bool in_place;       // y is base
+  int32_t tokens, in, out, rank, count, ld_h;
+  int32_t few, sub;    // tiles found by each wave; groups of 16 tokens in a tile
+  int32_t windows, tile_cap, parts;
+  int32_t out_blocks;  // 128-column blocks of y that a workgroup of the second product takes
+  bool in_place;       // y is base: tokens without an adapter are left out
 };
 
-hipError_t launch_adapters(int dtype, int base_dtype, int out_dtype, const Adapters& a, hipStream_t s);
+// How a call is cut: a rule on sizes alone.
+struct AdapterPlan {
+  int32_t few, sub, windows, tile_cap, parts, out_blocks;
+};
+AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count);
+
+hipError_t launch_adapters_plan(const Adapters& l, hipStream_t s);
+hipError_t launch_adapters_in(int dtype, const Adapters& l, hipStream_t s);
+hipError_t launch_adapters_out(int dtype, int base_dtype, int out_dtype, const Adapters& l, hipStream_t s);
 
 }  // namespace ftmoe

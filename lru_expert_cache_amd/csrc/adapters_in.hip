@@ -1,0 +1,218 @@
+// Adapters: tiles of tokens, and the first product, h = A x.
+#include "adapters_device.h"
+
+namespace ftmoe {
+
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kPlanThreads = 1024, kEach = kAdapterWindow / kPlanThreads;
+
+// The tiles of a window: tokens are counted by adapter (those without one last),
+// and placed at their adapter's offset.  Which place within it a token gets
+// depends on the order of the atomics; its result does not.
+__global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
+  extern __shared__ int lds[];
+  __shared__ uint32_t sums[kPlanThreads / 64];
+  int* hist = lds;                                               // [count + 1]
+  uint32_t* before = reinterpret_cast<uint32_t*>(lds) + l.count + 1;  // [count + 1]: tokens, and tiles above
+  const int tid = threadIdx.x, lane = tid & 63, groups = l.count + 1, size = 16 * l.sub;
+  const int64_t t0 = int64_t(blockIdx.x) * kAdapterWindow;
+  const int tokens = int(min(int64_t(kAdapterWindow), l.tokens - t0));
+  for (int g = tid; g < groups; g += kPlanThreads) hist[g] = 0;
+  int group[kEach], place[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int t = kEach * tid + i;
+    group[i] = -1;
+    if (t < tokens) {
+      const int id = gload<int32_t>(l.ids + t0 + t);
+      group[i] = uint32_t(id) < uint32_t(l.count) ? id : l.in_place ? -1 : l.count;
+    }
+  }
+  __syncthreads();
+  // one addition for each run of the same adapter
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    place[i] = 0;
+    if (i > 0 && group[i] == group[i - 1]) {
+      place[i] = place[i - 1] + 1;
+    } else if (group[i] >= 0) {
+      int run = 1;
+      bool on = true;
+#pragma unroll
+      for (int j = i + 1; j < kEach; ++j) {
+        on = on && group[j] == group[i];
+        run += on;
+      }
+      place[i] = atomicAdd(&hist[group[i]], run);
+    }
+  }
+  __syncthreads();
+  // a window's tokens and tiles fit 16 bits each
+  const int each = (groups + kPlanThreads - 1) / kPlanThreads;
+  uint32_t own = 0;
+  for (int j = 0; j < each; ++j) {
+    const int g = tid * each + j, c = g < groups ? hist[g] : 0;
+    own += uint32_t(c) + (uint32_t((c + size - 1) / size) << 16);
+  }
+  uint32_t sum = own;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(sum, o);
+    sum += lane >= o ? v : 0;
+  }
+  if (lane == 63) sums[tid >> 6] = sum;
+  __syncthreads();
+  uint32_t at = sum - own;
+  for (int i = 0; i < tid >> 6; ++i) at += sums[i];
+  if (tid == kPlanThreads - 1) l.tile_count[blockIdx.x] = int((at + own) >> 16);
+  for (int j = 0; j < each; ++j) {
+    const int g = tid * each + j;
+    if (g >= groups) break;
+    before[g] = at;
+    const int c = hist[g];
+    at += uint32_t(c) + (uint32_t((c + size - 1) / size) << 16);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int g = group[i];
+    if (g < 0) continue;
+    const uint32_t b = before[g];
+    const int first = int(t0) + int(b & 0xFFFF) + place[i];
+    l.order[first] = int(t0) + kEach * tid + i;
+    if (place[i] % size == 0)
+      l.tiles[int64_t(blockIdx.x) * l.tile_cap + (b >> 16) + place[i] / size] = {g, first, min(size, hist[g] - place[i]), 0};
+  }
+}
+
+// A workgroup takes a tile of tokens, up to 64 rows of its adapter's A and a
+// part of K, which its four waves share; their sums meet in LDS.  A matrix
+// instruction takes 16 rows of A and 16 tokens, 16 bytes of each row a lane.
+template <typename D, int SUB, int ROWS>
+__global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
+  typedef typename D::elem E;
+  __shared__ floatx4 lds[kWaves][SUB * ROWS][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
+  const int blocks = (l.rank + 16 * ROWS - 1) / (16 * ROWS);
+  const int64_t total = int64_t(l.windows) * l.tile_cap * blocks * l.parts;
+  for (int64_t flat = blockIdx.x; flat < total; flat += gridDim.x) {
+    const int part = int(flat % l.parts), block = int(flat / l.parts % blocks);
+    const TileTokens<SUB> t = find_tile<SUB>(l, flat / l.parts / blocks);
+    if (!t.live || t.id == l.count) continue;
+    const E* x[SUB];
+    const E* a[ROWS];
+#pragma unroll
+    for (int m = 0; m < SUB; ++m) x[m] = static_cast<const E*>(l.x) + int64_t(t.token[m]) * l.ld_x;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const int r = min(16 * (block * ROWS + j) + (lane & 15), l.rank - 1);
+      a[j] = static_cast<const E*>(l.a) + (int64_t(t.id) * l.rank + r) * l.ld_a;
+    }
+    // K in units of 64 elements: two instructions, 128 bytes of a row
+    const int64_t units = (l.in + 63) / 64;
+    const int64_t p0 = units * part / l.parts, p1 = units * (part + 1) / l.parts;
+    const int u0 = int(p0 + (p1 - p0) * wave / kWaves);
+    int u1 = int(p0 + (p1 - p0) * (wave + 1) / kWaves);
+    const bool tail = u1 == units && u1 > u0 && l.in % 64 != 0;
+    if (tail) --u1;
+    floatx4 acc[SUB][ROWS] = {};
+    auto step = [&](const u32x4(&xv)[SUB], const u32x4(&av)[ROWS]) {
+#pragma unroll
+      for (int m = 0; m < SUB; ++m)
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) acc[m][j] = D::mfma16(av[j], xv[m], acc[m][j]);
+    };
+    typedef u32x4 __attribute__((aligned(1))) any;
+    u32x4 xv[2][SUB], av[2][ROWS];
+    auto fetch = [&](int u) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 64 * u + 32 * h + 8 * q;
+#pragma unroll
+        for (int m = 0; m < SUB; ++m) xv[h][m] = gload<any>(x[m] + k);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) av[h][j] = gload<any>(a[j] + k);
+      }
+    };
+    if (u0 < u1) fetch(u0);
+    for (int u = u0; u < u1; ++u) {
+      u32x4 xn[2][SUB], an[2][ROWS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int m = 0; m < SUB; ++m) xn[h][m] = xv[h][m];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) an[h][j] = av[h][j];
+      }
+      if (u + 1 < u1) fetch(u + 1);
+      step(xn[0], an[0]);
+      step(xn[1], an[1]);
+    }
+    if (tail) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = 8 * u1 + 4 * h + q;
+#pragma unroll
+        for (int m = 0; m < SUB; ++m) xv[h][m] = row_piece<E, true>(x[m], c, l.in);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) av[h][j] = row_piece<E, false>(a[j], c, l.in);
+        step(xv[h], av[h]);
+      }
+    }
+    __syncthreads();  // the last tile's sums have been read
+#pragma unroll
+    for (int m = 0; m < SUB; ++m)
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) lds[wave][m * ROWS + j][lane] = acc[m][j];
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < SUB; ++m) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        if ((m * ROWS + j) % kWaves != wave) continue;
+        floatx4 v = lds[0][m * ROWS + j][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += lds[w][m * ROWS + j][lane];
+        const int r = 16 * (block * ROWS + j) + 4 * q;
+        float* h = l.h + (int64_t(part) * l.tokens + t.token[m]) * l.ld_h + r;
+        // h's rows hold whole groups of four
+        if (16 * m + (lane & 15) < t.count && r < l.ld_h) gstore<floatx4>(h, v);
+      }
+    }
+  }
+}
+
+template <typename D, int SUB, int ROWS>
+hipError_t launch(const Adapters& l, hipStream_t s) {
+  const int64_t blocks = (l.rank + 16 * ROWS - 1) / (16 * ROWS);
+  const int64_t total = int64_t(l.windows) * l.tile_cap * blocks * l.parts;
+  hipLaunchKernelGGL((k_adapters_in<D, SUB, ROWS>), dim3(uint32_t(total < (1 << 22) ? total : (1 << 22))), dim3(kThreads), 0,
+                     s, l);
+  return hipGetLastError();
+}
+template <typename D, int SUB>
+hipError_t launch_rank(const Adapters& l, hipStream_t s) {
+  if (l.rank <= 16) return launch<D, SUB, 1>(l, s);
+  if (l.rank <= 32) return launch<D, SUB, 2>(l, s);
+  return launch<D, SUB, 4>(l, s);
+}
+template <typename D>
+hipError_t launch_sub(const Adapters& l, hipStream_t s) {
+  if (l.sub == 1) return launch_rank<D, 1>(l, s);
+  if (l.sub == 2) return launch_rank<D, 2>(l, s);
+  return launch_rank<D, 4>(l, s);
+}
+
+}  // namespace
+
+hipError_t launch_adapters_plan(const Adapters& l, hipStream_t s) {
+  hipLaunchKernelGGL(k_adapters_plan, dim3(uint32_t(l.windows)), dim3(kPlanThreads), size_t(l.count + 1) * 8, s, l);
+  return hipGetLastError();
+}
+hipError_t launch_adapters_in(int dtype, const Adapters& l, hipStream_t s) {
+  return dtype == FT_DT_F16 ? launch_sub<DenseF16>(l, s) : launch_sub<DenseBf16>(l, s);
+}
+
+}  // namespace ftmoe

@@ -71,8 +71,8 @@ def test_bad_norms(kw):
 @pytest.mark.parametrize("kw", [dict(dtype=ft.FT_DT_F32), dict(dtype=0), dict(out_dtype=ft.FT_DT_F16), dict(base_dtype=ft.FT_DT_F16),
                                 dict(out_dtype=ft.FT_DT_F32, base_dtype=ft.FT_DT_BF16), dict(tokens=-1), dict(tokens=1 << 24),
                                 dict(in_features=0), dict(out_features=0), dict(rank=0), dict(rank=257), dict(adapters=0),
-                                dict(adapters=65537), dict(ld_x=31), dict(ld_a=31), dict(ld_b=7), dict(ld_base=47),
-                                dict(ld_y=1 << 32), dict(out_features=(1 << 24) - 1, adapters=65536, ld_b=(1 << 32) - 1)])
+                                dict(adapters=4097), dict(ld_x=31), dict(ld_a=31), dict(ld_b=7), dict(ld_base=47),
+                                dict(ld_y=1 << 32), dict(out_features=(1 << 24) - 1, adapters=4096, ld_b=(1 << 32) - 1)])
 def test_bad_adapters(kw):
     d = _adapters(**kw)
     _refused(ft.ft_moe_adapters_work, d)
