@@ -28,6 +28,11 @@ struct NormBackward {
 // groups of rows whose weight gradients are summed apart
 int norm_groups(int32_t rows, int32_t cols);
 
+// norm_rows.hip: rows that a workgroup's registers hold; norm_any.hip: all others
+bool norm_rows(int32_t cols);
+hipError_t launch_norm_rows(int dtype, int residual_dtype, const NormForward& a, hipStream_t s);
+hipError_t launch_norm_rows(int dtype, int residual_dtype, const NormBackward& a, hipStream_t s);
+
 hipError_t launch_norm(int dtype, int residual_dtype, const NormForward& a, hipStream_t s);
 hipError_t launch_norm_backward(int dtype, int residual_dtype, const NormBackward& a, hipStream_t s);
 // dweight = the sum of the groups' parts, in order

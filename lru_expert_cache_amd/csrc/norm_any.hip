@@ -89,10 +89,6 @@ __global__ __launch_bounds__(1024) void k_norm_join(const float* part, int group
   }
 }
 
-}  // namespace
-
-int norm_groups(int32_t rows, int32_t cols) { return rows < 64 ? rows : 64; }
-
 template <typename X, typename R>
 hipError_t launch(const NormForward& a, hipStream_t s) {
   hipLaunchKernelGGL((k_norm_any<X, R>), dim3(uint32_t(a.rows)), dim3(kThreads), 0, s, a);
@@ -115,11 +111,18 @@ hipError_t launch_types(int dtype, int residual_dtype, const A& a, hipStream_t s
   return same ? launch<__bf16, __bf16>(a, s) : launch<__bf16, float>(a, s);
 }
 
+}  // namespace
+
+int norm_groups(int32_t rows, int32_t cols) {
+  const int32_t most = norm_rows(cols) ? 512 : 64;
+  return rows < most ? rows : most;
+}
+
 hipError_t launch_norm(int dtype, int residual_dtype, const NormForward& a, hipStream_t s) {
-  return launch_types(dtype, residual_dtype, a, s);
+  return norm_rows(a.cols) ? launch_norm_rows(dtype, residual_dtype, a, s) : launch_types(dtype, residual_dtype, a, s);
 }
 hipError_t launch_norm_backward(int dtype, int residual_dtype, const NormBackward& a, hipStream_t s) {
-  return launch_types(dtype, residual_dtype, a, s);
+  return norm_rows(a.cols) ? launch_norm_rows(dtype, residual_dtype, a, s) : launch_types(dtype, residual_dtype, a, s);
 }
 
 hipError_t launch_norm_join(int dtype, const float* part, int32_t groups, int32_t cols, void* dweight, hipStream_t s) {
