@@ -25,16 +25,19 @@ int check_balance(const ft_moe_balance* d, ft_moe_balance& o) {
 
 struct BalanceWork {
   float* p;
-  int32_t *c, *v;
+  int32_t *c, *v, *arrived;
+  double* share;
   int64_t bytes;
 };
 BalanceWork balance_work(const ft_moe_balance& d, void* base) {
   BalanceWork w{};
   Carve c{static_cast<uint8_t*>(base)};
   const int64_t groups = balance_groups(d.tokens);
-  w.p = reinterpret_cast<float*>(c.take(groups * d.experts * 4));
-  w.c = reinterpret_cast<int32_t*>(c.take(groups * d.experts * 4));
+  w.p = reinterpret_cast<float*>(c.take(groups * balance_width(d.experts) * 4));
+  w.c = reinterpret_cast<int32_t*>(c.take(groups * balance_width(d.experts) * 4));
   w.v = reinterpret_cast<int32_t*>(c.take(groups * 4));
+  w.share = reinterpret_cast<double*>(c.take(kMaxExperts / 16 * 8));
+  w.arrived = reinterpret_cast<int32_t*>(c.take(4));
   w.bytes = c.used;
   return w;
 }
@@ -87,6 +90,9 @@ int ft_moe_balance_forward(const ft_moe_balance* desc, const void* logits, const
     a.part_p = k.p;
     a.part_c = k.c;
     a.part_v = k.v;
+    a.share = k.share;
+    a.arrived = k.arrived;
+    a.ld_part = balance_width(d.experts);
     a.ld = d.ld_logits;
     a.tokens = d.tokens;
     a.experts = d.experts;

@@ -12,11 +12,13 @@ struct BalanceForward {
   float* w;
   int32_t* counts;  // [E + 1]
   float* loss;
-  // by workgroup: sums of p [groups][E], choices [groups][E], tokens counted [groups]
+  // by workgroup: sums of p and choices [groups][ld_part], tokens counted [groups]
   float* part_p;
   int32_t *part_c, *part_v;
+  double* share;     // of the loss, without its factor: of 16 experts each
+  int32_t* arrived;  // workgroups that have written theirs
   int64_t ld;
-  int32_t tokens, experts, top_k, groups;
+  int32_t tokens, experts, top_k, groups, ld_part;
   float weight;
 };
 
@@ -34,6 +36,8 @@ struct BalanceBackward {
 };
 
 int balance_groups(int32_t tokens);
+// experts' places in a part: whole lanes of a wave
+inline int balance_width(int32_t experts) { return experts <= 64 ? 64 : experts <= 128 ? 128 : experts <= 256 ? 256 : 512; }
 hipError_t launch_balance(int dtype, const BalanceForward& a, hipStream_t s);
 hipError_t launch_balance_backward(int dtype, const BalanceBackward& a, hipStream_t s);
 

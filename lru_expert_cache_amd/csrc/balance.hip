@@ -1,8 +1,11 @@
 // A router's balance: choice, weights, counts and loss of a batch of tokens, and the gradient of the logits.
 //
-// A wave takes a token at a time; lane l holds experts l, l + 64, ...  The sums
-// over the tokens are kept by each lane for its experts, added up within the
-// workgroup, and over the workgroups, in order, by a second kernel.
+// A wave takes a token at a time; lane l holds experts l, l + 64, ...  The k
+// largest are found in k rounds of a maximum over the wave: logits are taken
+// as integers of the same order, and reduced with DPP (no LDS round trips);
+// which expert it is follows from ballots, one for each of a lane's experts.
+// The sums over the tokens are kept by each lane for its experts, added up
+// within the workgroup, and over the workgroups, in order, by a second kernel.
 #include "balance.h"
 
 namespace ftmoe {
@@ -11,16 +14,43 @@ namespace {
 
 constexpr int kWaves = 16;
 constexpr float kInf = __builtin_huge_valf();
+constexpr int kNever = int(0x80000000u);  // below every logit that can be chosen
 
-__device__ __attribute__((always_inline)) inline float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+// lanes' partners within a row of 16, then lane 15 of a row to the next, lane 31 to the upper half: lane 63 has all
+template <int CTRL, int ROWS = 0xF>
+__device__ __attribute__((always_inline)) inline int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
-__device__ __attribute__((always_inline)) inline float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+__device__ __attribute__((always_inline)) inline int wave_top(int v) {
+  v = max(v, dpp<0xB1>(v, v));
+  v = max(v, dpp<0x4E>(v, v));
+  v = max(v, dpp<0x141>(v, v));
+  v = max(v, dpp<0x140>(v, v));
+  v = max(v, dpp<0x142, 0xA>(v, v));
+  v = max(v, dpp<0x143, 0xC>(v, v));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __attribute__((always_inline)) inline float wave_sum(float x) {
+  auto add = [](float a, int b) { return a + __int_as_float(b); };
+  x = add(x, dpp<0xB1>(0, __float_as_int(x)));
+  x = add(x, dpp<0x4E>(0, __float_as_int(x)));
+  x = add(x, dpp<0x141>(0, __float_as_int(x)));
+  x = add(x, dpp<0x140>(0, __float_as_int(x)));
+  x = add(x, dpp<0x142, 0xA>(0, __float_as_int(x)));
+  x = add(x, dpp<0x143, 0xC>(0, __float_as_int(x)));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// Logits as integers of their order (-0 as 0); -inf and NaN, which are never chosen, below all.
+__device__ __attribute__((always_inline)) inline int order_of(float z) {
+  const int b = __float_as_int(z + 0.f), k = b < 0 ? b ^ 0x7FFFFFFF : b;
+  return z > -kInf ? k : kNever;
+}
+__device__ __attribute__((always_inline)) inline float logit_of(int k) { return __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k); }
+
+// e^d, d <= 0: the product with log2 e and the hardware's exp2 round once each
+__device__ __attribute__((always_inline)) inline float exp_of(float d) {
+  return __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
 }
 
 // A token's logits, J for each lane; -inf beyond the last.
@@ -41,16 +71,21 @@ struct Logits {
     for (int j = 0; j < J; ++j) any = any || !(z[j] == -kInf);
     return __any(any);
   }
-  // softmax; 0 beyond the last expert
-  __device__ __attribute__((always_inline)) inline void softmax(float (&p)[J], int experts, int lane) const {
-    float top = -kInf;
+  __device__ __attribute__((always_inline)) inline int top(int (&key)[J]) const {
+    int best = kNever;
 #pragma unroll
-    for (int j = 0; j < J; ++j) top = fmaxf(top, z[j]);
-    top = wave_max(top);
+    for (int j = 0; j < J; ++j) {
+      key[j] = order_of(z[j]);
+      best = max(best, key[j]);
+    }
+    return wave_top(best);
+  }
+  // softmax, the largest logit known; 0 beyond the last expert
+  __device__ __attribute__((always_inline)) inline void softmax(float (&p)[J], float top, int experts, int lane) const {
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      p[j] = lane + 64 * j < experts ? expf(z[j] - top) : 0.f;
+      p[j] = lane + 64 * j < experts ? exp_of(z[j] - top) : 0.f;
       sum += p[j];
     }
     sum = 1.f / wave_sum(sum);
@@ -66,45 +101,59 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   __shared__ int lds_v;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int e = threadIdx.x; e < 64 * J; e += 64 * kWaves) lds_c[e] = 0;
-  if (threadIdx.x == 0) lds_v = 0;
+  if (threadIdx.x == 0) {
+    lds_v = 0;
+    if (blockIdx.x == 0) *a.arrived = 0;  // of the next kernel's workgroups
+  }
   __syncthreads();
   float sums[J] = {};
   int counted = 0;
-  for (int64_t t = int64_t(blockIdx.x) * kWaves + wave; t < a.tokens; t += int64_t(a.groups) * kWaves) {
-    Logits<X, J> l;
-    l.load(static_cast<const X*>(a.logits) + t * a.ld, a.experts, lane);
-    const bool on = (!a.valid || gload<uint8_t>(a.valid + t)) && l.some();
-    int mine = -1;          // lane i: the choice of rank i, and its logit
-    float mine_z = -kInf, first = 0.f;
+  const int64_t step = int64_t(a.groups) * kWaves;
+  Logits<X, J> next;
+  bool next_on = true;
+  auto fetch = [&](int64_t t) {
+    next.load(static_cast<const X*>(a.logits) + t * a.ld, a.experts, lane);
+    next_on = !a.valid || gload<uint8_t>(a.valid + t);
+  };
+  int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+  if (t < a.tokens) fetch(t);
+  for (; t < a.tokens; t += step) {
+    const Logits<X, J> l = next;
+    const bool on = next_on && l.some();
+    if (t + step < a.tokens) fetch(t + step);
+    int mine = -1, mine_key = kNever, first = kNever;  // lane i: the choice of rank i, and its logit
     if (on) {
       ++counted;
+      int key[J];
+      first = l.top(key);
       float p[J];
-      l.softmax(p, a.experts, lane);
+      l.softmax(p, logit_of(first), a.experts, lane);
 #pragma unroll
       for (int j = 0; j < J; ++j) sums[j] += p[j];
-      for (int i = 0; i < a.top_k; ++i) {
-        float best = -kInf;
+      int best = first;
+      for (int i = 0; i < a.top_k && best != kNever; ++i) {
+        // the lowest expert of that logit
+        int at = 0;
+        bool found = false;
 #pragma unroll
-        for (int j = 0; j < J; ++j) best = fmaxf(best, l.z[j]);  // NaN is passed over
-        best = wave_max(best);
-        if (best == -kInf) break;
-        int at = 0x7FFFFFFF;
-#pragma unroll
-        for (int j = J - 1; j >= 0; --j) at = l.z[j] == best ? lane + 64 * j : at;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) at = min(at, __shfl_xor(at, o));
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (lane + 64 * j == at) l.z[j] = -kInf;
-        if (i == 0) first = best;
-        if (lane == i) {
-          mine = at;
-          mine_z = best;
+        for (int j = 0; j < J; ++j) {
+          const uint64_t same = __ballot(key[j] == best);
+          const bool here = !found && same != 0;
+          const int src = here ? __builtin_ctzll(same) : 64;
+          at = here ? src + 64 * j : at;
+          key[j] = lane == src ? kNever : key[j];
+          found = found || here;
         }
+        mine = lane == i ? at : mine;
+        mine_key = lane == i ? best : mine_key;
+        best = key[0];
+#pragma unroll
+        for (int j = 1; j < J; ++j) best = max(best, key[j]);
+        best = wave_top(best);
       }
       if (mine >= 0) atomicAdd(&lds_c[mine], 1);
     }
-    const float ex = mine >= 0 ? expf(mine_z - first) : 0.f;
+    const float ex = mine >= 0 ? exp_of(logit_of(mine_key) - logit_of(first)) : 0.f;
     const float sum = wave_sum(ex);
     if (lane < a.top_k) {
       a.sel[t * a.top_k + lane] = mine;
@@ -115,36 +164,82 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   for (int j = 0; j < J; ++j) lds_p[wave][lane + 64 * j] = sums[j];
   if (lane == 0) atomicAdd(&lds_v, counted);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += 64 * kWaves) {
+  for (int e = threadIdx.x; e < 64 * J; e += 64 * kWaves) {
     float s = 0.f;
     for (int i = 0; i < kWaves; ++i) s += lds_p[i][e];
-    a.part_p[int64_t(blockIdx.x) * a.experts + e] = s;
-    a.part_c[int64_t(blockIdx.x) * a.experts + e] = lds_c[e];
+    a.part_p[int64_t(blockIdx.x) * a.ld_part + e] = s;
+    a.part_c[int64_t(blockIdx.x) * a.ld_part + e] = lds_c[e];
   }
   if (threadIdx.x == 0) a.part_v[blockIdx.x] = lds_v;
 }
 
-// one workgroup
-__global__ __launch_bounds__(512) void k_balance_join(BalanceForward a) {
-  __shared__ double lds[512];
-  const int e = threadIdx.x;
-  double p = 0.0;
-  int c = 0, v = 0;
-  if (e < a.experts) {
-    for (int g = 0; g < a.groups; ++g) {
-      p += double(a.part_p[int64_t(g) * a.experts + e]);
-      c += a.part_c[int64_t(g) * a.experts + e];
+// Sixteen experts a workgroup: four lanes have four each, 64 groups of lanes
+// every 64th part.  The workgroup that arrives last adds up the loss: the
+// others' shares of it are written past the XCD's own cache, and the counter
+// is touched after them.
+constexpr int kJoin = 256;
+__global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
+  typedef float floatx4 __attribute__((ext_vector_type(4)));
+  typedef int intx4 __attribute__((ext_vector_type(4)));
+  __shared__ double lds_p[kJoin / 64][16];
+  __shared__ int lds_c[kJoin / 64][16];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = 4 * (tid & 3);
+  const int e0 = 16 * int(blockIdx.x);
+  double p[4] = {};
+  int c[4] = {};
+#pragma unroll 4
+  for (int g = tid >> 2; g < a.groups; g += kJoin / 4) {
+    const floatx4 pv = gload<floatx4>(a.part_p + int64_t(g) * a.ld_part + e0 + col);
+    const intx4 cv = gload<intx4>(a.part_c + int64_t(g) * a.ld_part + e0 + col);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] += double(pv[i]);
+      c[i] += cv[i];
     }
-    a.counts[e] = c;
   }
-  lds[e] = p * c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int o = 4; o < 64; o <<= 1) {
+      p[i] += __shfl_xor(p[i], o);
+      c[i] += __shfl_xor(c[i], o);
+    }
+    if (lane < 4) {
+      lds_p[wave][col + i] = p[i];
+      lds_c[wave][col + i] = c[i];
+    }
+  }
   __syncthreads();
-  if (e == 0) {
-    for (int g = 0; g < a.groups; ++g) v += a.part_v[g];
-    a.counts[a.experts] = v;
-    double sum = 0.0;
-    for (int i = 0; i < a.experts; ++i) sum += lds[i];
+  if (tid < 16) {
+    double ps = 0.0;
+    int cs = 0;
+    for (int w = 0; w < kJoin / 64; ++w) {
+      ps += lds_p[w][tid];
+      cs += lds_c[w][tid];
+    }
+    if (e0 + tid < a.experts) a.counts[e0 + tid] = cs;
+    double share = ps * cs;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) share += __shfl_xor(share, o);
+    if (tid == 0) {
+      __hip_atomic_store(a.share + blockIdx.x, share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(a.arrived, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == int(gridDim.x) - 1;
+    }
+  }
+  __syncthreads();
+  if (!last || wave != 0) return;
+  int v = 0;
+  for (int g = lane; g < a.groups; g += 64) v += a.part_v[g];
+  double sum = lane < int(gridDim.x) ? __hip_atomic_load(a.share + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    v += __shfl_xor(v, o);
+    sum += __shfl_xor(sum, o);
+  }
+  if (lane == 0) {
     const double n = double(v);
+    a.counts[a.experts] = v;
     a.loss[0] = v ? float(double(a.weight) * a.experts / (a.top_k * n * n) * sum) : 0.f;
   }
 }
@@ -165,24 +260,41 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
     }
   }
   const float dloss = a.dloss ? a.dloss[0] : 1.f;
-  for (int64_t t = int64_t(blockIdx.x) * kWaves + wave; t < a.tokens; t += int64_t(gridDim.x) * kWaves) {
-    Logits<X, J> l;
-    l.load(static_cast<const X*>(a.logits) + t * a.ld, a.experts, lane);
+  const int64_t step = int64_t(gridDim.x) * kWaves;
+  Logits<X, J> next;
+  bool next_on = true;
+  int next_sel = -1;
+  float next_w = 0.f, next_dw = 0.f;
+  auto fetch = [&](int64_t t) {
+    next.load(static_cast<const X*>(a.logits) + t * a.ld, a.experts, lane);
+    next_on = !a.valid || gload<uint8_t>(a.valid + t);
+    if (a.dw && lane < a.top_k) {
+      next_sel = gload<int>(a.sel + t * a.top_k + lane);
+      next_w = gload<float>(a.w + t * a.top_k + lane);
+      next_dw = gload<float>(a.dw + t * a.top_k + lane);
+    }
+  };
+  int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+  if (t < a.tokens) fetch(t);
+  for (; t < a.tokens; t += step) {
+    const Logits<X, J> l = next;
+    const bool on = next_on && l.some();
+    const int i = next_sel;
+    const bool chosen = uint32_t(i) < uint32_t(a.experts);
+    const float w = chosen ? next_w : 0.f, dw = chosen ? next_dw : 0.f;
+    if (t + step < a.tokens) fetch(t + step);
     X* dz = static_cast<X*>(a.dlogits) + t * a.ld;
-    const bool on = (!a.valid || gload<uint8_t>(a.valid + t)) && l.some();
     float d[J] = {};
     if (on) {
+      int key[J];
       float p[J], sum = 0.f;
-      l.softmax(p, a.experts, lane);
+      l.softmax(p, logit_of(l.top(key)), a.experts, lane);
 #pragma unroll
       for (int j = 0; j < J; ++j) sum = fmaf(p[j], c[j], sum);
       sum = wave_sum(sum);
 #pragma unroll
       for (int j = 0; j < J; ++j) d[j] = dloss * p[j] * (c[j] - sum);
       if (a.dw) {
-        const int i = lane < a.top_k ? a.sel[t * a.top_k + lane] : -1;
-        const bool chosen = uint32_t(i) < uint32_t(a.experts);
-        const float w = chosen ? a.w[t * a.top_k + lane] : 0.f, dw = chosen ? a.dw[t * a.top_k + lane] : 0.f;
         const float mean = wave_sum(w * dw);
         if (chosen) atomicAdd(&lds[wave][i], w * (dw - mean));  // the same expert twice counts twice
         __builtin_amdgcn_wave_barrier();
@@ -201,8 +313,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
 
 template <typename X, int J>
 hipError_t launch(const BalanceForward& a, hipStream_t s) {
+  if (a.ld_part != 64 * J) return hipErrorInvalidValue;
   hipLaunchKernelGGL((k_balance<X, J>), dim3(uint32_t(a.groups)), dim3(64 * kWaves), 0, s, a);
-  hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(512), 0, s, a);
+  hipLaunchKernelGGL(k_balance_join, dim3(uint32_t((a.experts + 15) / 16)), dim3(kJoin), 0, s, a);
   return hipGetLastError();
 }
 template <typename X, int J>
@@ -229,7 +342,7 @@ hipError_t launch_type(int dtype, const A& a, hipStream_t s) {
 
 int balance_groups(int32_t tokens) {
   const int32_t g = (tokens + kWaves - 1) / kWaves;
-  return g < 1 ? 1 : g < 256 ? g : 256;
+  return g < 1 ? 1 : g < 512 ? g : 512;
 }
 
 hipError_t launch_balance(int dtype, const BalanceForward& a, hipStream_t s) { return launch_type(dtype, a, s); }
