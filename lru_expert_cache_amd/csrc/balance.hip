@@ -1,11 +1,13 @@
 // A router's balance: choice, weights, counts and loss of a batch of tokens, and the gradient of the logits.
 //
-// A wave takes a token at a time; lane l holds experts l, l + 64, ...  The k
-// largest are found in k rounds of a maximum over the wave: logits are taken
-// as integers of the same order, and reduced with DPP (no LDS round trips);
-// which expert it is follows from ballots, one for each of a lane's experts.
+// A wave takes a token at a time; lane l holds experts l, l + 64, ..., sorted.
+// The k largest are found in k rounds: the maximum over the lanes' first ones
+// (as integers of the logits' order, reduced with DPP: no LDS round trips),
+// the lane that has it from a ballot, and that lane moves up its next.
 // The sums over the tokens are kept by each lane for its experts, added up
 // within the workgroup, and over the workgroups, in order, by a second kernel.
+#include <type_traits>
+
 #include "balance.h"
 
 namespace ftmoe {
@@ -14,39 +16,44 @@ namespace {
 
 constexpr int kWaves = 16;
 constexpr float kInf = __builtin_huge_valf();
-constexpr int kNever = int(0x80000000u);  // below every logit that can be chosen
+constexpr uint32_t kNever = 0;  // below every logit that can be chosen
 
 // lanes' partners within a row of 16, then lane 15 of a row to the next, lane 31 to the upper half: lane 63 has all
 template <int CTRL, int ROWS = 0xF>
-__device__ __attribute__((always_inline)) inline int dpp(int old, int v) {
-  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
+__device__ __attribute__((always_inline)) inline uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
 }
-__device__ __attribute__((always_inline)) inline int wave_top(int v) {
-  v = max(v, dpp<0xB1>(v, v));
-  v = max(v, dpp<0x4E>(v, v));
-  v = max(v, dpp<0x141>(v, v));
-  v = max(v, dpp<0x140>(v, v));
-  v = max(v, dpp<0x142, 0xA>(v, v));
-  v = max(v, dpp<0x143, 0xC>(v, v));
-  return __builtin_amdgcn_readlane(v, 63);
+__device__ __attribute__((always_inline)) inline uint32_t wave_top(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  v = max(v, dpp<0x140>(v));
+  v = max(v, dpp<0x142, 0xA>(v));
+  v = max(v, dpp<0x143, 0xC>(v));
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 __device__ __attribute__((always_inline)) inline float wave_sum(float x) {
-  auto add = [](float a, int b) { return a + __int_as_float(b); };
-  x = add(x, dpp<0xB1>(0, __float_as_int(x)));
-  x = add(x, dpp<0x4E>(0, __float_as_int(x)));
-  x = add(x, dpp<0x141>(0, __float_as_int(x)));
-  x = add(x, dpp<0x140>(0, __float_as_int(x)));
-  x = add(x, dpp<0x142, 0xA>(0, __float_as_int(x)));
-  x = add(x, dpp<0x143, 0xC>(0, __float_as_int(x)));
+  auto all = [](float v, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x += all(x, std::integral_constant<int, 0xB1>{});
+  x += all(x, std::integral_constant<int, 0x4E>{});
+  x += all(x, std::integral_constant<int, 0x141>{});
+  x += all(x, std::integral_constant<int, 0x140>{});
+  x += __uint_as_float(dpp<0x142, 0xA>(__float_as_uint(x)));
+  x += __uint_as_float(dpp<0x143, 0xC>(__float_as_uint(x)));
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
 // Logits as integers of their order (-0 as 0); -inf and NaN, which are never chosen, below all.
-__device__ __attribute__((always_inline)) inline int order_of(float z) {
-  const int b = __float_as_int(z + 0.f), k = b < 0 ? b ^ 0x7FFFFFFF : b;
+__device__ __attribute__((always_inline)) inline uint32_t order_of(float z) {
+  const int b = __float_as_int(z + 0.f);
+  const uint32_t k = uint32_t(b) ^ (uint32_t(b >> 31) | 0x80000000u);
   return z > -kInf ? k : kNever;
 }
-__device__ __attribute__((always_inline)) inline float logit_of(int k) { return __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k); }
+__device__ __attribute__((always_inline)) inline float logit_of(uint32_t k) {
+  return __uint_as_float(k ^ (uint32_t(int(~k) >> 31) | 0x80000000u));
+}
 
 // e^d, d <= 0: the product with log2 e and the hardware's exp2 round once each
 __device__ __attribute__((always_inline)) inline float exp_of(float d) {
@@ -61,18 +68,13 @@ struct Logits {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = lane + 64 * j;
-      z[j] = e < experts ? float(gload<X>(row + e)) : -kInf;
+      const float v = float(gload<X>(row + min(e, experts - 1)));
+      z[j] = e < experts ? v : -kInf;
     }
   }
-  // whether some logit is not -inf
-  __device__ __attribute__((always_inline)) inline bool some() const {
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < J; ++j) any = any || !(z[j] == -kInf);
-    return __any(any);
-  }
-  __device__ __attribute__((always_inline)) inline int top(int (&key)[J]) const {
-    int best = kNever;
+  // the largest as its integer; kNever where none can be chosen
+  __device__ __attribute__((always_inline)) inline uint32_t top(uint32_t (&key)[J]) const {
+    uint32_t best = kNever;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       key[j] = order_of(z[j]);
@@ -80,12 +82,21 @@ struct Logits {
     }
     return wave_top(best);
   }
+  // whether some logit is not -inf
+  __device__ __attribute__((always_inline)) inline bool some(uint32_t top) const {
+    if (top != kNever) return true;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < J; ++j) nan = nan || z[j] != z[j];
+    return __any(nan);
+  }
   // softmax, the largest logit known; 0 beyond the last expert
   __device__ __attribute__((always_inline)) inline void softmax(float (&p)[J], float top, int experts, int lane) const {
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      p[j] = lane + 64 * j < experts ? exp_of(z[j] - top) : 0.f;
+      const float e = exp_of(z[j] - top);
+      p[j] = lane + 64 * j < experts ? e : 0.f;
       sum += p[j];
     }
     sum = 1.f / wave_sum(sum);
@@ -119,37 +130,58 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   if (t < a.tokens) fetch(t);
   for (; t < a.tokens; t += step) {
     const Logits<X, J> l = next;
-    const bool on = next_on && l.some();
+    const bool valid = next_on;
     if (t + step < a.tokens) fetch(t + step);
-    int mine = -1, mine_key = kNever, first = kNever;  // lane i: the choice of rank i, and its logit
-    if (on) {
+    uint32_t key[J];
+    const uint32_t first = l.top(key);
+    int mine = -1;  // lane i: the choice of rank i, and its logit
+    uint32_t mine_key = kNever;
+    if (valid && l.some(first)) {
       ++counted;
-      int key[J];
-      first = l.top(key);
       float p[J];
       l.softmax(p, logit_of(first), a.experts, lane);
 #pragma unroll
       for (int j = 0; j < J; ++j) sums[j] += p[j];
-      int best = first;
-      for (int i = 0; i < a.top_k && best != kNever; ++i) {
-        // the lowest expert of that logit
-        int at = 0;
-        bool found = false;
+      // larger first, the lower expert first on ties (neighbours only are exchanged)
+      int expert[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint64_t same = __ballot(key[j] == best);
-          const bool here = !found && same != 0;
-          const int src = here ? __builtin_ctzll(same) : 64;
-          at = here ? src + 64 * j : at;
-          key[j] = lane == src ? kNever : key[j];
-          found = found || here;
+      for (int j = 0; j < J; ++j) expert[j] = lane + 64 * j;
+#pragma unroll
+      for (int r = 0; r < J; ++r) {
+#pragma unroll
+        for (int j = r & 1; j + 1 < J; j += 2) {
+          const bool swap = key[j + 1] > key[j];
+          const uint32_t hi = max(key[j], key[j + 1]), lo = min(key[j], key[j + 1]);
+          key[j] = hi;
+          key[j + 1] = lo;
+          const int x = expert[j], y = expert[j + 1];
+          expert[j] = swap ? y : x;
+          expert[j + 1] = swap ? x : y;
+        }
+      }
+      uint32_t best = first;
+      for (int i = 0; i < a.top_k && best != kNever; ++i) {
+        uint64_t same = __ballot(key[0] == best);
+        int src = __builtin_ctzll(same);
+        int at = __builtin_amdgcn_readlane(expert[0], src);
+        for (same &= same - 1; same; same &= same - 1) {  // other lanes have that logit too
+          const int s = __builtin_ctzll(same), e = __builtin_amdgcn_readlane(expert[0], s);
+          if (e < at) {
+            at = e;
+            src = s;
+          }
         }
         mine = lane == i ? at : mine;
         mine_key = lane == i ? best : mine_key;
-        best = key[0];
+        if (lane == src) {
 #pragma unroll
-        for (int j = 1; j < J; ++j) best = max(best, key[j]);
-        best = wave_top(best);
+          for (int j = 0; j + 1 < J; ++j) {
+            key[j] = key[j + 1];
+            expert[j] = expert[j + 1];
+          }
+          key[J - 1] = kNever;
+        }
+        best = wave_top(key[0]);
       }
       if (mine >= 0) atomicAdd(&lds_c[mine], 1);
     }
@@ -278,17 +310,18 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
   if (t < a.tokens) fetch(t);
   for (; t < a.tokens; t += step) {
     const Logits<X, J> l = next;
-    const bool on = next_on && l.some();
+    const bool valid = next_on;
     const int i = next_sel;
     const bool chosen = uint32_t(i) < uint32_t(a.experts);
     const float w = chosen ? next_w : 0.f, dw = chosen ? next_dw : 0.f;
     if (t + step < a.tokens) fetch(t + step);
     X* dz = static_cast<X*>(a.dlogits) + t * a.ld;
     float d[J] = {};
-    if (on) {
-      int key[J];
+    uint32_t key[J];
+    const uint32_t top = l.top(key);
+    if (valid && l.some(top)) {
       float p[J], sum = 0.f;
-      l.softmax(p, logit_of(l.top(key)), a.experts, lane);
+      l.softmax(p, logit_of(top), a.experts, lane);
 #pragma unroll
       for (int j = 0; j < J; ++j) sum = fmaf(p[j], c[j], sum);
       sum = wave_sum(sum);
