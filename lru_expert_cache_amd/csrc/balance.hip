@@ -14,7 +14,10 @@ namespace ftmoe {
 
 namespace {
 
-constexpr int kWaves = 16;
+// waves of a workgroup
+// of a workgroup: few tokens are spread over more CUs, many leave fewer parts to add up
+constexpr int balance_waves(int32_t tokens) { return tokens <= 2048 ? 4 : 16; }
+constexpr int kBackWaves = 4;
 constexpr float kInf = __builtin_huge_valf();
 constexpr uint32_t kNever = 0;  // below every logit that can be chosen
 
@@ -105,7 +108,7 @@ struct Logits {
   }
 };
 
-template <typename X, int J>
+template <typename X, int J, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   __shared__ float lds_p[kWaves][64 * J];
   __shared__ int lds_c[64 * J];
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
 // every 64th part.  The workgroup that arrives last adds up the loss: the
 // others' shares of it are written past the XCD's own cache, and the counter
 // is touched after them.
-constexpr int kJoin = 256;
+constexpr int kJoin = 512;
 __global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
   typedef float floatx4 __attribute__((ext_vector_type(4)));
   typedef int intx4 __attribute__((ext_vector_type(4)));
@@ -219,7 +222,9 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = 4 * (tid & 3);
   const int e0 = 16 * int(blockIdx.x);
   double p[4] = {};
-  int c[4] = {};
+  int c[4] = {}, v = 0;
+  if (wave == 0)
+    for (int g = lane; g < a.groups; g += 64) v += a.part_v[g];
 #pragma unroll 4
   for (int g = tid >> 2; g < a.groups; g += kJoin / 4) {
     const floatx4 pv = gload<floatx4>(a.part_p + int64_t(g) * a.ld_part + e0 + col);
@@ -261,8 +266,6 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
   }
   __syncthreads();
   if (!last || wave != 0) return;
-  int v = 0;
-  for (int g = lane; g < a.groups; g += 64) v += a.part_v[g];
   double sum = lane < int(gridDim.x) ? __hip_atomic_load(a.share + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -277,8 +280,8 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
 }
 
 template <typename X, int J>
-__global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackward a) {
-  __shared__ float lds[kWaves][64 * J];
+__global__ __launch_bounds__(64 * kBackWaves) void k_balance_backward(BalanceBackward a) {
+  __shared__ float lds[kBackWaves][64 * J];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float c[J];
   {
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
     }
   }
   const float dloss = a.dloss ? a.dloss[0] : 1.f;
-  const int64_t step = int64_t(gridDim.x) * kWaves;
+  const int64_t step = int64_t(gridDim.x) * kBackWaves;
   Logits<X, J> next;
   bool next_on = true;
   int next_sel = -1;
@@ -306,7 +309,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
       next_dw = gload<float>(a.dw + t * a.top_k + lane);
     }
   };
-  int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+  int64_t t = int64_t(blockIdx.x) * kBackWaves + wave;
   if (t < a.tokens) fetch(t);
   for (; t < a.tokens; t += step) {
     const Logits<X, J> l = next;
@@ -347,14 +350,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance_backward(BalanceBackwar
 template <typename X, int J>
 hipError_t launch(const BalanceForward& a, hipStream_t s) {
   if (a.ld_part != 64 * J) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_balance<X, J>), dim3(uint32_t(a.groups)), dim3(64 * kWaves), 0, s, a);
+  if (balance_waves(a.tokens) == 4)
+    hipLaunchKernelGGL((k_balance<X, J, 4>), dim3(uint32_t(a.groups)), dim3(64 * 4), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_balance<X, J, 16>), dim3(uint32_t(a.groups)), dim3(64 * 16), 0, s, a);
   hipLaunchKernelGGL(k_balance_join, dim3(uint32_t((a.experts + 15) / 16)), dim3(kJoin), 0, s, a);
   return hipGetLastError();
 }
 template <typename X, int J>
 hipError_t launch(const BalanceBackward& a, hipStream_t s) {
-  const uint32_t grid = uint32_t(balance_groups(a.tokens));
-  hipLaunchKernelGGL((k_balance_backward<X, J>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+  const int32_t groups = (a.tokens + kBackWaves - 1) / kBackWaves;
+  hipLaunchKernelGGL((k_balance_backward<X, J>), dim3(uint32_t(groups < 2048 ? groups : 2048)), dim3(64 * kBackWaves), 0, s, a);
   return hipGetLastError();
 }
 template <typename X, typename A>
@@ -374,7 +380,7 @@ hipError_t launch_type(int dtype, const A& a, hipStream_t s) {
 }  // namespace
 
 int balance_groups(int32_t tokens) {
-  const int32_t g = (tokens + kWaves - 1) / kWaves;
+  const int32_t waves = balance_waves(tokens), g = (tokens + waves - 1) / waves;
   return g < 1 ? 1 : g < 512 ? g : 512;
 }
 
