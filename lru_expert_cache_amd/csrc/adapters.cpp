@@ -124,6 +124,15 @@ int ft_moe_adapters_apply(const ft_moe_adapters* desc, const void* x, const int3
     l.tile_cap = w.plan.tile_cap;
     l.parts = w.plan.parts;
     l.out_blocks = w.plan.out_blocks;
+    const uint32_t tiles = uint32_t(l.windows) * uint32_t(l.tile_cap);
+    const uint32_t rows = d.rank <= 64 ? 1 : uint32_t(d.rank + 63) / 64;  // blocks of up to 64 rows of A
+    const uint32_t wide = 128u * uint32_t(l.out_blocks), across = (uint32_t(d.out) + wide - 1) / wide;
+    l.by_cap = FastDiv(uint32_t(l.tile_cap));
+    l.by_parts = FastDiv(uint32_t(l.parts));
+    l.by_rows = FastDiv(rows);
+    l.by_across = FastDiv(across);
+    l.in_total = tiles * rows * uint32_t(l.parts);
+    l.out_total = tiles * across;
     if (!l.few) FT_HIP_CHECK(launch_adapters_plan(l, s));
     FT_HIP_CHECK(launch_adapters_in(d.dtype, l, s));
     FT_HIP_CHECK(launch_adapters_out(d.dtype, d.base_dtype, d.out_dtype, l, s));

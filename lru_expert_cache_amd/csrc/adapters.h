@@ -17,6 +17,24 @@ constexpr int32_t kAdapterWindow = 8192;
 // Up to this many, each wave finds its tile by itself; else a launch of its own writes down the tiles.
 constexpr int32_t kAdapterFew = 64;
 
+// Division of a number below 2^31 by one that is known before the launch.
+struct FastDiv {
+  uint32_t by, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) : by(d), mul(0), shift(0) {
+    if (d <= 1) return;
+    uint32_t bits = 1;  // 2^bits >= d
+    while ((uint64_t(1) << bits) < d) ++bits;
+    shift = bits - 1;
+    mul = uint32_t(((uint64_t(1) << (31 + bits)) + d - 1) / d);
+  }
+#ifdef __HIPCC__
+  __device__ __attribute__((always_inline)) inline uint32_t operator()(uint32_t n) const {
+    return by <= 1 ? n : __umulhi(n, mul) >> shift;
+  }
+#endif
+};
+
 struct AdapterTile {
   int32_t id;     // adapter, or their number for tokens that have none
   int32_t first;  // in `order`
@@ -40,6 +58,8 @@ struct Adapters {
   int32_t few, sub;    // tiles found by each wave; groups of 16 tokens in a tile
   int32_t windows, tile_cap, parts;
   int32_t out_blocks;  // 128-column blocks of y that a workgroup of the second product takes
+  FastDiv by_cap, by_parts, by_rows, by_across;  // by tile_cap, parts, blocks of A's rows, workgroups across y
+  uint32_t in_total, out_total;                   // workgroups' worth of work of either product
   bool in_place;       // y is base: tokens without an adapter are left out
 };
 

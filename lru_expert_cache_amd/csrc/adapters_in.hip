@@ -31,10 +31,25 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
     }
   }
   __syncthreads();
-  // one addition for each run of the same adapter
+  // One addition for each run of the same adapter: lanes whose tokens are all
+  // of one, and of the same as the lane's before, leave it to the first of
+  // them (an addition for each lane of a long prompt took 3 us more).
+  bool whole = group[0] >= 0;
+#pragma unroll
+  for (int i = 1; i < kEach; ++i) whole = whole && group[i] == group[0];
+  const int before_whole = __shfl_up(int(whole), 1), before_group = __shfl_up(group[0], 1);  // by every lane
+  const bool follows = whole && lane > 0 && before_whole && before_group == group[0];
+  const uint64_t heads = ~__ballot(follows);
+  const int head = 63 - __builtin_clzll(heads & (~uint64_t(0) >> (63 - lane)));
+  const uint64_t later = heads >> lane >> 1;  // this lane's run ends before the next head
+  const int lanes = later ? __builtin_ctzll(later) + 1 : 64 - lane;
+  int base = 0;
+  if (whole && !follows) base = atomicAdd(&hist[group[0]], kEach * lanes);
+  base = __shfl(base, head) + kEach * (lane - head);
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    place[i] = 0;
+    place[i] = base + i;
+    if (whole) continue;
     if (i > 0 && group[i] == group[i - 1]) {
       place[i] = place[i - 1] + 1;
     } else if (group[i] >= 0) {
@@ -95,11 +110,12 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
   typedef typename D::elem E;
   __shared__ floatx4 lds[kWaves][SUB * ROWS][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-  const int blocks = (l.rank + 16 * ROWS - 1) / (16 * ROWS);
-  const int64_t total = int64_t(l.windows) * l.tile_cap * blocks * l.parts;
-  for (int64_t flat = blockIdx.x; flat < total; flat += gridDim.x) {
-    const int part = int(flat % l.parts), block = int(flat / l.parts % blocks);
-    const TileTokens<SUB> t = find_tile<SUB>(l, flat / l.parts / blocks);
+  for (uint32_t round = blockIdx.x; round < adapter_rounds(l.in_total); round += gridDim.x) {
+    const uint32_t flat = adapter_work(round, l.in_total);
+    if (flat >= l.in_total) continue;
+    const uint32_t above = l.by_parts(flat), tile = l.by_rows(above);
+    const int part = int(flat - above * uint32_t(l.parts)), block = int(above - tile * l.by_rows.by);
+    const TileTokens<SUB> t = find_tile<SUB>(l, tile);
     if (!t.live || t.id == l.count) continue;
     const E* x[SUB];
     const E* a[ROWS];
@@ -111,11 +127,11 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
       a[j] = static_cast<const E*>(l.a) + (int64_t(t.id) * l.rank + r) * l.ld_a;
     }
     // K in units of 64 elements: two instructions, 128 bytes of a row
-    const int64_t units = (l.in + 63) / 64;
-    const int64_t p0 = units * part / l.parts, p1 = units * (part + 1) / l.parts;
+    const uint32_t units = uint32_t(l.in + 63) / 64;  // times a part's number: below 2^31
+    const uint32_t p0 = l.by_parts(units * part), p1 = l.by_parts(units * (part + 1));
     const int u0 = int(p0 + (p1 - p0) * wave / kWaves);
     int u1 = int(p0 + (p1 - p0) * (wave + 1) / kWaves);
-    const bool tail = u1 == units && u1 > u0 && l.in % 64 != 0;
+    const bool tail = u1 == int(units) && u1 > u0 && l.in % 64 != 0;
     if (tail) --u1;
     floatx4 acc[SUB][ROWS] = {};
     auto step = [&](const u32x4(&xv)[SUB], const u32x4(&av)[ROWS]) {
@@ -125,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
         for (int j = 0; j < ROWS; ++j) acc[m][j] = D::mfma16(av[j], xv[m], acc[m][j]);
     };
     typedef u32x4 __attribute__((aligned(1))) any;
-    u32x4 xv[2][SUB], av[2][ROWS];
+    u32x4 xv[2][SUB] = {}, av[2][ROWS] = {};
     auto fetch = [&](int u) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -136,8 +152,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
         for (int j = 0; j < ROWS; ++j) av[h][j] = gload<any>(a[j] + k);
       }
     };
-    if (u0 < u1) fetch(u0);
-    for (int u = u0; u < u1; ++u) {
+    for (int u = u0 - 1; u < u1; ++u) {  // each unit's loads are a turn ahead of its products
       u32x4 xn[2][SUB], an[2][ROWS];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -147,18 +162,19 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
         for (int j = 0; j < ROWS; ++j) an[h][j] = av[h][j];
       }
       if (u + 1 < u1) fetch(u + 1);
+      if (u < u0) continue;
       step(xn[0], an[0]);
       step(xn[1], an[1]);
     }
     if (tail) {
-#pragma unroll
+#pragma nounroll
       for (int h = 0; h < 2; ++h) {
         const int c = 8 * u1 + 4 * h + q;
 #pragma unroll
-        for (int m = 0; m < SUB; ++m) xv[h][m] = row_piece<E, true>(x[m], c, l.in);
+        for (int m = 0; m < SUB; ++m) xv[0][m] = row_piece<E, true>(x[m], c, l.in);
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) av[h][j] = row_piece<E, false>(a[j], c, l.in);
-        step(xv[h], av[h]);
+        for (int j = 0; j < ROWS; ++j) av[0][j] = row_piece<E, false>(a[j], c, l.in);
+        step(xv[0], av[0]);
       }
     }
     __syncthreads();  // the last tile's sums have been read
@@ -186,10 +202,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
 
 template <typename D, int SUB, int ROWS>
 hipError_t launch(const Adapters& l, hipStream_t s) {
-  const int64_t blocks = (l.rank + 16 * ROWS - 1) / (16 * ROWS);
-  const int64_t total = int64_t(l.windows) * l.tile_cap * blocks * l.parts;
-  hipLaunchKernelGGL((k_adapters_in<D, SUB, ROWS>), dim3(uint32_t(total < (1 << 22) ? total : (1 << 22))), dim3(kThreads), 0,
-                     s, l);
+  hipLaunchKernelGGL((k_adapters_in<D, SUB, ROWS>), dim3(adapter_grid(l.in_total)), dim3(kThreads), 0, s, l);
   return hipGetLastError();
 }
 template <typename D, int SUB>

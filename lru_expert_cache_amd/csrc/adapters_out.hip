@@ -13,6 +13,20 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
+// A row's last columns, fewer than eight, from column c on (none of them where
+// it has ended); the loop is not unrolled, to keep the code short.
+template <typename B>
+__device__ __attribute__((always_inline)) inline B __attribute__((ext_vector_type(8))) last_columns(const B* row, int c, int width) {
+  B __attribute__((ext_vector_type(8))) v{};
+#pragma nounroll
+  for (int i = width - 1; i >= c; --i) {
+#pragma unroll
+    for (int j = 7; j > 0; --j) v[j] = v[j - 1];
+    v[0] = gload<B>(row + i);
+  }
+  return v;
+}
+
 // KS: steps of 32 ranks; 0: up to 16 ranks, two parts in a step
 template <typename D, typename B, typename Y, int SUB, int KS>
 __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
@@ -25,44 +39,72 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
   constexpr int kParts = !kHalf && sizeof(Y) == 4 ? 3 : 2;
   constexpr int kSteps = KS == 0 ? 1 : KS;                              // of B's pieces
   constexpr int kFrags = KS == 0 ? (kParts + 1) / 2 : KS * kParts;      // of h's
+  // sums of h: one for each group of 16 tokens and step of ranks, in kGroups shares of the parts of K
+  constexpr int kGroups = SUB * kSteps >= kWaves ? 1 : kWaves / (SUB * kSteps), kSlots = SUB * kSteps * kGroups;
+  __shared__ floatx4 lds[kSlots][2][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-  const int across = (l.out + 128 * l.out_blocks - 1) / (128 * l.out_blocks);
-  const int64_t total = int64_t(l.windows) * l.tile_cap * across;
-  for (int64_t flat = blockIdx.x; flat < total; flat += gridDim.x) {
-    const TileTokens<SUB> t = find_tile<SUB>(l, flat / across);
+  for (uint32_t round = blockIdx.x; round < adapter_rounds(l.out_total); round += gridDim.x) {
+    const uint32_t flat = adapter_work(round, l.out_total);
+    if (flat >= l.out_total) continue;
+    const uint32_t tile = l.by_across(flat);
+    const TileTokens<SUB> t = find_tile<SUB>(l, tile);
     if (!t.live) continue;
-    const int n0 = int(flat % across) * 128 * l.out_blocks + 32 * wave;
-    const int n1 = int(min(int64_t(l.out), int64_t(flat % across + 1) * 128 * l.out_blocks));
+    const int wide = 128 * l.out_blocks, c0 = int(flat - tile * l.by_across.by) * wide;
+    const int n0 = c0 + 32 * wave, n1 = min(l.out - c0, wide) + c0;
     const bool on = t.id != l.count;
 
-    // this lane's token and ranks: 8 (q mod 2) .. for KS 0, else 32 step + 8 q ..
     u32x4 h[SUB][kFrags] = {};
-    float scale[SUB];
-    if (on) {
+    float scale[SUB] = {};
+    // The parts of h, added up by the four waves together.  A lane has its
+    // token's ranks 8 (q mod 2) .. for KS 0, else 32 step + 8 q ..; a row's
+    // last pieces as row_piece takes them of B.
+    auto join = [&]() {
+      __syncthreads();  // the last tile's sums have been read
+#pragma unroll
+      for (int i = 0; i < kSlots / kWaves; ++i) {
+        const int slot = wave + kWaves * i, m = slot / kGroups / kSteps, k = slot / kGroups % kSteps;
+        const int c = KS == 0 ? (q & 1) : 4 * k + q;
+        const float* row = l.h + int64_t(t.token[0]) * l.ld_h;
+#pragma unroll
+        for (int n = 1; n < SUB; ++n) row = m == n ? l.h + int64_t(t.token[n]) * l.ld_h : row;
+        const int64_t part = int64_t(l.tokens) * l.ld_h;
+        const int from = min(8 * c, max(l.rank - 8, 0));
+        float8 sum{};
+        if (8 * c < l.rank) {
+          if (l.rank >= 8) {
+#pragma unroll 4
+            for (int p = slot % kGroups; p < l.parts; p += kGroups) sum += gload<float8_any>(row + p * part + from);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = from + e >= 8 * c ? sum[e] : 0.f;
+          } else {
+            for (int p = slot % kGroups; p < l.parts; p += kGroups) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e < l.rank) sum[e] += gload<float>(row + p * part + e);
+            }
+          }
+        }
+        lds[slot][0][lane] = __builtin_shufflevector(sum, sum, 0, 1, 2, 3);
+        lds[slot][1][lane] = __builtin_shufflevector(sum, sum, 4, 5, 6, 7);
+      }
+      __syncthreads();
 #pragma unroll
       for (int m = 0; m < SUB; ++m) {
         float v[kSteps][8];
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          const int c = KS == 0 ? (q & 1) : 4 * k + q;  // piece of eight ranks, as row_piece takes it of B
-          const float* row = l.h + int64_t(t.token[m]) * l.ld_h;
-          const int from = min(8 * c, max(l.rank - 8, 0));
+          const int slot = (m * kSteps + k) * kGroups;
+          floatx4 lo = lds[slot][0][lane], hi = lds[slot][1][lane];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-          if (8 * c < l.rank) {
-            if (l.rank >= 8) {
-              float8 sum{};
-              for (int p = 0; p < l.parts; ++p) sum += gload<float8_any>(row + int64_t(p) * l.tokens * l.ld_h + from);
+          for (int g = 1; g < kGroups; ++g) {
+            lo += lds[slot + g][0][lane];
+            hi += lds[slot + g][1][lane];
+          }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[k][i] = from + i >= 8 * c ? sum[i] : 0.f;
-            } else {
-              for (int p = 0; p < l.parts; ++p) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i < l.rank) v[k][i] += gload<float>(row + int64_t(p) * l.tokens * l.ld_h + i);
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            v[k][i] = lo[i];
+            v[k][4 + i] = hi[i];
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
@@ -101,12 +143,12 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
           }
         }
       }
-    }
+    };
 
     // A step's 32 columns: two instructions, whose rows 4 a + i are columns 8 a + 4 j + i: lane (q, token) gets
     // columns 8 q .. 8 q + 7.
-    u32x4 b[2][kSteps];
-    base8 with[SUB];
+    u32x4 b[2][kSteps] = {};
+    base8 with[SUB] = {};
     const int mine = 8 * ((lane & 15) >> 2) + (lane & 3);
     auto fetch = [&](int n) {
       if (on) {
@@ -117,23 +159,18 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
           for (int k = 0; k < kSteps; ++k) b[j][k] = row_piece<E, false>(row, KS == 0 ? (q & 1) : 4 * k + q, l.rank);
         }
       }
-      const int c = n + 8 * q;
       if (l.base) {
+        const int c = n + 8 * q;
 #pragma unroll
         for (int m = 0; m < SUB; ++m) {
           const B* row = static_cast<const B*>(l.base) + int64_t(t.token[m]) * l.ld_base;
           typedef base8 __attribute__((aligned(1))) any;
-          if (c + 8 <= l.out) {
-            with[m] = gload<any>(row + c);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) with[m][i] = c + i < l.out ? gload<B>(row + c + i) : B(0);
-          }
+          if (c + 8 <= l.out) with[m] = gload<any>(row + c);
+          else with[m] = last_columns(row, c, l.out);
         }
       }
     };
-    if (n0 < n1) fetch(n0);
-    for (int n = n0; n < n1; n += 128) {
+    for (int n = n0 - 128; n < n1; n += 128) {  // each step's loads are a turn ahead of its products
       u32x4 bn[2][kSteps];
       base8 wn[SUB];
 #pragma unroll
@@ -143,6 +180,11 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
 #pragma unroll
       for (int m = 0; m < SUB; ++m) wn[m] = with[m];
       if (n + 128 < n1) fetch(n + 128);
+      if (n < n0) {  // the first turn, of every wave
+        if (on) join();
+        continue;
+      }
+      const int c = n + 8 * q;
 #pragma unroll
       for (int m = 0; m < SUB; ++m) {
         float v[8] = {};
@@ -159,7 +201,6 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += float(wn[m][i]);
         }
-        const int c = n + 8 * q;
         if (16 * m + (lane & 15) < t.count && c < l.out)
           dense_store<Y, 8>(static_cast<uint8_t*>(l.y), int64_t(t.token[m]) * l.ld_y + c, v, min(8, l.out - c));
       }
@@ -169,10 +210,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
 
 template <typename D, typename B, typename Y, int SUB, int KS>
 hipError_t launch(const Adapters& l, hipStream_t s) {
-  const int64_t across = (l.out + 128 * l.out_blocks - 1) / (128 * l.out_blocks);
-  const int64_t total = int64_t(l.windows) * l.tile_cap * across;
-  hipLaunchKernelGGL((k_adapters_out<D, B, Y, SUB, KS>), dim3(uint32_t(total < (1 << 22) ? total : (1 << 22))),
-                     dim3(kThreads), 0, s, l);
+  hipLaunchKernelGGL((k_adapters_out<D, B, Y, SUB, KS>), dim3(adapter_grid(l.out_total)), dim3(kThreads), 0, s, l);
   return hipGetLastError();
 }
 template <typename D, typename B, typename Y>

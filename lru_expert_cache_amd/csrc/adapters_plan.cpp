@@ -22,6 +22,9 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>(512 / tiles, in / 256), 1, 32));
   const int64_t blocks = (out + 127) / 128;  // of a workgroup's 128 columns
   p.out_blocks = int32_t(std::clamp<int64_t>(blocks * tiles / 1024, 1, 8));
+  // (numbers of workgroups stay below 2^30)
+  const int64_t all = int64_t(p.windows) * p.tile_cap;
+  p.out_blocks = int32_t(std::max<int64_t>(p.out_blocks, (all * blocks >> 30) + 1));
   return p;
 }
 
