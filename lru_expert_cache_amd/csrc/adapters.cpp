@@ -43,12 +43,12 @@ struct AdaptersWork {
 AdaptersWork adapters_work(const ft_moe_adapters& d, void* base) {
   AdaptersWork w{};
   Carve c{static_cast<uint8_t*>(base)};
-  w.plan = adapter_plan(d.tokens, d.in, d.out, d.rank, d.adapters);
+  w.plan = adapter_plan(d.tokens, d.in, d.out, d.rank, d.adapters, int(size_of(d.base_dtype)), int(size_of(d.out_dtype)));
   w.ld_h = int32_t(up(d.rank, 4));
   w.h = reinterpret_cast<float*>(c.take(int64_t(w.plan.parts) * d.tokens * w.ld_h * 4));
   if (!w.plan.few) {
     w.order = reinterpret_cast<int32_t*>(c.take(int64_t(d.tokens) * 4));
-    w.tile_count = reinterpret_cast<int32_t*>(c.take(int64_t(w.plan.windows) * 4));
+    w.tile_count = reinterpret_cast<int32_t*>(c.take(int64_t(w.plan.windows) * 8));
     w.tiles = reinterpret_cast<AdapterTile*>(c.take(int64_t(w.plan.windows) * w.plan.tile_cap * int64_t(sizeof(AdapterTile))));
   }
   w.bytes = c.used;
@@ -124,15 +124,13 @@ int ft_moe_adapters_apply(const ft_moe_adapters* desc, const void* x, const int3
     l.tile_cap = w.plan.tile_cap;
     l.parts = w.plan.parts;
     l.out_blocks = w.plan.out_blocks;
-    const uint32_t tiles = uint32_t(l.windows) * uint32_t(l.tile_cap);
     const uint32_t rows = d.rank <= 64 ? 1 : uint32_t(d.rank + 63) / 64;  // blocks of up to 64 rows of A
-    const uint32_t wide = 128u * uint32_t(l.out_blocks), across = (uint32_t(d.out) + wide - 1) / wide;
-    l.by_cap = FastDiv(uint32_t(l.tile_cap));
+    const uint32_t wide = uint32_t(w.plan.out_step) * uint32_t(l.out_blocks);
     l.by_parts = FastDiv(uint32_t(l.parts));
-    l.by_rows = FastDiv(rows);
-    l.by_across = FastDiv(across);
-    l.in_total = tiles * rows * uint32_t(l.parts);
-    l.out_total = tiles * across;
+    l.in_each = FastDiv(rows * uint32_t(l.parts));
+    l.out_each = FastDiv((uint32_t(d.out) + wide - 1) / wide);
+    l.in_window = FastDiv(uint32_t(up(int64_t(l.tile_cap) * l.in_each.by, 8)));
+    l.out_window = FastDiv(uint32_t(up(int64_t(l.tile_cap) * l.out_each.by, 8)));
     if (!l.few) FT_HIP_CHECK(launch_adapters_plan(l, s));
     FT_HIP_CHECK(launch_adapters_in(d.dtype, l, s));
     FT_HIP_CHECK(launch_adapters_out(d.dtype, d.base_dtype, d.out_dtype, l, s));

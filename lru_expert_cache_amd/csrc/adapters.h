@@ -52,22 +52,33 @@ struct Adapters {
   float* h;            // [parts][T][ld_h]: sums over each part of K
   int32_t* order;      // [T]: tokens of each tile next to each other
   AdapterTile* tiles;  // [windows][tile_cap]
-  int32_t* tile_count; // [windows]
+  int32_t* tile_count; // [windows][2]: all tiles, and those of an adapter, which come first
   int64_t ld_x, ld_a, ld_b, ld_base, ld_y;
   int32_t tokens, in, out, rank, count, ld_h;
   int32_t few, sub;    // tiles found by each wave; groups of 16 tokens in a tile
   int32_t windows, tile_cap, parts;
-  int32_t out_blocks;  // 128-column blocks of y that a workgroup of the second product takes
-  FastDiv by_cap, by_parts, by_rows, by_across;  // by tile_cap, parts, blocks of A's rows, workgroups across y
-  uint32_t in_total, out_total;                   // workgroups' worth of work of either product
+  int32_t out_blocks;  // steps of columns of y that a workgroup of the second product takes
+  // either product: a tile's pieces of work, and a window's (of as many tiles as it can have; a multiple of the XCDs)
+  FastDiv in_each, in_window, out_each, out_window;
+  FastDiv by_parts;
   bool in_place;       // y is base: tokens without an adapter are left out
 };
 
-// How a call is cut: a rule on sizes alone.
+// Blocks of 32 columns that a wave of the second product takes at once: 128
+// bytes of a row of base and y, whose halves would else be asked for by two
+// waves (adapters of rank 64, 8192 tokens: half as many requests to the L2
+// cache); one where they would take too many registers.
+constexpr int adapter_out_blocks(int base_bytes, int out_bytes, int sub) {
+  return out_bytes == 4 || (base_bytes == 4 && sub == 4) ? 1 : 2;
+}
+
+// How a call is cut: a rule on sizes and types alone.
 struct AdapterPlan {
   int32_t few, sub, windows, tile_cap, parts, out_blocks;
+  int32_t out_step;  // columns of y in a step of a workgroup: its four waves' blocks
 };
-AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count);
+AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count, int base_bytes,
+                         int out_bytes);
 
 hipError_t launch_adapters_plan(const Adapters& l, hipStream_t s);
 hipError_t launch_adapters_in(int dtype, const Adapters& l, hipStream_t s);

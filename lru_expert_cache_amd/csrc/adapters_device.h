@@ -12,18 +12,28 @@ template <int SUB>
 struct TileTokens {
   int id, count;
   int token[SUB];
-  bool live;
 };
 
-// Tile `item` of up to 64 tokens: the wave holds a token's id in each lane and
-// counts, for each token, those of the same adapter before it; every 16th of
-// an adapter begins a tile.
-__device__ __attribute__((always_inline)) inline TileTokens<1> few_tile(const Adapters& l, int item) {
+// Workgroups are handed to the eight XCDs in turn; each XCD takes a range of a
+// window's pieces of work next to each other, so that the tiles of one adapter
+// find its matrices in their XCD's cache.  The piece of workgroup (or round)
+// `at` of a window with `pieces`, or one that is not there.
+constexpr uint32_t kXcds = 8;
+__device__ __attribute__((always_inline)) inline uint32_t xcd_piece(uint32_t at, uint32_t pieces) {
+  const uint32_t per = (pieces + kXcds - 1) / kXcds;
+  return at / kXcds < per ? at % kXcds * per + at / kXcds : pieces;
+}
+
+// The tile of round `at` among up to 64 tokens, and which of its `each` pieces
+// of work.  The wave holds a token's id in each lane and counts, for each
+// token, those of the same adapter before it; every 16th of an adapter begins a tile.
+__device__ __attribute__((always_inline)) inline bool few_tile(const Adapters& l, uint32_t at, FastDiv each, bool bare,
+                                                               TileTokens<1>& t, int& piece) {
   const int lane = threadIdx.x & 63;
   int group = -1;
   if (lane < l.tokens) {
     const int id = gload<int32_t>(l.ids + lane);
-    group = uint32_t(id) < uint32_t(l.count) ? id : l.in_place ? -1 : l.count;
+    group = uint32_t(id) < uint32_t(l.count) ? id : bare && !l.in_place ? l.count : -1;
   }
   int rank = 0;
   for (int j = 0; j < l.tokens; ++j) {
@@ -32,10 +42,11 @@ __device__ __attribute__((always_inline)) inline TileTokens<1> few_tile(const Ad
   }
   const bool start = group >= 0 && rank % 16 == 0;
   const uint64_t starts = __ballot(start);
+  const uint32_t pieces = uint32_t(__popcll(starts)) * each.by, work = xcd_piece(at, pieces);
+  if (work >= pieces) return false;
+  const int item = int(each(work));
+  piece = int(work - uint32_t(item) * each.by);
   const int nth = __popcll(starts & ((uint64_t(1) << lane) - 1));
-  TileTokens<1> t{};
-  t.live = item < __popcll(starts);
-  if (!t.live) return t;
   const int src = __builtin_ctzll(__ballot(start && nth == item));
   t.id = __builtin_amdgcn_readlane(group, src);
   const int first = __builtin_amdgcn_readlane(rank, src);
@@ -44,37 +55,34 @@ __device__ __attribute__((always_inline)) inline TileTokens<1> few_tile(const Ad
   // each of its lanes sends its number to the lane of its place (the others to one that nobody reads)
   const int token = __builtin_amdgcn_ds_permute((mine ? rank - first : 63) * 4, lane);
   t.token[0] = __builtin_amdgcn_ds_bpermute(min(lane % 16, t.count - 1) * 4, token);
-  return t;
+  return true;
 }
 
+// The same of any round of any call; bare: tiles of tokens without an adapter count too.
 template <int SUB>
-__device__ __attribute__((always_inline)) inline TileTokens<SUB> find_tile(const Adapters& l, uint32_t item) {
-  TileTokens<SUB> t{};
+__device__ __attribute__((always_inline)) inline bool find_tile(const Adapters& l, uint32_t round, FastDiv window, FastDiv each,
+                                                                bool bare, TileTokens<SUB>& t, int& piece) {
   if constexpr (SUB == 1)
-    if (l.few) return few_tile(l, int(item));
-  const uint32_t window = l.by_cap(item);
-  t.live = int(item - window * uint32_t(l.tile_cap)) < gload<int32_t>(l.tile_count + window);
-  if (!t.live) return t;
+    if (l.few) return few_tile(l, round, each, bare, t, piece);
+  const uint32_t w = window(round);
+  const uint32_t pieces = uint32_t(gload<int32_t>(l.tile_count + 2 * w + (bare ? 0 : 1))) * each.by;
+  const uint32_t work = xcd_piece(round - w * window.by, pieces);
+  if (work >= pieces) return false;
+  const uint32_t item = each(work);
+  piece = int(work - item * each.by);
   static_assert(sizeof(AdapterTile) == 16, "one load");
-  const u32x4 w = gload<u32x4>(l.tiles + item);  // id, first, count
-  t.id = __builtin_amdgcn_readfirstlane(int(w[0]));
-  t.count = __builtin_amdgcn_readfirstlane(int(w[2]));
+  const u32x4 v = gload<u32x4>(l.tiles + int64_t(w) * l.tile_cap + item);  // id, first, count
+  t.id = __builtin_amdgcn_readfirstlane(int(v[0]));
+  t.count = __builtin_amdgcn_readfirstlane(int(v[2]));
 #pragma unroll
   for (int m = 0; m < SUB; ++m)
-    t.token[m] = gload<int32_t>(l.order + int(w[1]) + min(int(threadIdx.x & 15) + 16 * m, t.count - 1));
-  return t;
+    t.token[m] = gload<int32_t>(l.order + int(v[1]) + min(int(threadIdx.x & 15) + 16 * m, t.count - 1));
+  return true;
 }
 
-// Workgroups are handed to the eight XCDs in turn; each takes a range of the
-// work next to each other, so that tiles of one adapter find its matrices in
-// their XCD's cache.  Rounds of the loop go over adapter_rounds(total) numbers.
-constexpr uint32_t kXcds = 8;
-__host__ __device__ inline uint32_t adapter_rounds(uint32_t total) { return (total + kXcds - 1) / kXcds * kXcds; }
-__device__ __attribute__((always_inline)) inline uint32_t adapter_work(uint32_t round, uint32_t total) {
-  return round % kXcds * (adapter_rounds(total) / kXcds) + round / kXcds;
-}
-// workgroups of a launch, which go on to further rounds if there are more (a multiple of the XCDs)
-inline uint32_t adapter_grid(uint32_t total) { return std::min(adapter_rounds(total), uint32_t(1) << 22); }
+// rounds of a product, and workgroups of its launch, which go on to further rounds if there are more
+inline uint32_t adapter_rounds(const Adapters& l, FastDiv window) { return uint32_t(l.windows) * window.by; }
+inline uint32_t adapter_grid(uint32_t rounds) { return std::min(rounds, uint32_t(1) << 22); }
 
 // Eight neighbouring elements of a row of `width`, as a matrix instruction
 // takes them, from element 8 c.  Where the row ends within them, or before,

@@ -81,7 +81,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
   __syncthreads();
   uint32_t at = sum - own;
   for (int i = 0; i < tid >> 6; ++i) at += sums[i];
-  if (tid == kPlanThreads - 1) l.tile_count[blockIdx.x] = int((at + own) >> 16);
+  if (tid == kPlanThreads - 1) {
+    const int all = int((at + own) >> 16);
+    l.tile_count[2 * blockIdx.x] = all;
+    l.tile_count[2 * blockIdx.x + 1] = all - (hist[l.count] + size - 1) / size;
+  }
   for (int j = 0; j < each; ++j) {
     const int g = tid * each + j;
     if (g >= groups) break;
@@ -110,13 +114,11 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
   typedef typename D::elem E;
   __shared__ floatx4 lds[kWaves][SUB * ROWS][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-  for (uint32_t round = blockIdx.x; round < adapter_rounds(l.in_total); round += gridDim.x) {
-    const uint32_t flat = adapter_work(round, l.in_total);
-    if (flat >= l.in_total) continue;
-    const uint32_t above = l.by_parts(flat), tile = l.by_rows(above);
-    const int part = int(flat - above * uint32_t(l.parts)), block = int(above - tile * l.by_rows.by);
-    const TileTokens<SUB> t = find_tile<SUB>(l, tile);
-    if (!t.live || t.id == l.count) continue;
+  for (uint32_t round = blockIdx.x; round < uint32_t(l.windows) * l.in_window.by; round += gridDim.x) {
+    TileTokens<SUB> t;
+    int piece = 0;
+    if (!find_tile<SUB>(l, round, l.in_window, l.in_each, false, t, piece)) continue;
+    const int block = int(l.by_parts(uint32_t(piece))), part = piece - block * l.parts;
     const E* x[SUB];
     const E* a[ROWS];
 #pragma unroll
@@ -129,10 +131,9 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
     // K in units of 64 elements: two instructions, 128 bytes of a row
     const uint32_t units = uint32_t(l.in + 63) / 64;  // times a part's number: below 2^31
     const uint32_t p0 = l.by_parts(units * part), p1 = l.by_parts(units * (part + 1));
-    const int u0 = int(p0 + (p1 - p0) * wave / kWaves);
-    int u1 = int(p0 + (p1 - p0) * (wave + 1) / kWaves);
-    const bool tail = u1 == int(units) && u1 > u0 && l.in % 64 != 0;
-    if (tail) --u1;
+    // the waves take units in turn: 512 bytes of each row are asked for at about the same time
+    const int u0 = int(p0) + wave, u1 = int(min(p1, uint32_t(l.in) / 64));
+    const bool tail = p1 == units && l.in % 64 != 0 && (int(units) - 1 - u0) % kWaves == 0 && u0 < int(units);
     floatx4 acc[SUB][ROWS] = {};
     auto step = [&](const u32x4(&xv)[SUB], const u32x4(&av)[ROWS]) {
 #pragma unroll
@@ -143,16 +144,19 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
     typedef u32x4 __attribute__((aligned(1))) any;
     u32x4 xv[2][SUB] = {}, av[2][ROWS] = {};
     auto fetch = [&](int u) {
+      // both halves of a line next to each other
+      const int k = 64 * u + 8 * q;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = 64 * u + 32 * h + 8 * q;
+      for (int m = 0; m < SUB; ++m)
 #pragma unroll
-        for (int m = 0; m < SUB; ++m) xv[h][m] = gload<any>(x[m] + k);
+        for (int h = 0; h < 2; ++h) xv[h][m] = gload<any>(x[m] + k + 32 * h);
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) av[h][j] = gload<any>(a[j] + k);
-      }
+      for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) av[h][j] = gload<any>(a[j] + k + 32 * h);
     };
-    for (int u = u0 - 1; u < u1; ++u) {  // each unit's loads are a turn ahead of its products
+    if (u0 < u1) fetch(u0);
+    for (int u = u0; u < u1; u += kWaves) {
       u32x4 xn[2][SUB], an[2][ROWS];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -161,15 +165,14 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) an[h][j] = av[h][j];
       }
-      if (u + 1 < u1) fetch(u + 1);
-      if (u < u0) continue;
+      if (u + kWaves < u1) fetch(u + kWaves);
       step(xn[0], an[0]);
       step(xn[1], an[1]);
     }
     if (tail) {
 #pragma nounroll
       for (int h = 0; h < 2; ++h) {
-        const int c = 8 * u1 + 4 * h + q;
+        const int c = 8 * (int(units) - 1) + 4 * h + q;
 #pragma unroll
         for (int m = 0; m < SUB; ++m) xv[0][m] = row_piece<E, true>(x[m], c, l.in);
 #pragma unroll
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_in(Adapters l) {
 
 template <typename D, int SUB, int ROWS>
 hipError_t launch(const Adapters& l, hipStream_t s) {
-  hipLaunchKernelGGL((k_adapters_in<D, SUB, ROWS>), dim3(adapter_grid(l.in_total)), dim3(kThreads), 0, s, l);
+  hipLaunchKernelGGL((k_adapters_in<D, SUB, ROWS>), dim3(adapter_grid(adapter_rounds(l, l.in_window))), dim3(kThreads), 0, s, l);
   return hipGetLastError();
 }
 template <typename D, int SUB>

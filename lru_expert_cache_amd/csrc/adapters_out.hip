@@ -35,31 +35,89 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
   typedef float float8 __attribute__((ext_vector_type(8)));
   typedef float8 __attribute__((aligned(4))) float8_any;
   typedef B base8 __attribute__((ext_vector_type(8)));
-  constexpr bool kHalf = sizeof(E) == 2 && __is_same(E, _Float16);
+  constexpr bool kHalf = __is_same(E, _Float16);
   constexpr int kParts = !kHalf && sizeof(Y) == 4 ? 3 : 2;
-  constexpr int kSteps = KS == 0 ? 1 : KS;                              // of B's pieces
-  constexpr int kFrags = KS == 0 ? (kParts + 1) / 2 : KS * kParts;      // of h's
+  constexpr int kSteps = KS == 0 ? 1 : KS;                          // of B's pieces
+  constexpr int kFrags = KS == 0 ? (kParts + 1) / 2 : KS * kParts;  // of h's
+  constexpr int kBlocks = adapter_out_blocks(sizeof(B), sizeof(Y), SUB), kStep = 32 * kBlocks * kWaves;
   // sums of h: one for each group of 16 tokens and step of ranks, in kGroups shares of the parts of K
   constexpr int kGroups = SUB * kSteps >= kWaves ? 1 : kWaves / (SUB * kSteps), kSlots = SUB * kSteps * kGroups;
-  __shared__ floatx4 lds[kSlots][2][64];
+  // h's operands are kept in LDS where they would take many registers, made by one wave for all
+  constexpr bool kShare = SUB * kFrags > 4;
+  constexpr int kKept = kShare ? 1 : SUB;
+  __shared__ floatx4 sums[kSlots][2][64];
+  __shared__ u32x4 shared_h[kShare ? SUB * kFrags : 1][64];
+  __shared__ float shared_scale[kShare ? SUB : 1][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-  for (uint32_t round = blockIdx.x; round < adapter_rounds(l.out_total); round += gridDim.x) {
-    const uint32_t flat = adapter_work(round, l.out_total);
-    if (flat >= l.out_total) continue;
-    const uint32_t tile = l.by_across(flat);
-    const TileTokens<SUB> t = find_tile<SUB>(l, tile);
-    if (!t.live) continue;
-    const int wide = 128 * l.out_blocks, c0 = int(flat - tile * l.by_across.by) * wide;
-    const int n0 = c0 + 32 * wave, n1 = min(l.out - c0, wide) + c0;
+  for (uint32_t round = blockIdx.x; round < uint32_t(l.windows) * l.out_window.by; round += gridDim.x) {
+    TileTokens<SUB> t;
+    int piece = 0;
+    if (!find_tile<SUB>(l, round, l.out_window, l.out_each, true, t, piece)) continue;
+    const int wide = kStep * l.out_blocks, c0 = piece * wide;
+    const int n0 = c0 + 32 * kBlocks * wave, n1 = min(l.out - c0, wide) + c0;
     const bool on = t.id != l.count;
 
-    u32x4 h[SUB][kFrags] = {};
-    float scale[SUB] = {};
     // The parts of h, added up by the four waves together.  A lane has its
     // token's ranks 8 (q mod 2) .. for KS 0, else 32 step + 8 q ..; a row's
     // last pieces as row_piece takes them of B.
+    u32x4 h[kKept][kFrags] = {};
+    float scale[kKept] = {};
+    auto operands = [&](int m, u32x4(&out)[kFrags], float& factor) {
+      float v[kSteps][8];
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int slot = (m * kSteps + k) * kGroups;
+        floatx4 lo = sums[slot][0][lane], hi = sums[slot][1][lane];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+          lo += sums[slot + g][0][lane];
+          hi += sums[slot + g][1][lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[k][i] = lo[i];
+          v[k][4 + i] = hi[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
+      }
+      factor = l.scale ? gload<float>(l.scale + t.id) : 1.f;
+      if constexpr (kHalf) {
+        // the row's largest value to 2^13 .. 2^14
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const int e = top > 0.f && top < __builtin_huge_valf() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
+        factor = __builtin_ldexpf(factor, -e);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] = __builtin_ldexpf(v[k][i], e);
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        elem8 part[kParts];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float left = v[k][i];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            part[p][i] = E(left);
+            const float is = float(part[p][i]);
+            left = __builtin_isfinite(is) ? left - is : 0.f;
+          }
+        }
+        if constexpr (KS == 0) {
+          out[0] = q < 2 ? (u32x4)part[0] : (u32x4)part[1];
+          if constexpr (kParts == 3) out[1] = q < 2 ? (u32x4)part[2] : u32x4{};
+        } else {
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) out[k * kParts + p] = (u32x4)part[p];
+        }
+      }
+    };
     auto join = [&]() {
-      __syncthreads();  // the last tile's sums have been read
+      __syncthreads();  // the last tile's are done with
 #pragma unroll
       for (int i = 0; i < kSlots / kWaves; ++i) {
         const int slot = wave + kWaves * i, m = slot / kGroups / kSteps, k = slot / kGroups % kSteps;
@@ -84,125 +142,104 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
             }
           }
         }
-        lds[slot][0][lane] = __builtin_shufflevector(sum, sum, 0, 1, 2, 3);
-        lds[slot][1][lane] = __builtin_shufflevector(sum, sum, 4, 5, 6, 7);
+        sums[slot][0][lane] = __builtin_shufflevector(sum, sum, 0, 1, 2, 3);
+        sums[slot][1][lane] = __builtin_shufflevector(sum, sum, 4, 5, 6, 7);
       }
       __syncthreads();
+      if constexpr (kShare) {
+        for (int m = wave; m < SUB; m += kWaves) {
+          u32x4 made[kFrags];
+          float factor;
+          operands(m, made, factor);
 #pragma unroll
-      for (int m = 0; m < SUB; ++m) {
-        float v[kSteps][8];
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const int slot = (m * kSteps + k) * kGroups;
-          floatx4 lo = lds[slot][0][lane], hi = lds[slot][1][lane];
-#pragma unroll
-          for (int g = 1; g < kGroups; ++g) {
-            lo += lds[slot + g][0][lane];
-            hi += lds[slot + g][1][lane];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[k][i] = lo[i];
-            v[k][4 + i] = hi[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
+          for (int f = 0; f < kFrags; ++f) shared_h[m * kFrags + f][lane] = made[f];
+          shared_scale[m][lane] = factor;
         }
-        scale[m] = l.scale ? gload<float>(l.scale + t.id) : 1.f;
-        if constexpr (kHalf) {
-          // the row's largest value to 2^13 .. 2^14
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const int e = top > 0.f && top < __builtin_huge_valf() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-          scale[m] = __builtin_ldexpf(scale[m], -e);
+        __syncthreads();
+      } else {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = __builtin_ldexpf(v[k][i], e);
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          elem8 part[kParts];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float left = v[k][i];
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-              part[p][i] = E(left);
-              const float is = float(part[p][i]);
-              left = __builtin_isfinite(is) ? left - is : 0.f;
-            }
-          }
-          if constexpr (KS == 0) {
-            h[m][0] = q < 2 ? (u32x4)part[0] : (u32x4)part[1];
-            if constexpr (kParts == 3) h[m][1] = q < 2 ? (u32x4)part[2] : u32x4{};
-          } else {
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) h[m][k * kParts + p] = (u32x4)part[p];
-          }
-        }
+        for (int m = 0; m < SUB; ++m) operands(m, h[m], scale[m]);
       }
     };
 
-    // A step's 32 columns: two instructions, whose rows 4 a + i are columns 8 a + 4 j + i: lane (q, token) gets
-    // columns 8 q .. 8 q + 7.
-    u32x4 b[2][kSteps] = {};
-    base8 with[SUB] = {};
+    // A block's 32 columns: two instructions, whose rows 4 a + i are columns 8 a + 4 j + i: lane (q, token) gets
+    // columns 8 q .. 8 q + 7.  A wave takes as many blocks at once as fill a cache line of base and y.
+    u32x4 b[kBlocks][2][kSteps] = {};
+    base8 with[SUB][kBlocks] = {};
     const int mine = 8 * ((lane & 15) >> 2) + (lane & 3);
     auto fetch = [&](int n) {
       if (on) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const E* row = static_cast<const E*>(l.b) + (int64_t(t.id) * l.out + min(n + mine + 4 * j, l.out - 1)) * l.ld_b;
+        for (int w = 0; w < kBlocks; ++w) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) b[j][k] = row_piece<E, false>(row, KS == 0 ? (q & 1) : 4 * k + q, l.rank);
+          for (int j = 0; j < 2; ++j) {
+            const int64_t at = int64_t(t.id) * l.out + min(n + 32 * w + mine + 4 * j, l.out - 1);
+            const E* row = static_cast<const E*>(l.b) + at * l.ld_b;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) b[w][j][k] = row_piece<E, false>(row, KS == 0 ? (q & 1) : 4 * k + q, l.rank);
+          }
         }
       }
       if (l.base) {
-        const int c = n + 8 * q;
 #pragma unroll
         for (int m = 0; m < SUB; ++m) {
           const B* row = static_cast<const B*>(l.base) + int64_t(t.token[m]) * l.ld_base;
           typedef base8 __attribute__((aligned(1))) any;
-          if (c + 8 <= l.out) with[m] = gload<any>(row + c);
-          else with[m] = last_columns(row, c, l.out);
+#pragma unroll
+          for (int w = 0; w < kBlocks; ++w) {
+            const int c = n + 32 * w + 8 * q;
+            if (c + 8 <= l.out) with[m][w] = gload<any>(row + c);
+            else with[m][w] = last_columns(row, c, l.out);
+          }
         }
       }
     };
-    for (int n = n0 - 128; n < n1; n += 128) {  // each step's loads are a turn ahead of its products
-      u32x4 bn[2][kSteps];
-      base8 wn[SUB];
+    for (int n = n0 - kStep; n < n1; n += kStep) {  // each step's loads are a turn ahead of its products
+      u32x4 bn[kBlocks][2][kSteps];
+      base8 wn[SUB][kBlocks];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int w = 0; w < kBlocks; ++w) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) bn[j][k] = b[j][k];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int m = 0; m < SUB; ++m) wn[m] = with[m];
-      if (n + 128 < n1) fetch(n + 128);
+          for (int k = 0; k < kSteps; ++k) bn[w][j][k] = b[w][j][k];
+#pragma unroll
+        for (int m = 0; m < SUB; ++m) wn[m][w] = with[m][w];
+      }
+      if (n + kStep < n1) fetch(n + kStep);
       if (n < n0) {  // the first turn, of every wave
         if (on) join();
         continue;
       }
-      const int c = n + 8 * q;
 #pragma unroll
       for (int m = 0; m < SUB; ++m) {
-        float v[8] = {};
+        u32x4 hm[kFrags];
+        float factor = 0.f;
         if (on) {
-          floatx4 acc[2] = {};
 #pragma unroll
-          for (int f = 0; f < kFrags; ++f)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[j] = D::mfma16(bn[j][KS == 0 ? 0 : f / kParts], h[m][f], acc[j]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[i >> 2][i & 3] * scale[m];
+          for (int f = 0; f < kFrags; ++f) hm[f] = kShare ? shared_h[m * kFrags + f][lane] : h[kShare ? 0 : m][f];
+          factor = kShare ? shared_scale[m][lane] : scale[kShare ? 0 : m];
         }
-        if (l.base) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += float(wn[m][i]);
+        for (int w = 0; w < kBlocks; ++w) {
+          const int c = n + 32 * w + 8 * q;
+          float v[8] = {};
+          if (on) {
+            floatx4 acc[2] = {};
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) acc[j] = D::mfma16(bn[w][j][KS == 0 ? 0 : f / kParts], hm[f], acc[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = acc[i >> 2][i & 3] * factor;
+          }
+          if (l.base) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += float(wn[m][w][i]);
+          }
+          if (16 * m + (lane & 15) < t.count && c < l.out)
+            dense_store<Y, 8>(static_cast<uint8_t*>(l.y), int64_t(t.token[m]) * l.ld_y + c, v, min(8, l.out - c));
         }
-        if (16 * m + (lane & 15) < t.count && c < l.out)
-          dense_store<Y, 8>(static_cast<uint8_t*>(l.y), int64_t(t.token[m]) * l.ld_y + c, v, min(8, l.out - c));
       }
     }
   }
@@ -210,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
 
 template <typename D, typename B, typename Y, int SUB, int KS>
 hipError_t launch(const Adapters& l, hipStream_t s) {
-  hipLaunchKernelGGL((k_adapters_out<D, B, Y, SUB, KS>), dim3(adapter_grid(l.out_total)), dim3(kThreads), 0, s, l);
+  hipLaunchKernelGGL((k_adapters_out<D, B, Y, SUB, KS>), dim3(adapter_grid(adapter_rounds(l, l.out_window))), dim3(kThreads), 0, s, l);
   return hipGetLastError();
 }
 template <typename D, typename B, typename Y>

@@ -5,23 +5,33 @@
 
 namespace ftmoe {
 
-AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count) {
+AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count, int base_bytes,
+                         int out_bytes) {
   AdapterPlan p{};
   const int32_t most = std::min(tokens, kAdapterWindow);
   p.few = tokens <= kAdapterFew;
   p.sub = 1;
-  // larger tiles read an adapter's matrices less often, once an adapter has that many tokens
-  if (rank <= 64 && tokens / 64 >= 4 * count) p.sub = 4;
-  else if (rank <= 64 && tokens / 32 >= 4 * count) p.sub = 2;
+  // Larger tiles read an adapter's matrices less often and leave more places
+  // empty.  Tiles of 16, 32 and 64 tokens, prompts, bf16, us: 512 tokens (in =
+  // out = 7168, rank 64) 26 / 25 / 29; 2048 tokens (2048, rank 16) 22 / 20 /
+  // 22; 8192 tokens (2048, rank 64) 71 / 58 / 58; 8192 tokens (7168, rank 64)
+  // 194 / 137 / 115; 1531 tokens (rank 8, half of them single) 30 / 35 / -.
+  if (rank <= 64 && int64_t(tokens) * (rank > 16 ? 2 : 1) >= 2048 && tokens >= 32 * count) p.sub = 2;
+  if (rank <= 64 && tokens >= 4096 && int64_t(in) + out >= 8192 && tokens >= 64 * count) p.sub = 4;
   p.windows = std::max(1, (tokens + kAdapterWindow - 1) / kAdapterWindow);
   // each adapter (and the tokens that have none) can leave one tile partly filled
   p.tile_cap = int32_t(std::min<int64_t>(most, most / (16 * p.sub) + int64_t(count) + 1));
-  // about two workgroups on each CU; 256 elements of K a part at least
+  // About a workgroup on each CU, so that none waits for a second round (8192
+  // tokens, 7168, rank 64: 42 us with two parts, 52 with three, 43 with four);
+  // 256 elements of K a part at least.  Half of the adapters are taken to have a last tile partly filled.
   const int64_t rows = p.sub == 1 && rank > 64 ? (rank + 63) / 64 : 1;
   const int64_t tiles = int64_t(p.windows) * std::min<int64_t>(p.tile_cap, tokens / (16 * p.sub) + 1 + count / 2) * rows;
-  p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>(512 / tiles, in / 256), 1, 32));
-  const int64_t blocks = (out + 127) / 128;  // of a workgroup's 128 columns
-  p.out_blocks = int32_t(std::clamp<int64_t>(blocks * tiles / 1024, 1, 8));
+  p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>((256 + tiles / 2) / tiles, in / 256), 1, 32));
+  p.out_step = 4 * 32 * adapter_out_blocks(base_bytes, out_bytes, p.sub);
+  // columns for about 1024 workgroups: each joins h's parts first (8192 tokens, 7168, rank 64: steps of 256 columns
+  // 1 / 2 / 4 / 7 a workgroup: 132 / 118 / 115 / 128 us for the call)
+  const int64_t blocks = (out + p.out_step - 1) / p.out_step;
+  p.out_blocks = int32_t(std::clamp<int64_t>((blocks * tiles + 512) / 1024, 1, 8));
   // (numbers of workgroups stay below 2^30)
   const int64_t all = int64_t(p.windows) * p.tile_cap;
   p.out_blocks = int32_t(std::max<int64_t>(p.out_blocks, (all * blocks >> 30) + 1));
