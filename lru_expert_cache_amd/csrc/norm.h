@@ -18,13 +18,18 @@ struct NormForward {
 struct NormBackward {
   const void *sum, *weight, *dy, *dsum;  // dsum: null for 0
   void *dx, *dresidual;                  // null: not wanted
-  float* part;                           // [groups][cols]: sums of dy s r over each group's rows, null: not wanted
+  float* part;                           // [groups][norm_part_ld]: sums of dy s r over each group's rows, null: not wanted
   float* stats;                          // rows that no workgroup holds: r and mean(g s r) of each
   int64_t ld_sum, ld_y, ld_residual, ld_x;
   int32_t rows, cols, groups;
   double eps;
 };
 
+// floats between two groups' parts: whole 16-byte pieces
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline int64_t norm_part_ld(int32_t cols) { return (int64_t(cols) + 3) / 4 * 4; }
 // groups of rows whose weight gradients are summed apart
 int norm_groups(int32_t rows, int32_t cols);
 

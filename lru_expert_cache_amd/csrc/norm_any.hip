@@ -70,22 +70,35 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad_any(NormBackward a) {
     if (a.dresidual) gstore<R>(static_cast<R*>(a.dresidual) + row * a.ld_residual + c, R(ds));
     dw = fmaf(dy, n, dw);
   }
-  if (a.part) a.part[int64_t(blockIdx.y) * a.cols + c] = dw;
+  if (a.part) a.part[int64_t(blockIdx.y) * norm_part_ld(a.cols) + c] = dw;
 }
 
+// 32 columns a workgroup: eight lanes have four each, 128 groups of lanes every 128th part.
+constexpr int kJoin = 1024;
 template <typename X>
-__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int groups, int cols, X* dweight) {
-  __shared__ float lds[16][64];
-  const int lane = threadIdx.x & 63, g0 = threadIdx.x >> 6;
-  const int c = int(blockIdx.x) * 64 + lane;
-  float t = 0.f;
-  if (c < cols)
-    for (int g = g0; g < groups; g += 16) t += part[int64_t(g) * cols + c];
-  lds[g0][lane] = t;
+__global__ __launch_bounds__(kJoin) void k_norm_join(const float* part, int groups, int cols, X* dweight) {
+  typedef float floatx4 __attribute__((ext_vector_type(4)));
+  __shared__ floatx4 lds[kJoin / 64][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t ld = norm_part_ld(cols);
+  const int c0 = 32 * int(blockIdx.x), c = c0 + 4 * (tid & 7);
+  floatx4 t{};
+  if (c < cols) {
+#pragma unroll 4
+    for (int g = tid >> 3; g < groups; g += kJoin / 8) t += gload<floatx4>(part + g * ld + c);
+  }
+#pragma unroll
+  for (int o = 8; o < 64; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] += __shfl_xor(t[i], o);
+  }
+  if (lane < 8) lds[wave][lane] = t;
   __syncthreads();
-  if (g0 == 0 && c < cols) {
-    for (int g = 1; g < 16; ++g) t += lds[g][lane];
-    gstore<X>(dweight + c, X(t));
+  if (tid < 32 && c0 + tid < cols) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoin / 64; ++w) v += lds[w][tid >> 2][tid & 3];
+    gstore<X>(dweight + c0 + tid, X(v));
   }
 }
 
@@ -126,14 +139,14 @@ hipError_t launch_norm_backward(int dtype, int residual_dtype, const NormBackwar
 }
 
 hipError_t launch_norm_join(int dtype, const float* part, int32_t groups, int32_t cols, void* dweight, hipStream_t s) {
-  const dim3 grid(uint32_t((cols + 63) / 64));
+  const dim3 grid(uint32_t((cols + 31) / 32));
   if (dtype == FT_DT_F32)
-    hipLaunchKernelGGL((k_norm_join<float>), grid, dim3(1024), 0, s, part, groups, cols, static_cast<float*>(dweight));
+    hipLaunchKernelGGL((k_norm_join<float>), grid, dim3(kJoin), 0, s, part, groups, cols, static_cast<float*>(dweight));
   else if (dtype == FT_DT_F16)
-    hipLaunchKernelGGL((k_norm_join<_Float16>), grid, dim3(1024), 0, s, part, groups, cols,
+    hipLaunchKernelGGL((k_norm_join<_Float16>), grid, dim3(kJoin), 0, s, part, groups, cols,
                        static_cast<_Float16*>(dweight));
   else
-    hipLaunchKernelGGL((k_norm_join<__bf16>), grid, dim3(1024), 0, s, part, groups, cols, static_cast<__bf16*>(dweight));
+    hipLaunchKernelGGL((k_norm_join<__bf16>), grid, dim3(kJoin), 0, s, part, groups, cols, static_cast<__bf16*>(dweight));
   return hipGetLastError();
 }
 
