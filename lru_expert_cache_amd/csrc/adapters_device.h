@@ -65,9 +65,12 @@ __device__ __attribute__((always_inline)) inline bool find_tile(const Adapters& 
   if constexpr (SUB == 1)
     if (l.few) return few_tile(l, round, each, bare, t, piece);
   const uint32_t w = window(round);
-  const uint32_t pieces = uint32_t(gload<int32_t>(l.tile_count + 2 * w + (bare ? 0 : 1))) * each.by;
-  const uint32_t work = xcd_piece(round - w * window.by, pieces);
-  if (work >= pieces) return false;
+  // tiles without an adapter are less work: the XCDs share the others first, and then these
+  const uint32_t pieces = uint32_t(gload<int32_t>(l.tile_count + 2 * w + 1)) * each.by;
+  const uint32_t all = bare ? uint32_t(gload<int32_t>(l.tile_count + 2 * w)) * each.by : pieces;
+  const uint32_t at = round - w * window.by, full = (pieces + kXcds - 1) / kXcds * kXcds;
+  const uint32_t work = at < full ? xcd_piece(at, pieces) : pieces + xcd_piece(at - full, all - pieces);
+  if (work >= (at < full ? pieces : all)) return false;
   const uint32_t item = each(work);
   piece = int(work - item * each.by);
   static_assert(sizeof(AdapterTile) == 16, "one load");

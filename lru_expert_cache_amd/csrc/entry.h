@@ -67,6 +67,7 @@ struct DeviceGuard {
     dev = cur;
     if (s) FT_HIP_CHECK(hipStreamGetDevice(s, &dev));
     for (const Arg& a : args) {
+      if (&a != args.begin() && a.p == args.begin()->p) continue;  // (arguments that are not there)
       hipPointerAttribute_t at;
       if (hipPointerGetAttributes(&at, a.p) != hipSuccess) {
         (void)hipGetLastError();

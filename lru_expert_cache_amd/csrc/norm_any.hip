@@ -12,7 +12,8 @@ constexpr int kThreads = 256;
 template <typename X, typename R>
 __global__ __launch_bounds__(kThreads) void k_norm_any(NormForward a) {
   __shared__ double lds[3 * kThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = int64_t(blockIdx.y) * kNormGrid + blockIdx.x;
+  if (row >= a.rows) return;
   const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
   const R* residual = a.residual ? static_cast<const R*>(a.residual) + row * a.ld_residual : nullptr;
   const X* weight = static_cast<const X*>(a.weight);
@@ -37,7 +38,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_any(NormForward a) {
 template <typename X, typename R>
 __global__ __launch_bounds__(kThreads) void k_norm_stats_any(NormBackward a) {
   __shared__ double lds[2 * kThreads / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = int64_t(blockIdx.y) * kNormGrid + blockIdx.x;
+  if (row >= a.rows) return;
   const R* sum = static_cast<const R*>(a.sum) + row * a.ld_sum;
   const X* dy = static_cast<const X*>(a.dy) + row * a.ld_y;
   const X* weight = static_cast<const X*>(a.weight);
@@ -104,13 +106,13 @@ __global__ __launch_bounds__(kJoin) void k_norm_join(const float* part, int grou
 
 template <typename X, typename R>
 hipError_t launch(const NormForward& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_any<X, R>), dim3(uint32_t(a.rows)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_norm_any<X, R>), norm_grid(a.rows), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename X, typename R>
 hipError_t launch(const NormBackward& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_stats_any<X, R>), dim3(uint32_t(a.rows)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_norm_stats_any<X, R>), norm_grid(a.rows), dim3(kThreads), 0, s, a);
   const uint32_t across = uint32_t((a.cols + kThreads - 1) / kThreads);
   hipLaunchKernelGGL((k_norm_grad_any<X, R>), dim3(across, uint32_t(a.groups)), dim3(kThreads), 0, s, a);
   return hipGetLastError();

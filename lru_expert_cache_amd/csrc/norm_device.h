@@ -13,6 +13,12 @@
 
 namespace ftmoe {
 
+// a workgroup for each row, as many across as any workgroup size allows
+constexpr int32_t kNormGrid = 1 << 21;
+inline dim3 norm_grid(int32_t rows) {
+  return dim3(uint32_t(rows < kNormGrid ? rows : kNormGrid), uint32_t((rows + kNormGrid - 1) / kNormGrid));
+}
+
 __device__ __attribute__((always_inline)) inline double wave_add(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);

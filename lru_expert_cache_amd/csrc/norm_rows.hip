@@ -17,8 +17,6 @@ namespace ftmoe {
 
 namespace {
 
-typedef float floatx8 __attribute__((ext_vector_type(8)));
-
 template <typename E>
 struct Piece {
   typedef E elems __attribute__((ext_vector_type(8)));
@@ -42,7 +40,8 @@ template <typename X, typename R, int THREADS, int PIECES>
 __global__ __launch_bounds__(THREADS) void k_norm(NormForward a) {
   __shared__ double lds[3 * (THREADS / 64)];
   const X* weight = static_cast<const X*>(a.weight);
-  const int64_t row = blockIdx.x;
+  const int64_t row = int64_t(blockIdx.y) * kNormGrid + blockIdx.x;
+  if (row >= a.rows) return;
   const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
   const R* residual = static_cast<const R*>(a.residual) + row * a.ld_residual;
   Piece<X> xv[PIECES], wv[PIECES];
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
 
 template <typename X, typename R, int THREADS, int PIECES>
 hipError_t launch(const NormForward& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm<X, R, THREADS, PIECES>), dim3(uint32_t(a.rows)), dim3(THREADS), 0, s, a);
+  hipLaunchKernelGGL((k_norm<X, R, THREADS, PIECES>), norm_grid(a.rows), dim3(THREADS), 0, s, a);
   return hipGetLastError();
 }
 template <typename X, typename R, int THREADS, int PIECES>
