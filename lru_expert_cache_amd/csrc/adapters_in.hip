@@ -16,18 +16,29 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
   __shared__ uint32_t sums[kPlanThreads / 64];
   int* hist = lds;                                               // [count + 1]
   uint32_t* before = reinterpret_cast<uint32_t*>(lds) + l.count + 1;  // [count + 1]: tokens, and tiles above
-  const int tid = threadIdx.x, lane = tid & 63, groups = l.count + 1, size = 16 * l.sub;
+  const int tid = threadIdx.x, lane = tid & 63, groups = l.count + 1;
+  const int size = 16 * l.sub, shift = l.sub == 1 ? 4 : l.sub == 2 ? 5 : 6;  // tokens of a tile, a power of two
   const int64_t t0 = int64_t(blockIdx.x) * kAdapterWindow;
   const int tokens = int(min(int64_t(kAdapterWindow), l.tokens - t0));
   for (int g = tid; g < groups; g += kPlanThreads) hist[g] = 0;
+  // eight tokens a thread, in two loads where they are all there
   int group[kEach], place[kEach];
+  {
+    static_assert(kEach == 8, "two loads");
+    typedef int intx4_any __attribute__((ext_vector_type(4), aligned(4)));
+    const int32_t* ids = l.ids + t0 + kEach * tid;
+    if (kEach * tid + kEach <= tokens) {
+      const intx4_any a = gload<intx4_any>(ids), b = gload<intx4_any>(ids + 4);
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int t = kEach * tid + i;
-    group[i] = -1;
-    if (t < tokens) {
-      const int id = gload<int32_t>(l.ids + t0 + t);
-      group[i] = uint32_t(id) < uint32_t(l.count) ? id : l.in_place ? -1 : l.count;
+      for (int i = 0; i < kEach; ++i) group[i] = i < 4 ? a[i & 3] : b[i & 3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) group[i] = kEach * tid + i < tokens ? gload<int32_t>(ids + i) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool bare = uint32_t(group[i]) >= uint32_t(l.count);
+      group[i] = kEach * tid + i >= tokens || (bare && l.in_place) ? -1 : bare ? l.count : group[i];
     }
   }
   __syncthreads();
@@ -69,7 +80,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
   uint32_t own = 0;
   for (int j = 0; j < each; ++j) {
     const int g = tid * each + j, c = g < groups ? hist[g] : 0;
-    own += uint32_t(c) + (uint32_t((c + size - 1) / size) << 16);
+    own += uint32_t(c) + (uint32_t((c + size - 1) >> shift) << 16);
   }
   uint32_t sum = own;
 #pragma unroll
@@ -84,14 +95,14 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
   if (tid == kPlanThreads - 1) {
     const int all = int((at + own) >> 16);
     l.tile_count[2 * blockIdx.x] = all;
-    l.tile_count[2 * blockIdx.x + 1] = all - (hist[l.count] + size - 1) / size;
+    l.tile_count[2 * blockIdx.x + 1] = all - ((hist[l.count] + size - 1) >> shift);
   }
   for (int j = 0; j < each; ++j) {
     const int g = tid * each + j;
     if (g >= groups) break;
     before[g] = at;
     const int c = hist[g];
-    at += uint32_t(c) + (uint32_t((c + size - 1) / size) << 16);
+    at += uint32_t(c) + (uint32_t((c + size - 1) >> shift) << 16);
   }
   __syncthreads();
 #pragma unroll
@@ -101,8 +112,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_adapters_plan(Adapters l) {
     const uint32_t b = before[g];
     const int first = int(t0) + int(b & 0xFFFF) + place[i];
     l.order[first] = int(t0) + kEach * tid + i;
-    if (place[i] % size == 0)
-      l.tiles[int64_t(blockIdx.x) * l.tile_cap + (b >> 16) + place[i] / size] = {g, first, min(size, hist[g] - place[i]), 0};
+    if ((place[i] & (size - 1)) == 0)
+      l.tiles[int64_t(blockIdx.x) * l.tile_cap + (b >> 16) + (place[i] >> shift)] = {g, first, min(size, hist[g] - place[i]), 0};
   }
 }
 
