@@ -80,8 +80,36 @@ def test_sums_beyond_fp16s_range(x, a, scale):
     ac.check(c.apply(), c.reference())
 
 
-def test_in_place():
-    c = ac.Adapters(90, 256, 300, 16, 4, pad=8)
+@pytest.mark.parametrize("type_,base,out", FORMS)
+@pytest.mark.parametrize("size", [(8500, 4200, 4100, 40, 3), (4100, 6000, 2203, 5, 2), (4096, 4104, 4096, 64, 20)])
+def test_large_tiles(size, type_, base, out):
+    """Tiles of 64 tokens, several windows, odd widths."""
+    c = ac.Adapters(*size, type_, base, out)
+    c.ids = torch.sort(c.ids).values.contiguous()  # long runs
+    ac.check(c.apply(), c.reference(), "y")
+
+
+def test_more_work_than_a_launch_has_workgroups():
+    """Many windows, each with room for thousands of adapters: workgroups go round; rows picked from all over."""
+    T, N, n = 300_000, 51_200, 4096
+    g = ac.gen(1)
+    x, a = torch.randn(T, 8, generator=g, device="cuda").to(torch.bfloat16), torch.randn(n, 1, 8, generator=g, device="cuda").to(torch.bfloat16)
+    b = torch.randn(n, N, 1, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(-1, n, (T,), generator=g, device="cuda").to(torch.int32)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    d = ft.make_adapters(ft.FT_DT_BF16, T, 8, N, 1, n)
+    ft.ft_moe_adapters_apply(d, x, ids, a, b, None, None, y, torch.empty(ft.ft_moe_adapters_work(d), dtype=torch.uint8, device="cuda"))
+    at = torch.cat([torch.tensor([0, 1, 8191, 8192, T - 1], device="cuda"), torch.randint(0, T, (60,), generator=g, device="cuda")])
+    i = ids[at].long()
+    h = (x[at].double() * a[i, 0].double()).sum(1)
+    v = torch.where((i >= 0)[:, None], h[:, None] * b[i, :, 0].double(), 0.0)
+    hm = (x[at].double() * a[i, 0].double()).abs().sum(1)[:, None] * b[i, :, 0].double().abs()
+    ac.check(y[at], (v, ac.rounded(v, y.dtype, hm * (10 * 2 * ac.E + 2.0**-17 + 14 * ac.E))), "y")
+
+
+@pytest.mark.parametrize("T", [40, 90, 5000])
+def test_in_place(T):
+    c = ac.Adapters(T, 256, 300, 16, 4, pad=8)
     y, before = c.apply(), c.base.clone()
     ft.ft_moe_adapters_apply(c.d, c.x, c.ids, c.a, c.b, c.scale, c.base, c.base, c.work())
     assert torch.equal(c.base, y)

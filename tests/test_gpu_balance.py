@@ -166,3 +166,17 @@ def test_in_place():
     dz = b.backward(f)
     ft.ft_moe_balance_backward(b.d, b.z, b.valid, f["sel"], f["w"], f["counts"], b.dw, b.dloss, b.z)
     assert torch.equal(b.z, dz)
+
+
+def test_rows_beyond_4_gb():
+    """Offsets of more than 32 bits: rows far apart."""
+    b = ac.Balance(40, 100, 4)
+    f = b.forward()
+    dz, ld = b.backward(f), 1 << 25
+    assert 39 * ld * 4 > 2**32
+    b.z = torch.as_strided(torch.empty(39 * ld + 100, device="cuda"), (40, 100), (ld, 1)).copy_(b.z)
+    b.d.ld_logits = ld
+    f2 = b.forward()
+    assert all(torch.equal(f[k], f2[k]) for k in f)
+    ft.ft_moe_balance_backward(b.d, b.z, b.valid, f["sel"], f["w"], f["counts"], b.dw, b.dloss, b.z)
+    assert torch.equal(b.z, dz)

@@ -174,3 +174,30 @@ def test_rows_at_odd_addresses():
         n.x, n.residual = x, res
         got, ref = n.forward(), n.forward_reference()
         _check_forward(n, got, ref)
+
+
+@pytest.mark.parametrize("cols", [3, 8])
+def test_millions_of_rows(cols):
+    n = ac.Norm((1 << 21) + 3, cols)
+    got, ref = n.forward(), n.forward_reference()
+    _check_forward(n, got, ref)
+    got, ref = n.backward(), n.backward_reference()
+    for k, v in ref.items():
+        ac.check(got[k], v, k)
+
+
+def test_rows_beyond_4_gb():
+    """Offsets of more than 32 bits: rows far apart."""
+    n = ac.Norm(40, 300)
+    fwd, bwd, ld = n.forward(), n.backward(), 1 << 26
+    far = lambda v: torch.as_strided(torch.empty(39 * ld + 300, dtype=v.dtype, device="cuda"), (40, 300), (ld, 1)).copy_(v)  # noqa: E731
+    assert 39 * ld * 2 > 2**32
+    y = far(n.x)
+    n.d.ld_x = n.d.ld_y = n.d.ld_residual = n.d.ld_sum = n.d.ld_codes = ld
+    x, res = far(n.x), far(n.residual)
+    codes, scale = far(fwd["codes"] * 0), torch.empty(40, device="cuda")
+    ft.ft_moe_rms_norm_forward(n.d, x, res, n.weight, res, y, codes, scale)
+    assert torch.equal(res, fwd["sum"]) and torch.equal(y, fwd["y"]) and torch.equal(codes, fwd["codes"])
+    s, dy, dsum = far(n.s), far(n.dy), far(n.dsum)
+    ft.ft_moe_rms_norm_backward(n.d, s, n.weight, dy, dsum, dy, dsum, None, n.work())
+    assert torch.equal(dy, bwd["dx"]) and torch.equal(dsum, bwd["dresidual"])
