@@ -64,17 +64,26 @@ __device__ __attribute__((always_inline)) inline bool find_tile(const Adapters& 
                                                                 bool bare, TileTokens<SUB>& t, int& piece) {
   if constexpr (SUB == 1)
     if (l.few) return few_tile(l, round, each, bare, t, piece);
-  const uint32_t w = window(round);
-  // tiles without an adapter are less work: the XCDs share the others first, and then these
-  const uint32_t pieces = uint32_t(gload<int32_t>(l.tile_count + 2 * w + 1)) * each.by;
-  const uint32_t all = bare ? uint32_t(gload<int32_t>(l.tile_count + 2 * w)) * each.by : pieces;
-  const uint32_t at = round - w * window.by, full = (pieces + kXcds - 1) / kXcds * kXcds;
-  const uint32_t work = at < full ? xcd_piece(at, pieces) : pieces + xcd_piece(at - full, all - pieces);
-  if (work >= (at < full ? pieces : all)) return false;
-  const uint32_t item = each(work);
-  piece = int(work - item * each.by);
+  const uint32_t w = window(round), at = round - w * window.by;
+  uint32_t item;
+  if constexpr (SUB == 1) {
+    // few tokens for each adapter, whose matrices are not met again: tiles as they come, looked up without waiting
+    item = each(at);
+    piece = int(at - item * each.by);
+    if (item >= uint32_t(l.tile_cap)) return false;
+  } else {
+    // tiles without an adapter are less work: the XCDs share the others first, and then these
+    const uint32_t pieces = uint32_t(gload<int32_t>(l.tile_count + 2 * w + 1)) * each.by;
+    const uint32_t all = bare ? uint32_t(gload<int32_t>(l.tile_count + 2 * w)) * each.by : pieces;
+    const uint32_t full = (pieces + kXcds - 1) / kXcds * kXcds;
+    const uint32_t work = at < full ? xcd_piece(at, pieces) : pieces + xcd_piece(at - full, all - pieces);
+    if (work >= (at < full ? pieces : all)) return false;
+    item = each(work);
+    piece = int(work - item * each.by);
+  }
   static_assert(sizeof(AdapterTile) == 16, "one load");
   const u32x4 v = gload<u32x4>(l.tiles + int64_t(w) * l.tile_cap + item);  // id, first, count
+  if (SUB == 1 && int(item) >= gload<int32_t>(l.tile_count + 2 * w + (bare ? 0 : 1))) return false;
   t.id = __builtin_amdgcn_readfirstlane(int(v[0]));
   t.count = __builtin_amdgcn_readfirstlane(int(v[2]));
 #pragma unroll

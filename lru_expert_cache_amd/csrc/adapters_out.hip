@@ -56,6 +56,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
     const int wide = kStep * l.out_blocks, c0 = piece * wide;
     const int n0 = c0 + 32 * kBlocks * wave, n1 = min(l.out - c0, wide) + c0;
     const bool on = t.id != l.count;
+    const float given = on && l.scale ? gload<float>(l.scale + t.id) : 1.f;
 
     // The parts of h, added up by the four waves together.  A lane has its
     // token's ranks 8 (q mod 2) .. for KS 0, else 32 step + 8 q ..; a row's
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
       }
-      factor = l.scale ? gload<float>(l.scale + t.id) : 1.f;
+      factor = given;
       if constexpr (kHalf) {
         // the row's largest value to 2^13 .. 2^14
         top = fmaxf(top, __shfl_xor(top, 16));
