@@ -7,7 +7,6 @@ using namespace ftmoe;
 namespace {
 
 constexpr int32_t kMaxRank = 256;
-constexpr int32_t kMaxAdapters = 4096;  // counters of the grouping, in LDS
 
 int check_adapters(const ft_moe_adapters* d, ft_moe_adapters& o) {
   if (!d) return bad("NULL description");

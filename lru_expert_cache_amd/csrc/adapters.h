@@ -12,6 +12,7 @@
 
 namespace ftmoe {
 
+constexpr int32_t kMaxAdapters = 4096;  // counters of the grouping, in LDS
 // Tokens are grouped within windows of this many.
 constexpr int32_t kAdapterWindow = 8192;
 // Up to this many, each wave finds its tile by itself; else a launch of its own writes down the tiles.

@@ -26,7 +26,7 @@ __device__ __attribute__((always_inline)) inline uint32_t xcd_piece(uint32_t at,
 
 // The tile of round `at` among up to 64 tokens, and which of its `each` pieces
 // of work.  The wave holds a token's id in each lane and counts, for each
-// token, those of the same adapter before it; every 16th of an adapter begins a tile.
+// token, those of the same adapter before it; every 16th begins a tile.
 __device__ __attribute__((always_inline)) inline bool few_tile(const Adapters& l, uint32_t at, FastDiv each, bool bare,
                                                                TileTokens<1>& t, int& piece) {
   const int lane = threadIdx.x & 63;
@@ -35,11 +35,17 @@ __device__ __attribute__((always_inline)) inline bool few_tile(const Adapters& l
     const int id = gload<int32_t>(l.ids + lane);
     group = uint32_t(id) < uint32_t(l.count) ? id : bare && !l.in_place ? l.count : -1;
   }
-  int rank = 0;
-  for (int j = 0; j < l.tokens; ++j) {
-    const int other = __builtin_amdgcn_readlane(group, j);
-    rank += (other == group) & (j < lane);
+  // lanes of the same adapter, bit by bit of its number (13 bits, those of "none" all ones): a comparison with one
+  // token after the other took 2 us for 64 tokens
+  uint64_t same = ~uint64_t(0);
+#pragma unroll
+  for (int b = 0; b < 13; ++b) {
+    const bool bit = group >> b & 1;
+    const uint64_t set = __ballot(bit);  // of every lane, whatever its own bit
+    same &= bit ? set : ~set;
   }
+  static_assert(kMaxAdapters < (1 << 13) - 1, "numbers of 13 bits");
+  const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
   const bool start = group >= 0 && rank % 16 == 0;
   const uint64_t starts = __ballot(start);
   const uint32_t pieces = uint32_t(__popcll(starts)) * each.by, work = xcd_piece(at, pieces);
