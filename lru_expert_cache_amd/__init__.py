@@ -249,9 +249,7 @@ def _check(rc: int, allow_warn: bool = False) -> int:
 def _ptr(t) -> int:
     if t is None:
         return 0
-    if isinstance(t, int):
-        return t
-    return int(t.data_ptr())
+    return t if isinstance(t, int) else t.data_ptr()
 
 
 def make_config(num_layers, hidden, inter, num_experts, top_k, layer_fmt: Sequence[int], pool_slots=0,
