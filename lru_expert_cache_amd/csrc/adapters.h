@@ -69,8 +69,8 @@ struct Adapters {
 // bytes of a row of base and y, whose halves would else be asked for by two
 // waves (adapters of rank 64, 8192 tokens: half as many requests to the L2
 // cache); one where they would take too many registers.
-constexpr int adapter_out_blocks(int base_bytes, int out_bytes, int sub) {
-  return out_bytes == 4 || (base_bytes == 4 && sub == 4) ? 1 : 2;
+constexpr int adapter_out_blocks(int base_bytes, int out_bytes, int sub, int rank) {
+  return out_bytes == 4 || (base_bytes == 4 && sub == 4) || rank > 64 ? 1 : 2;
 }
 
 // How a call is cut: a rule on sizes and types alone.

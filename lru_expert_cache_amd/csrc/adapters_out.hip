@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
   constexpr int kParts = !kHalf && sizeof(Y) == 4 ? 3 : 2;
   constexpr int kSteps = KS == 0 ? 1 : KS;                          // of B's pieces
   constexpr int kFrags = KS == 0 ? (kParts + 1) / 2 : KS * kParts;  // of h's
-  constexpr int kBlocks = adapter_out_blocks(sizeof(B), sizeof(Y), SUB), kStep = 32 * kBlocks * kWaves;
+  constexpr int kBlocks = adapter_out_blocks(sizeof(B), sizeof(Y), SUB, 32 * KS), kStep = 32 * kBlocks * kWaves;
   // sums of h: one for each group of 16 tokens and step of ranks, in kGroups shares of the parts of K
   constexpr int kGroups = SUB * kSteps >= kWaves ? 1 : kWaves / (SUB * kSteps), kSlots = SUB * kSteps * kGroups;
   // h's operands are kept in LDS where they would take many registers, made by one wave for all
@@ -264,7 +264,8 @@ hipError_t launch_form(const Adapters& l, hipStream_t s) {
   if (l.sub == 2) {
     if (ks == 0) return launch<D, B, Y, 2, 0>(l, s);
     if (ks == 1) return launch<D, B, Y, 2, 1>(l, s);
-    return launch<D, B, Y, 2, 2>(l, s);
+    if (ks == 2) return launch<D, B, Y, 2, 2>(l, s);
+    return launch<D, B, Y, 2, 4>(l, s);
   }
   if (ks == 0) return launch<D, B, Y, 4, 0>(l, s);
   if (ks == 1) return launch<D, B, Y, 4, 1>(l, s);

@@ -16,7 +16,7 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   // out = 7168, rank 64) 26 / 25 / 29; 2048 tokens (2048, rank 16) 22 / 20 /
   // 22; 8192 tokens (2048, rank 64) 71 / 58 / 58; 8192 tokens (7168, rank 64)
   // 194 / 137 / 115; 1531 tokens (rank 8, half of them single) 30 / 35 / -.
-  if (rank <= 64 && int64_t(tokens) * (rank > 16 ? 2 : 1) >= 2048 && tokens >= 32 * count) p.sub = 2;
+  if (rank <= 128 && int64_t(tokens) * (rank > 16 ? 2 : 1) >= 2048 && tokens >= 32 * count) p.sub = 2;
   if (rank <= 64 && tokens >= 4096 && int64_t(in) + out >= 8192 && tokens >= 64 * count) p.sub = 4;
   p.windows = std::max(1, (tokens + kAdapterWindow - 1) / kAdapterWindow);
   // each adapter (and the tokens that have none) can leave one tile partly filled
@@ -24,10 +24,10 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   // About a workgroup on each CU, so that none waits for a second round (8192
   // tokens, 7168, rank 64: 42 us with two parts, 52 with three, 43 with four);
   // 256 elements of K a part at least.  Half of the adapters are taken to have a last tile partly filled.
-  const int64_t rows = p.sub == 1 && rank > 64 ? (rank + 63) / 64 : 1;
+  const int64_t rows = (rank + 63) / 64;
   const int64_t tiles = int64_t(p.windows) * std::min<int64_t>(p.tile_cap, tokens / (16 * p.sub) + 1 + count / 2) * rows;
   p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>((256 + tiles / 2) / tiles, in / 256), 1, 32));
-  p.out_step = 4 * 32 * adapter_out_blocks(base_bytes, out_bytes, p.sub);
+  p.out_step = 4 * 32 * adapter_out_blocks(base_bytes, out_bytes, p.sub, rank);
   // columns for about 1024 workgroups: each joins h's parts first (8192 tokens, 7168, rank 64: steps of 256 columns
   // 1 / 2 / 4 / 7 a workgroup: 132 / 118 / 115 / 128 us for the call)
   const int64_t blocks = (out + p.out_step - 1) / p.out_step;

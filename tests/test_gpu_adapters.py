@@ -81,9 +81,10 @@ def test_sums_beyond_fp16s_range(x, a, scale):
 
 
 @pytest.mark.parametrize("type_,base,out", FORMS)
-@pytest.mark.parametrize("size", [(8500, 4200, 4100, 40, 3), (4100, 6000, 2203, 5, 2), (4096, 4104, 4096, 64, 20)])
+@pytest.mark.parametrize("size", [(8500, 4200, 4100, 40, 3), (4100, 6000, 2203, 5, 2), (4096, 4104, 4096, 64, 20), (2100, 520, 1030, 100, 3),
+                                  (1030, 70, 260, 128, 2), (3000, 300, 260, 30, 5)])
 def test_large_tiles(size, type_, base, out):
-    """Tiles of 64 tokens, several windows, odd widths."""
+    """Tiles of 64 and 32 tokens, several windows, odd widths."""
     c = ac.Adapters(*size, type_, base, out)
     c.ids = torch.sort(c.ids).values.contiguous()  # long runs
     ac.check(c.apply(), c.reference(), "y")
