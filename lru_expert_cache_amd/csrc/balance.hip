@@ -102,7 +102,7 @@ struct Logits {
       p[j] = lane + 64 * j < experts ? e : 0.f;
       sum += p[j];
     }
-    sum = 1.f / wave_sum(sum);
+    sum = __builtin_amdgcn_rcpf(wave_sum(sum));  // 1 or more; off by a unit
 #pragma unroll
     for (int j = 0; j < J; ++j) p[j] *= sum;
   }
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   __shared__ float lds_p[kWaves][64 * J];
   __shared__ int lds_c[64 * J];
   __shared__ int lds_v;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // addresses of rows: scalar
   for (int e = threadIdx.x; e < 64 * J; e += 64 * kWaves) lds_c[e] = 0;
   if (threadIdx.x == 0) {
     lds_v = 0;
@@ -125,11 +125,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
   const int64_t step = int64_t(a.groups) * kWaves;
   Logits<X, J> next;
   bool next_on = true;
-  auto fetch = [&](int64_t t) {
-    next.load(static_cast<const X*>(a.logits) + t * a.ld, a.experts, lane);
-    next_on = !a.valid || gload<uint8_t>(a.valid + t);
-  };
   int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+  const X* row = static_cast<const X*>(a.logits) + t * a.ld;
+  int32_t* sel = a.sel + t * a.top_k;
+  float* w = a.w + t * a.top_k;
+  auto fetch = [&](int64_t t) {
+    next.load(row, a.experts, lane);
+    next_on = !a.valid || gload<uint8_t>(a.valid + t);
+    row += step * a.ld;
+  };
   if (t < a.tokens) fetch(t);
   for (; t < a.tokens; t += step) {
     const Logits<X, J> l = next;
@@ -189,11 +193,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
       if (mine >= 0) atomicAdd(&lds_c[mine], 1);
     }
     const float ex = mine >= 0 ? exp_of(logit_of(mine_key) - logit_of(first)) : 0.f;
-    const float sum = wave_sum(ex);
+    const float sum = __builtin_amdgcn_rcpf(wave_sum(ex));
     if (lane < a.top_k) {
-      a.sel[t * a.top_k + lane] = mine;
-      a.w[t * a.top_k + lane] = mine >= 0 ? ex / sum : 0.f;
+      sel[lane] = mine;
+      w[lane] = mine >= 0 ? ex * sum : 0.f;
     }
+    sel += step * a.top_k;
+    w += step * a.top_k;
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) lds_p[wave][lane + 64 * j] = sums[j];
@@ -282,7 +288,7 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(BalanceForward a) {
 template <typename X, int J>
 __global__ __launch_bounds__(64 * kBackWaves) void k_balance_backward(BalanceBackward a) {
   __shared__ float lds[kBackWaves][64 * J];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float c[J];
   {
     const double v = double(a.counts[a.experts]);
