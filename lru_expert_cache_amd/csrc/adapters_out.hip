@@ -5,6 +5,14 @@
 // off, against y's own 2^-9) and three for a 32-bit one, fp16 two (22 bits),
 // with each token's row brought into fp16's range by a power of two.  Up to
 // rank 16, two parts are one instruction of 32 ranks.
+//
+// Bound by reading base and writing y: 8192 tokens, N 7168, bf16: 68 us at
+// rank 64, 60 at rank 16, 58 with no adapter at all (235 MB; 48 at a copy's
+// rate, whose rows lie side by side); a 32-bit base 90, a 32-bit y too 124.
+// 32 tokens of 32 adapters, N 6144, rank 16: 6.5 us, latency (ids, h, B and
+// base one after the other).  Not kept: a wave for 16 tokens and no LDS (97
+// us: too little of base on its way), loads past the L2 cache (10% slower),
+// three waves a SIMD by spilling (125 us).
 #include "adapters_device.h"
 
 namespace ftmoe {

@@ -15,7 +15,8 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   // empty.  Tiles of 16, 32 and 64 tokens, prompts, bf16, us: 512 tokens (in =
   // out = 7168, rank 64) 26 / 25 / 29; 2048 tokens (2048, rank 16) 22 / 20 /
   // 22; 8192 tokens (2048, rank 64) 71 / 58 / 58; 8192 tokens (7168, rank 64)
-  // 194 / 137 / 115; 1531 tokens (rank 8, half of them single) 30 / 35 / -.
+  // 194 / 137 / 115; 1531 tokens (rank 8, a quarter of them single) 29 / 35 /
+  // -; rank 128, 8192 tokens: 320 / 189 / -.
   if (rank <= 128 && int64_t(tokens) * (rank > 16 ? 2 : 1) >= 2048 && tokens >= 32 * count) p.sub = 2;
   if (rank <= 64 && tokens >= 4096 && int64_t(in) + out >= 8192 && tokens >= 64 * count) p.sub = 4;
   p.windows = std::max(1, (tokens + kAdapterWindow - 1) / kAdapterWindow);

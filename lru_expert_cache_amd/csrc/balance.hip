@@ -6,6 +6,11 @@
 // the lane that has it from a ballot, and that lane moves up its next.
 // The sums over the tokens are kept by each lane for its experts, added up
 // within the workgroup, and over the workgroups, in order, by a second kernel.
+//
+// 32768 tokens, 256 experts, top 8: 23.4 us (floor 7: the logits once), bound by
+// the vector units (330 instructions a token; 41 us when each round looked
+// through all of a lane's logits); the join 6.8; the gradient 15.3 (floor 14),
+// bound by HBM.  509 tokens, 128 experts: 4.3, 5.0 and 3.3 us, all latency.
 #include <type_traits>
 
 #include "balance.h"
@@ -14,8 +19,8 @@ namespace ftmoe {
 
 namespace {
 
-// waves of a workgroup
-// of a workgroup: few tokens are spread over more CUs, many leave fewer parts to add up
+// waves of a workgroup: few tokens are spread over more CUs (509 tokens, 128 experts: 4.4 us against 5.0 with 16
+// waves), many leave fewer parts to add up
 constexpr int balance_waves(int32_t tokens) { return tokens <= 2048 ? 4 : 16; }
 constexpr int kBackWaves = 4;
 constexpr float kInf = __builtin_huge_valf();

@@ -1,6 +1,8 @@
 // Root-mean-square norm: rows of any width, element by element.
 //
-// Every row is read twice: for its sums, and for its values.
+// For rows that norm_rows.hip does not take (fewer than 8 columns, more than
+// 16384).  Every row is read twice: for its sums, and for its values.  Here
+// too: the join of the weight gradient's parts (512 x 7168: 4.9 us).
 #include "norm_device.h"
 
 namespace ftmoe {

@@ -3,9 +3,11 @@
 // Bound by HBM: 8192 rows of 7168, bf16, called over and over: with a 32-bit
 // stream forward 126 us (5.6 TB/s read and written), backward 182 (5.2, the
 // join of the weight's gradient included); with a bf16 stream forward, codes and
-// y, 107 us (4.9).  A copy of 2 GiB moves 4.9 TB/s.  Persistent workgroups take the rows of the
-// backward pass in turn, so that 512 parts of the weight's gradient are left
-// to add up; the forward pass has a workgroup for each row.
+// y, 107 us (4.9).  A copy of 2 GiB moves 4.9 TB/s.  Persistent workgroups
+// take the rows of the backward pass in turn, so that 512 parts of the
+// weight's gradient are left to add up; the forward pass has a workgroup for
+// each row.  Pieces of four columns beside 32-bit rows (lanes then lie side by
+// side in either) were 1 to 3% faster forward and no faster backward: not kept.
 //
 // A thread has PIECES pieces of eight neighbouring columns.  The piece that
 // would pass the row's end is taken from its last eight columns instead: what
