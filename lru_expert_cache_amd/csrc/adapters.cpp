@@ -130,6 +130,10 @@ int ft_moe_adapters_apply(const ft_moe_adapters* desc, const void* x, const int3
     l.out_each = FastDiv((uint32_t(d.out) + wide - 1) / wide);
     l.in_window = FastDiv(uint32_t(up(int64_t(l.tile_cap) * l.in_each.by, 8)));
     l.out_window = FastDiv(uint32_t(up(int64_t(l.tile_cap) * l.out_each.by, 8) + 8));  // two ranges, each a multiple
+    if (w.plan.once) {
+      FT_HIP_CHECK(launch_adapters_few(d.dtype, d.base_dtype, d.out_dtype, l, s));
+      return FT_OK;
+    }
     if (!l.few) FT_HIP_CHECK(launch_adapters_plan(l, s));
     FT_HIP_CHECK(launch_adapters_in(d.dtype, l, s));
     FT_HIP_CHECK(launch_adapters_out(d.dtype, d.base_dtype, d.out_dtype, l, s));

@@ -76,6 +76,7 @@ constexpr int adapter_out_blocks(int base_bytes, int out_bytes, int sub, int ran
 // How a call is cut: a rule on sizes and types alone.
 struct AdapterPlan {
   int32_t few, sub, windows, tile_cap, parts, out_blocks;
+  int32_t once;      // both products in one launch: few tokens, up to 16 ranks
   int32_t out_step;  // columns of y in a step of a workgroup: its four waves' blocks
 };
 AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, int32_t count, int base_bytes,
@@ -83,6 +84,7 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
 
 hipError_t launch_adapters_plan(const Adapters& l, hipStream_t s);
 hipError_t launch_adapters_in(int dtype, const Adapters& l, hipStream_t s);
+hipError_t launch_adapters_few(int dtype, int base_dtype, int out_dtype, const Adapters& l, hipStream_t s);
 hipError_t launch_adapters_out(int dtype, int base_dtype, int out_dtype, const Adapters& l, hipStream_t s);
 
 }  // namespace ftmoe

@@ -132,4 +132,67 @@ __device__ __attribute__((always_inline)) inline u32x4 row_piece(const E* row, i
   return (u32x4)w;
 }
 
+// A row's last columns, fewer than eight, from column c on (none of them where
+// it has ended); the loop is not unrolled, to keep the code short.
+template <typename B>
+__device__ __attribute__((always_inline)) inline B __attribute__((ext_vector_type(8))) last_columns(const B* row, int c, int width) {
+  B __attribute__((ext_vector_type(8))) v{};
+#pragma nounroll
+  for (int i = width - 1; i >= c; --i) {
+#pragma unroll
+    for (int j = 7; j > 0; --j) v[j] = v[j - 1];
+    v[0] = gload<B>(row + i);
+  }
+  return v;
+}
+
+// h as the matrix instructions' second operand: 16-bit parts that add up to its
+// 32 bits.  bf16 takes two for a 16-bit y (which keeps 16 bits of h: 2^-18 off,
+// against y's own 2^-9) and three for a 32-bit one, fp16 two (22 bits), with
+// each token's row brought into fp16's range by a power of two.
+template <typename E, typename Y>
+constexpr int kAdapterParts = !__is_same(E, _Float16) && sizeof(Y) == 4 ? 3 : 2;
+
+// fp16: a token's values (in four lanes, COUNT each) scaled so that the largest lies in 2^13 .. 2^14, and the factor
+// that takes it back
+template <int COUNT>
+__device__ __attribute__((always_inline)) inline float to_half_range(float (&v)[COUNT]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) top = fmaxf(top, fabsf(v[i]));
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const int e = top > 0.f && top < __builtin_huge_valf() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) v[i] = __builtin_ldexpf(v[i], e);
+  return __builtin_ldexpf(1.f, -e);
+}
+
+template <typename E, int PARTS>
+__device__ __attribute__((always_inline)) inline void split_parts(const float* v, u32x4 (&out)[PARTS]) {
+  typedef E elem8 __attribute__((ext_vector_type(8)));
+  elem8 part[PARTS];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float left = v[i];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      part[p][i] = E(left);
+      const float is = float(part[p][i]);
+      left = __builtin_isfinite(is) ? left - is : 0.f;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) out[p] = (u32x4)part[p];
+}
+
+// Up to 16 ranks: two parts in one operand of 32, the third (with zeros behind) in a second.  q: the lane's quarter.
+template <typename E, int PARTS>
+__device__ __attribute__((always_inline)) inline void pack_parts(const float* v, int q, u32x4 (&out)[(PARTS + 1) / 2]) {
+  u32x4 part[PARTS];
+  split_parts<E, PARTS>(v, part);
+  out[0] = q < 2 ? part[0] : part[1];
+  if constexpr (PARTS == 3) out[1] = q < 2 ? part[2] : u32x4{};
+}
+
 }  // namespace ftmoe

@@ -1,11 +1,5 @@
 // Adapters: the second product, y = base + scale B h.
 //
-// h is the matrix instructions' second operand, in 16-bit parts that add up to
-// its 32 bits: bf16 takes two for a 16-bit y (which keeps 16 bits of h: 2^-18
-// off, against y's own 2^-9) and three for a 32-bit one, fp16 two (22 bits),
-// with each token's row brought into fp16's range by a power of two.  Up to
-// rank 16, two parts are one instruction of 32 ranks.
-//
 // Bound by reading base and writing y: 8192 tokens, N 7168, bf16: 68 us at
 // rank 64, 60 at rank 16, 58 with no adapter at all (235 MB; 48 at a copy's
 // rate, whose rows lie side by side); a 32-bit base 90, a 32-bit y too 124.
@@ -21,30 +15,15 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
-// A row's last columns, fewer than eight, from column c on (none of them where
-// it has ended); the loop is not unrolled, to keep the code short.
-template <typename B>
-__device__ __attribute__((always_inline)) inline B __attribute__((ext_vector_type(8))) last_columns(const B* row, int c, int width) {
-  B __attribute__((ext_vector_type(8))) v{};
-#pragma nounroll
-  for (int i = width - 1; i >= c; --i) {
-#pragma unroll
-    for (int j = 7; j > 0; --j) v[j] = v[j - 1];
-    v[0] = gload<B>(row + i);
-  }
-  return v;
-}
-
 // KS: steps of 32 ranks; 0: up to 16 ranks, two parts in a step
 template <typename D, typename B, typename Y, int SUB, int KS>
 __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
   typedef typename D::elem E;
-  typedef E elem8 __attribute__((ext_vector_type(8)));
   typedef float float8 __attribute__((ext_vector_type(8)));
   typedef float8 __attribute__((aligned(4))) float8_any;
   typedef B base8 __attribute__((ext_vector_type(8)));
   constexpr bool kHalf = __is_same(E, _Float16);
-  constexpr int kParts = !kHalf && sizeof(Y) == 4 ? 3 : 2;
+  constexpr int kParts = kAdapterParts<E, Y>;
   constexpr int kSteps = KS == 0 ? 1 : KS;                          // of B's pieces
   constexpr int kFrags = KS == 0 ? (kParts + 1) / 2 : KS * kParts;  // of h's
   constexpr int kBlocks = adapter_out_blocks(sizeof(B), sizeof(Y), SUB, 32 * KS), kStep = 32 * kBlocks * kWaves;
@@ -72,8 +51,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
     u32x4 h[kKept][kFrags] = {};
     float scale[kKept] = {};
     auto operands = [&](int m, u32x4(&out)[kFrags], float& factor) {
-      float v[kSteps][8];
-      float top = 0.f;
+      float v[kSteps * 8];
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         const int slot = (m * kSteps + k) * kGroups;
@@ -85,43 +63,21 @@ __global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[k][i] = lo[i];
-          v[k][4 + i] = hi[i];
+          v[8 * k + i] = lo[i];
+          v[8 * k + 4 + i] = hi[i];
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[k][i]));
       }
       factor = given;
-      if constexpr (kHalf) {
-        // the row's largest value to 2^13 .. 2^14
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const int e = top > 0.f && top < __builtin_huge_valf() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-        factor = __builtin_ldexpf(factor, -e);
+      if constexpr (kHalf) factor *= to_half_range(v);
+      if constexpr (KS == 0) {
+        pack_parts<E, kParts>(v, q, out);
+      } else {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < kSteps; ++k) {
+          u32x4 part[kParts];
+          split_parts<E, kParts>(v + 8 * k, part);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = __builtin_ldexpf(v[k][i], e);
-      }
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        elem8 part[kParts];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float left = v[k][i];
-#pragma unroll
-          for (int p = 0; p < kParts; ++p) {
-            part[p][i] = E(left);
-            const float is = float(part[p][i]);
-            left = __builtin_isfinite(is) ? left - is : 0.f;
-          }
-        }
-        if constexpr (KS == 0) {
-          out[0] = q < 2 ? (u32x4)part[0] : (u32x4)part[1];
-          if constexpr (kParts == 3) out[1] = q < 2 ? (u32x4)part[2] : u32x4{};
-        } else {
-#pragma unroll
-          for (int p = 0; p < kParts; ++p) out[k * kParts + p] = (u32x4)part[p];
+          for (int p = 0; p < kParts; ++p) out[k * kParts + p] = part[p];
         }
       }
     };
