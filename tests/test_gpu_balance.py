@@ -9,7 +9,7 @@ from tests import around_case as ac
 pytestmark = pytest.mark.gpu
 
 # (tokens, experts, top_k, row padding)
-SIZES = [(1, 1, 1, 0), (1, 8, 2, 0), (3, 5, 5, 1), (2, 64, 8, 0), (17, 65, 4, 3), (64, 16, 2, 0), (100, 60, 6, 0), (255, 128, 8, 0),
+SIZES = [(4, 512, 16, 0), (5, 400, 3, 0), (32, 512, 9, 1), (1, 1, 1, 0), (1, 8, 2, 0), (3, 5, 5, 1), (2, 64, 8, 0), (17, 65, 4, 3), (64, 16, 2, 0), (100, 60, 6, 0), (255, 128, 8, 0),
          (509, 128, 8, 64), (33, 129, 1, 0), (77, 160, 8, 0), (40, 256, 16, 0), (90, 257, 3, 0), (31, 300, 16, 5), (50, 512, 8, 0),
          (5000, 128, 8, 0), (9001, 256, 6, 0)]
 
