@@ -144,6 +144,8 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm* desc, const void* sum, const
     a.dsum = dsum;
     a.dx = dx;
     a.dresidual = dresidual;
+    const bool once = some && dweight && d.rows <= kNormOnce && norm_rows(d.cols);
+    a.dweight = once ? dweight : nullptr;
     a.part = dweight ? w.part : nullptr;
     a.stats = w.stats;
     a.ld_sum = d.ld_sum;
@@ -152,10 +154,10 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm* desc, const void* sum, const
     a.ld_x = d.ld_x;
     a.rows = d.rows;
     a.cols = d.cols;
-    a.groups = norm_groups(d.rows, d.cols);
+    a.groups = once ? 1 : norm_groups(d.rows, d.cols);
     a.eps = d.eps;
     if (some) FT_HIP_CHECK(launch_norm_backward(d.dtype, d.residual_dtype, a, s));
-    if (dweight) FT_HIP_CHECK(launch_norm_join(d.dtype, w.part, a.groups, d.cols, dweight, s));
+    if (dweight && !once) FT_HIP_CHECK(launch_norm_join(d.dtype, w.part, a.groups, d.cols, dweight, s));
     return FT_OK;
   });
 }

@@ -18,6 +18,7 @@ struct NormForward {
 struct NormBackward {
   const void *sum, *weight, *dy, *dsum;  // dsum: null for 0
   void *dx, *dresidual;                  // null: not wanted
+  void* dweight;                         // one group of rows writes it itself, null: not so
   float* part;                           // [groups][norm_part_ld]: sums of dy s r over each group's rows, null: not wanted
   float* stats;                          // rows that no workgroup holds: r and mean(g s r) of each
   int64_t ld_sum, ld_y, ld_residual, ld_x;
@@ -32,6 +33,10 @@ __host__ __device__
 inline int64_t norm_part_ld(int32_t cols) { return (int64_t(cols) + 3) / 4 * 4; }
 // groups of rows whose weight gradients are summed apart
 int norm_groups(int32_t rows, int32_t cols);
+// Rows that one workgroup takes one after the other, with the weight's gradient,
+// in one launch instead of two: bf16, 2048 / 7168 columns, us, one launch of
+// 1 / 2 / 3 rows 3.3 / 4.2 / 5.2 and 4.7 / 6.7 / 8.6, two launches 5.6 and 7.2.
+constexpr int kNormOnce = 2;
 
 // norm_rows.hip: rows that a workgroup's registers hold; norm_any.hip: all others
 bool norm_rows(int32_t cols);

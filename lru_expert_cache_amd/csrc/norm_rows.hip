@@ -153,6 +153,13 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
   for (int g = 0; g < PIECES; ++g) {
     const Place p(int(threadIdx.x) + g * THREADS, a.cols);
     if (!p.some()) continue;
+    if (a.dweight) {
+      Piece<X> v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.v[i] = X(dw[g][i]);
+      v.store(static_cast<X*>(a.dweight) + p.c);
+      continue;
+    }
     Piece<float> v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.v[i] = dw[g][i];
