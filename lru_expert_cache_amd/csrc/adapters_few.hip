@@ -19,8 +19,7 @@ __global__ __launch_bounds__(kThreads) void k_adapters_few(Adapters l) {
   typedef B base8 __attribute__((ext_vector_type(8)));
   typedef base8 __attribute__((aligned(1))) base8_any;
   typedef u32x4 __attribute__((aligned(1))) any;
-  constexpr int kParts = kAdapterParts<E, Y>, kFrags = (kParts + 1) / 2;
-  constexpr int kBlocks = adapter_out_blocks(sizeof(B), sizeof(Y), 1, 16), kStep = 32 * kBlocks * kWaves;
+  constexpr int kParts = kAdapterParts<E, Y>, kFrags = (kParts + 1) / 2, kStep = 32 * kWaves;
   __shared__ float sums[kWaves][256];  // of a wave's units: rank 4 q + i of token lane % 16 at 4 lane + i
   __shared__ float total[256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
@@ -30,28 +29,25 @@ __global__ __launch_bounds__(kThreads) void k_adapters_few(Adapters l) {
   const bool on = t.id != l.count, live = (lane & 15) < t.count;
   const float given = on && l.scale ? gload<float>(l.scale + t.id) : 1.f;
   const int wide = kStep * l.out_blocks, c0 = piece * wide;
-  const int n0 = c0 + 32 * kBlocks * wave, n1 = min(l.out - c0, wide) + c0;
+  const int n0 = c0 + 32 * wave, n1 = min(l.out - c0, wide) + c0;
 
   // B's rows and base's columns as k_adapters_out takes them
   const int mine = 8 * ((lane & 15) >> 2) + (lane & 3);
   const E* weights = static_cast<const E*>(l.b) + (int64_t(t.id) * l.out + mine) * l.ld_b;
   const B* base = static_cast<const B*>(l.base) + int64_t(t.token[0]) * l.ld_base;
   Y* y = static_cast<Y*>(l.y) + int64_t(t.token[0]) * l.ld_y;
-  u32x4 b[kBlocks][2] = {};
-  base8 with[kBlocks] = {};
+  u32x4 b[2] = {};
+  base8 with = {};
   auto fetch = [&](int n) {
+    if (on) {
 #pragma unroll
-    for (int w = 0; w < kBlocks; ++w) {
-      const int c = n + 32 * w + 8 * q;
-      if (on) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          b[w][j] = row_piece<E, false>(weights + int64_t(min(n + 32 * w + 4 * j, l.out - 1 - mine)) * l.ld_b, q & 1, l.rank);
-      }
-      if (l.base) {
-        if (c + 8 <= l.out) with[w] = gload<base8_any>(base + c);
-        else with[w] = last_columns(base, c, l.out);
-      }
+      for (int j = 0; j < 2; ++j)
+        b[j] = row_piece<E, false>(weights + int64_t(min(n + 4 * j, l.out - 1 - mine)) * l.ld_b, q & 1, l.rank);
+    }
+    if (l.base) {
+      const int c = n + 8 * q;
+      if (c + 8 <= l.out) with = gload<base8_any>(base + c);
+      else with = last_columns(base, c, l.out);
     }
   };
   if (n0 < n1) fetch(n0);
@@ -111,25 +107,22 @@ __global__ __launch_bounds__(kThreads) void k_adapters_few(Adapters l) {
   }
 
   for (int n = n0; n < n1; n += kStep) {
+    float v[8] = {};
+    if (l.base) {
 #pragma unroll
-    for (int w = 0; w < kBlocks; ++w) {
-      float v[8] = {};
-      if (l.base) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = float(with[w][i]);
-      }
-      if (on) {
-        floatx4 acc[2] = {};
-#pragma unroll
-        for (int f = 0; f < kFrags; ++f)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[j] = D::mfma16(b[w][j], h[f], acc[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(acc[i >> 2][i & 3], scale, v[i]);
-      }
-      const int c = n + 32 * w + 8 * q;
-      if (live && c < l.out) dense_store<Y, 8>(reinterpret_cast<uint8_t*>(y + c), 0, v, min(8, l.out - c));
+      for (int i = 0; i < 8; ++i) v[i] = float(with[i]);
     }
+    if (on) {
+      floatx4 acc[2] = {};
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j] = D::mfma16(b[j], h[f], acc[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(acc[i >> 2][i & 3], scale, v[i]);
+    }
+    const int c = n + 8 * q;
+    if (live && c < l.out) dense_store<Y, 8>(reinterpret_cast<uint8_t*>(y + c), 0, v, min(8, l.out - c));
     if (n + kStep < n1) fetch(n + kStep);
   }
 }

@@ -17,7 +17,7 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 
 // KS: steps of 32 ranks; 0: up to 16 ranks, two parts in a step
 template <typename D, typename B, typename Y, int SUB, int KS>
-__global__ __launch_bounds__(kThreads) void k_adapters_out(Adapters l) {
+__global__ __launch_bounds__(kThreads, SUB == 1 && KS == 0 ? 4 : 1) void k_adapters_out(Adapters l) {
   typedef typename D::elem E;
   typedef float float8 __attribute__((ext_vector_type(8)));
   typedef float8 __attribute__((aligned(4))) float8_any;

@@ -28,15 +28,17 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   const int64_t rows = (rank + 63) / 64;
   const int64_t tiles = int64_t(p.windows) * std::min<int64_t>(p.tile_cap, tokens / (16 * p.sub) + 1 + count / 2) * rows;
   p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>((256 + tiles / 2) / tiles, in / 256), 1, 32));
-  // One launch where a workgroup soon has all of A x: graphs of calls (rank 16), one launch against two, us: one token,
-  // in = out = 1024 / 2048 / 4096 / 7168: 6.0 / 6.8 / 8.2 / 10.4 against 7.2 / 7.4 / 8.0 / 8.3; 32 tokens of up to 64
-  // adapters 7.1 / 8.2 / 10.4 / 15.5 against 8.2 / 8.5 / 9.1 / 11.5.  Calls by themselves save the launch's 2 us too.
-  p.once = p.few && rank <= 16 && in <= 2048;
-  p.out_step = (p.once ? 16 : 4) * 32 * adapter_out_blocks(base_bytes, out_bytes, p.sub, rank);
+  // One launch where a workgroup soon has all of A x: graphs of calls (rank 16, N 4096), one launch against two, us:
+  // one / 8 / 32 tokens of as many adapters, K 2560: 6.6 / 8.0 / 8.4 against 7.4 / 8.3 / 8.9; 3584: 7.2 / 9.3 / 9.8
+  // against 7.5 / 8.7 / 9.4.  Calls by themselves save up to the launch's 2 us too.
+  p.once = p.few && rank <= 16 && in <= 2560;
+  p.out_step = 32 * (p.once ? 16 : 4 * adapter_out_blocks(base_bytes, out_bytes, p.sub, rank));
   // columns for about 1024 workgroups: each joins h's parts first (8192 tokens, 7168, rank 64: steps of 256 columns
-  // 1 / 2 / 4 / 7 a workgroup: 132 / 118 / 115 / 128 us for the call)
+  // 1 / 2 / 4 / 7 a workgroup: 132 / 118 / 115 / 128 us for the call); for fewer where each forms h itself (64 tokens
+  // of 64 adapters, 2048 into 16384: 14.9 us, in 1024 workgroups 18.9).  Few tokens are taken to be of as many adapters.
   const int64_t blocks = (out + p.out_step - 1) / p.out_step;
-  p.out_blocks = int32_t(std::clamp<int64_t>((blocks * tiles + 512) / 1024, 1, 8));
+  const int64_t each = p.few ? p.tile_cap * rows : tiles, goal = p.once ? 448 : 1024;
+  p.out_blocks = int32_t(std::clamp<int64_t>((blocks * each + goal / 2) / goal, 1, 8));
   // (numbers of workgroups stay below 2^30)
   const int64_t all = int64_t(p.windows) * p.tile_cap;
   p.out_blocks = int32_t(std::max<int64_t>(p.out_blocks, (all * blocks >> 30) + 1));

@@ -31,12 +31,20 @@ def test_apply(size, type_, base, out):
 
 
 @pytest.mark.parametrize("type_,base,out", FORMS)
-@pytest.mark.parametrize("in_", [7, 63, 200, 1000, 2048, 2049, 5000])
+@pytest.mark.parametrize("in_", [7, 63, 200, 1000, 2048, 2560, 2561, 5000])
 def test_few_tokens(in_, type_, base, out):
     """One launch, or two, for the same tokens: widths on either side, ranks on either side of a piece of eight."""
     for tokens, N, R, n in ((1, 2100, 16, 3), (9, 65, 7, 4), (37, 1030, 13, 2), (64, 300, 8, 64)):
         c = ac.Adapters(tokens, in_, N, R, n, type_, base, out, pad=1, seed=in_)
         ac.check(c.apply(), c.reference(), f"{tokens} tokens")
+
+
+@pytest.mark.parametrize("type_,base,out", FORMS)
+@pytest.mark.parametrize("tokens,in_,N", [(64, 72, 20001), (50, 72, 8200), (64, 2600, 20001)])
+def test_few_tokens_into_many_columns(tokens, in_, N, type_, base, out):
+    """A workgroup takes several steps of columns."""
+    c = ac.Adapters(tokens, in_, N, 16, 64, type_, base, out, ids=[(7 * i) % 64 for i in range(tokens)])
+    ac.check(c.apply(), c.reference())
 
 
 @pytest.mark.parametrize("tokens", [7, 64, 90, 1200, 9000])
