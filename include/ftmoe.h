@@ -586,7 +586,9 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm *d, const void *sum, const vo
  * 0..n-1 has no adapter: y[t] = base[t].  A x is held in 32 bits and enters
  * the second product in two 16-bit parts: y is rounded once.  base is the
  * projection's result (of ft_moe_int_matmul, say; with FT_DT_F32 nothing of it
- * was rounded before), or NULL for 0. */
+ * was rounded before), or NULL for 0.  Infinities and NaN in a row of x or
+ * base stay in that row of y; A and B are finite (an infinity in them may give
+ * NaN where the formula has an infinity, for their adapter's tokens only). */
 typedef struct {
   int32_t dtype;      /* of x, A and B: FT_DT_BF16 or FT_DT_F16 */
   int32_t base_dtype; /* of base: out_dtype or FT_DT_F32; 0 = out_dtype */
