@@ -67,10 +67,27 @@ __device__ __attribute__((always_inline)) inline float logit_of(uint32_t k) {
   return __uint_as_float(k ^ (uint32_t(int(~k) >> 31) | 0x80000000u));
 }
 
-// e^d, d <= 0: the product with log2 e and the hardware's exp2 round once each
+// e^d, d <= 0, to within two units at any distance, subnormal results too: d = n ln 2 + r, ln 2 in two parts (a single
+// product d log2 e rounds by up to |d| / 2 units, and the hardware's exp2 leaves 0 below 2^-126).  Below -104 it is 0.
 __device__ __attribute__((always_inline)) inline float exp_of(float d) {
-  return __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
+  const float c = d < -104.f ? -104.f : d;  // NaN stays
+  const float n = rintf(c * 1.4426950408889634f);
+  const float r = fmaf(-n, -1.904654323148236e-09f, fmaf(-n, 0.693147182464599609375f, c));
+  return ldexpf(__builtin_amdgcn_exp2f(r * 1.4426950408889634f), int(n));
 }
+
+// Quotients by v, of 1 to 512: by the hardware's reciprocal, which is off by a unit, and then by what is left over.
+struct Over {
+  float v, r;
+  __device__ __attribute__((always_inline)) inline explicit Over(float v_) : v(v_) {
+    const float near = __builtin_amdgcn_rcpf(v);
+    r = fmaf(fmaf(-v, near, 1.f), near, near);
+  }
+  __device__ __attribute__((always_inline)) inline float operator()(float e) const {
+    const float q = e * r;
+    return fmaf(fmaf(-v, q, e), r, q);
+  }
+};
 
 // A token's logits, J for each lane; -inf beyond the last.
 template <typename X, int J>
@@ -111,9 +128,9 @@ struct Logits {
       p[j] = lane + 64 * j < experts ? e : 0.f;
       sum += p[j];
     }
-    sum = __builtin_amdgcn_rcpf(wave_sum(sum));  // 1 or more; off by a unit
+    const Over over(wave_sum(sum));
 #pragma unroll
-    for (int j = 0; j < J; ++j) p[j] *= sum;
+    for (int j = 0; j < J; ++j) p[j] = over(p[j]);
   }
 };
 
@@ -208,10 +225,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_balance(BalanceForward a) {
       if (mine >= 0) atomicAdd(&lds_c[mine], 1);
     }
     const float ex = mine >= 0 ? exp_of(logit_of(mine_key) - logit_of(first)) : 0.f;
-    const float sum = __builtin_amdgcn_rcpf(wave_sum(ex));
+    const Over over(wave_sum(ex));
     if (lane < a.top_k) {
       sel[lane] = mine;
-      w[lane] = mine >= 0 ? ex * sum : 0.f;
+      w[lane] = mine >= 0 ? over(ex) : 0.f;
     }
     sel += step * a.top_k;
     w += step * a.top_k;

@@ -180,3 +180,27 @@ def test_rows_beyond_4_gb():
     assert all(torch.equal(f[k], f2[k]) for k in f)
     ft.ft_moe_balance_backward(b.d, b.z, b.valid, f["sel"], f["w"], f["counts"], b.dw, b.dloss, b.z)
     assert torch.equal(b.z, dz)
+
+
+@pytest.mark.parametrize("experts,k", [(2, 2), (8, 8), (16, 16), (130, 16), (250, 16), (500, 16)])
+def test_probabilities_keep_their_bits_at_any_distance(experts, k):
+    """Logits up to 110 below the largest, at differences that 32 bits hold: the bounds do not grow with the distance,
+    and reach into the subnormal numbers."""
+    T, tiny = 300, 2.0**-149
+    b = ac.Balance(T, experts, k, masked=0)
+    b.z.copy_((torch.rand(T, experts, generator=ac.gen(6), device="cuda") * -880).round() / 8)
+    at = torch.arange(T, device="cuda")
+    b.z[at, at % experts] = 0.0
+    f, r = b.forward(), b.reference()
+    assert torch.equal(f["sel"], r["sel"]) and torch.equal(f["counts"], r["counts"])
+    _, p, _, w, _, c, _, _, _ = b.dref
+    # an exponential is off by 3 E: its argument, at most ln 2 / 2, by less than one (two roundings of half a unit and
+    # the product with log2 e), exp2 by a unit.  The sum carries that and rounds for each term: w's 6 steps between lanes,
+    # p's 7 within a lane too.  The quotient rounds once.
+    ac.check(f["w"], (w, 14 * ac.E * w + tiny), "w")
+    ep = 21 * ac.E * p + tiny
+    loss = (c * p.sum(0)).sum()
+    ac.check(f["loss"], (loss[None], ((c * (ep.sum(0) + (T / 64 + 24) * ac.E * p.sum(0))).sum() + 2 * ac.E * loss)[None]), "loss")
+    s = (p * c).sum(1, keepdim=True)
+    dz, es = p * (c - s), (ep * c).sum(1, keepdim=True) + 20 * ac.E * s
+    ac.check(b.backward(f, dw=False, dloss=False), (dz, ep * (c - s).abs() + p * (3 * ac.E * c + es) + 4 * ac.E * dz.abs() + tiny), "dlogits")
