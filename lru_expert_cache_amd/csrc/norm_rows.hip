@@ -123,9 +123,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
 #pragma unroll
     for (int g = 0; g < PIECES; ++g) {
       const Place p(int(threadIdx.x) + g * THREADS, a.cols);
+      auto add = [&](int i) { t.add(float(sv[g].v[i]), float(yv[g].v[i]) * float(wv[g].v[i])); };
+      if (p.skip == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        t.add(i >= p.skip ? float(sv[g].v[i]) : 0.f, float(yv[g].v[i]) * float(wv[g].v[i]));
+        for (int i = 0; i < 8; ++i) add(i);
+      } else {  // the row's last piece: left out, not taken as 0, which an infinity in dy would make a NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i >= p.skip) add(i);
+      }
     }
     if (THREADS > 64 && row != blockIdx.x) __syncthreads();  // the last row's sums have been read
     t.join<THREADS>(lds);

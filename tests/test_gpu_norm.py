@@ -201,3 +201,23 @@ def test_rows_beyond_4_gb():
     s, dy, dsum = far(n.s), far(n.dy), far(n.dsum)
     ft.ft_moe_rms_norm_backward(n.d, s, n.weight, dy, dsum, dy, dsum, None, n.work())
     assert torch.equal(dy, bwd["dx"]) and torch.equal(dsum, bwd["dresidual"])
+
+
+@pytest.mark.parametrize("cols", [5, 8, 12, 100, 512, 1000, 2050, 7168, 16383, 20001])
+def test_infinite_gradients(cols):
+    """An infinity in dy, wherever it stands in its row: infinities and NaN where the formula has them."""
+    at = sorted({0, cols // 2, max(0, cols - 9), cols - 8 if cols >= 8 else 0, cols - 1})
+    n = ac.Norm(len(at) + 1, cols, "bf16", "fp32", pad=3)
+    before = n.backward()
+    for row, c in enumerate(at):
+        n.dy[row, c] = float("inf") if row % 2 else float("-inf")
+    got, ref = n.backward(), n.backward_reference()
+    for k in ("dx", "dresidual"):
+        want = ref[k][0][:-1]
+        assert torch.equal(torch.isnan(got[k][:-1]), torch.isnan(want)), k
+        assert torch.equal(got[k][:-1].double() == torch.inf, want == torch.inf), k
+        assert torch.equal(got[k][:-1].double() == -torch.inf, want == -torch.inf), k
+        assert torch.equal(got[k][-1], before[k][-1])
+    inf = torch.zeros(cols, dtype=torch.bool, device="cuda")
+    inf[at] = True
+    assert torch.equal(~torch.isfinite(got["dweight"]), inf)
