@@ -38,7 +38,7 @@ NormWork norm_work(const ft_moe_rms_norm& d, void* base) {
   NormWork w{};
   Carve c{static_cast<uint8_t*>(base)};
   w.part = reinterpret_cast<float*>(c.take(norm_groups(d.rows, d.cols) * norm_part_ld(d.cols) * 4));
-  w.stats = reinterpret_cast<float*>(c.take(int64_t(d.rows) * 8));
+  w.stats = reinterpret_cast<float*>(c.take(int64_t(d.rows) * 16));
   w.bytes = d.rows ? c.used : 0;
   return w;
 }

@@ -20,7 +20,7 @@ struct NormBackward {
   void *dx, *dresidual;                  // null: not wanted
   void* dweight;                         // one group of rows writes it itself, null: not so
   float* part;                           // [groups][norm_part_ld]: sums of dy s r over each group's rows, null: not wanted
-  float* stats;                          // rows that no workgroup holds: r and mean(g s r) of each
+  float* stats;                          // rows that no workgroup holds: a NormSlope of each
   int64_t ld_sum, ld_y, ld_residual, ld_x;
   int32_t rows, cols, groups;
   double eps;

@@ -37,7 +37,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_any(NormForward a) {
   }
 }
 
-template <typename X, typename R>
+typedef float NormStats __attribute__((ext_vector_type(4)));  // a row's NormSlope, in one load
+
+template <typename X, typename R, bool FAR>
 __global__ __launch_bounds__(kThreads) void k_norm_stats_any(NormBackward a) {
   __shared__ double lds[2 * kThreads / 64];
   const int64_t row = int64_t(blockIdx.y) * kNormGrid + blockIdx.x;
@@ -49,15 +51,15 @@ __global__ __launch_bounds__(kThreads) void k_norm_stats_any(NormBackward a) {
   for (int c = threadIdx.x; c < a.cols; c += kThreads)
     t.add(float(gload<R>(sum + c)), float(gload<X>(dy + c)) * float(gload<X>(weight + c)));
   t.join<kThreads>(lds);
-  const NormSlope k(t, a.cols, a.eps);
+  const NormSlope<FAR> k(t, a.cols, a.eps);
   if (threadIdx.x == 0) {
-    a.stats[2 * row] = k.r;
-    a.stats[2 * row + 1] = k.m;
+    const NormStats v{k.r, k.m, k.up, 0.f};
+    gstore<NormStats>(a.stats + 4 * row, v);
   }
 }
 
 // a column for each thread, the rows of a group one after the other
-template <typename X, typename R>
+template <typename X, typename R, bool FAR>
 __global__ __launch_bounds__(kThreads) void k_norm_grad_any(NormBackward a) {
   const int c = int(blockIdx.x) * kThreads + int(threadIdx.x);
   if (c >= a.cols) return;
@@ -66,8 +68,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad_any(NormBackward a) {
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const float s = float(gload<R>(static_cast<const R*>(a.sum) + row * a.ld_sum + c));
     const float dy = float(gload<X>(static_cast<const X*>(a.dy) + row * a.ld_y + c));
-    const NormSlope k(a.stats[2 * row], a.stats[2 * row + 1]);
-    const float n = s * k.r;
+    const NormStats v = gload<NormStats>(a.stats + 4 * row);
+    const NormSlope<FAR> k(v[0], v[1], v[2]);
+    const float n = k.n(s);
     float ds = k.ds(dy * w, n);
     if (a.dsum) ds += float(gload<R>(static_cast<const R*>(a.dsum) + row * a.ld_residual + c));
     if (a.dx) gstore<X>(static_cast<X*>(a.dx) + row * a.ld_x + c, X(ds));
@@ -112,12 +115,16 @@ hipError_t launch(const NormForward& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename X, typename R, bool FAR>
+hipError_t launch_backward(const NormBackward& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_norm_stats_any<X, R, FAR>), norm_grid(a.rows), dim3(kThreads), 0, s, a);
+  const uint32_t across = uint32_t((a.cols + kThreads - 1) / kThreads);
+  hipLaunchKernelGGL((k_norm_grad_any<X, R, FAR>), dim3(across, uint32_t(a.groups)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
 template <typename X, typename R>
 hipError_t launch(const NormBackward& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_stats_any<X, R>), norm_grid(a.rows), dim3(kThreads), 0, s, a);
-  const uint32_t across = uint32_t((a.cols + kThreads - 1) / kThreads);
-  hipLaunchKernelGGL((k_norm_grad_any<X, R>), dim3(across, uint32_t(a.groups)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  return a.eps > 0.0 ? launch_backward<X, R, false>(a, s) : launch_backward<X, R, true>(a, s);
 }
 
 template <typename A>

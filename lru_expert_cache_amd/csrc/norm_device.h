@@ -110,15 +110,29 @@ struct NormDots {
   }
 };
 
+// FAR, for an eps of 0: 1 / sqrt(mean(s^2)) as up r.  It then reaches from
+// 2^-128 to 2^161, beyond 32 bits; up is a power of two, and 1 within 2^100
+// either way.  (An eps above 0 is 2^-149 or more, and keeps it below 2^75.
+// Both products always: 8192 rows of 2048, bf16, 37.9 us against 36.7.)
+template <bool FAR>
 struct NormSlope {
-  float r, m;  // of n = s r: ds = r (g - n m), m = mean(g n)
-  __device__ __attribute__((always_inline)) inline NormSlope(float r_, float m_) : r(r_), m(m_) {}
+  float up = 1.f, r, m;  // of n = s up r: ds = up r (g - n m), m = mean(g n)
+  __device__ __attribute__((always_inline)) inline NormSlope(float r_, float m_, float up_) : up(up_), r(r_), m(m_) {}
   __device__ __attribute__((always_inline)) inline NormSlope(const NormDots& t, int cols, double eps) {
     const double rr = 1.0 / sqrt(t.squares / cols + eps);
     r = float(rr);
+    if constexpr (FAR) {
+      const bool large = rr > 0x1p100, small = rr < 0x1p-100;
+      up = large ? 0x1p100f : small ? 0x1p-100f : 1.f;
+      r = float(rr * (large ? 0x1p-100 : small ? 0x1p100 : 1.0));
+    }
     m = float(rr * (t.dot / cols));
   }
-  __device__ __attribute__((always_inline)) inline float ds(float g, float n) const { return r * fmaf(-n, m, g); }
+  __device__ __attribute__((always_inline)) inline float n(float s) const { return FAR ? s * up * r : s * r; }
+  __device__ __attribute__((always_inline)) inline float ds(float g, float n) const {
+    const float v = fmaf(-n, m, g);
+    return FAR ? v * up * r : v * r;
+  }
 };
 
 }  // namespace ftmoe

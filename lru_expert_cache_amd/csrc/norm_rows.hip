@@ -98,7 +98,7 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormForward a) {
 }
 
 // Rows blockIdx.x, + groups, ...; each thread sums its columns' weight gradients over them.
-template <typename X, typename R, int THREADS, int PIECES>
+template <typename X, typename R, int THREADS, int PIECES, bool FAR>
 __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
   __shared__ double lds[2 * (THREADS / 64)];
   const X* weight = static_cast<const X*>(a.weight);
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
     }
     if (THREADS > 64 && row != blockIdx.x) __syncthreads();  // the last row's sums have been read
     t.join<THREADS>(lds);
-    const NormSlope k(t, a.cols, a.eps);
+    const NormSlope<FAR> k(t, a.cols, a.eps);
 #pragma unroll
     for (int g = 0; g < PIECES; ++g) {
       const Place p(int(threadIdx.x) + g * THREADS, a.cols);
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
       Piece<R> dr;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float dy = float(yv[g].v[i]), n = float(sv[g].v[i]) * k.r;
+        const float dy = float(yv[g].v[i]), n = k.n(float(sv[g].v[i]));
         const float ds = k.ds(dy * float(wv[g].v[i]), n) + float(dv[g].v[i]);
         dw[g][i] = fmaf(dy, n, dw[g][i]);
         dx.v[i] = X(ds);
@@ -180,7 +180,9 @@ hipError_t launch(const NormForward& a, hipStream_t s) {
 }
 template <typename X, typename R, int THREADS, int PIECES>
 hipError_t launch(const NormBackward& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_backward<X, R, THREADS, PIECES>), dim3(uint32_t(a.groups)), dim3(THREADS), 0, s, a);
+  const dim3 grid(uint32_t(a.groups));
+  if (a.eps > 0.0) hipLaunchKernelGGL((k_norm_backward<X, R, THREADS, PIECES, false>), grid, dim3(THREADS), 0, s, a);
+  else hipLaunchKernelGGL((k_norm_backward<X, R, THREADS, PIECES, true>), grid, dim3(THREADS), 0, s, a);
   return hipGetLastError();
 }
 

@@ -221,3 +221,22 @@ def test_infinite_gradients(cols):
     inf = torch.zeros(cols, dtype=torch.bool, device="cuda")
     inf[at] = True
     assert torch.equal(~torch.isfinite(got["dweight"]), inf)
+
+
+@pytest.mark.parametrize("type_,res", [("fp32", None), ("bf16", "fp32"), ("bf16", None)])
+@pytest.mark.parametrize("cols", [5, 600, 7168, 16400])
+def test_gradients_of_the_smallest_and_largest_rows(cols, type_, res):
+    """1 / sqrt(mean(s^2)) beyond the range of 32 bits, either way, with gradients that are within it."""
+    g = ac.gen(9)
+    for size, dy in ((2.0**-130, 2.0**-20), (2.0**-145, 2.0**-60), (2.0**-110, 1.0), (2.0**110, 2.0**60), (2.0**125, 2.0**60)):
+        n = ac.Norm(4, cols, type_, res, pad=1, eps=0.0)
+        if size < 2.0**-133 and n.r == torch.bfloat16:
+            continue  # below the type's smallest number
+        n.s.copy_((torch.rand(4, cols, generator=g, device="cuda") - 0.5) * size)
+        n.dy.copy_(torch.randn(4, cols, generator=g, device="cuda") * dy)
+        n.dsum.zero_()
+        assert (n.s != 0).any(1).all() and torch.isfinite(n.s).all()
+        got, ref = n.backward(), n.backward_reference()
+        for k, v in ref.items():
+            assert torch.isfinite(v[0]).all() and v[0].abs().max() < 2.0**127
+            ac.check(got[k], v, f"{k} {size}")
