@@ -249,7 +249,10 @@ def _check(rc: int, allow_warn: bool = False) -> int:
 def _ptr(t) -> int:
     if t is None:
         return 0
-    return t if isinstance(t, int) else t.data_ptr()
+    if isinstance(t, int):
+        return t
+    p = t.data_ptr()
+    return p if type(p) is int else int(p)  # ctypes takes Python's own integers only
 
 
 def make_config(num_layers, hidden, inter, num_experts, top_k, layer_fmt: Sequence[int], pool_slots=0,

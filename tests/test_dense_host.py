@@ -161,3 +161,17 @@ def test_scratch_memory_that_is_an_input():
     assert ft.ft_moe_int_matmul_work(m) > 0
     _refused(ft.ft_moe_int_matmul, m, w.at, 2 * A, 3 * A, 4 * A, 5 * A, w)
     _refused(ft.ft_moe_int_matmul, m, A, 2 * A, w.at, 4 * A, 5 * A, w)
+
+
+def test_addresses_of_other_integer_types():
+    """Buffers whose data_ptr() returns an integer that is not Python's own, in calls of either kind."""
+    import numpy as np
+
+    class Buf(_Buf):
+        def data_ptr(self):
+            return np.uint64(self.at)
+
+    assert ft.ft_moe_int_quantize(ft.FT_DT_BF16, 0, 64, Buf(64, A), Buf(64, 2 * A), Buf(64, 3 * A)) == ft.FT_OK
+    norm = ft.make_rms_norm(ft.FT_DT_BF16, 4, 32, 1e-6)
+    _refused(ft.ft_moe_rms_norm_forward, norm, Buf(64, A), None, Buf(64, 2 * A), None, Buf(64, A + 2))
+    assert ft.ft_moe_rms_norm_forward(ft.make_rms_norm(ft.FT_DT_BF16, 0, 32, 1e-6), Buf(64, A), None, Buf(64, 2 * A)) == ft.FT_OK
