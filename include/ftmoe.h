@@ -564,7 +564,9 @@ typedef struct {
 int ft_moe_rms_norm_forward(const ft_moe_rms_norm *d, const void *x, const void *residual, const void *weight,
                             void *sum, void *y, int8_t *codes, float *scale, void *hip_stream);
 
-/* Scratch bytes of a backward call. */
+/* Scratch bytes of a backward call with dweight; one without needs no more.
+ * Rows of 8 to 16384 columns need none without dweight, nor for one or two of
+ * them: work may then be NULL. */
 int ft_moe_rms_norm_work(const ft_moe_rms_norm *d, int64_t *bytes);
 
 /* Gradients, from sum as the forward pass left it:

@@ -30,15 +30,20 @@ Rows rows_of(const ft_moe_rms_norm& d, const void* p, int64_t ld, int64_t es) {
   return {p, d.rows, d.cols * es, ld * es};
 }
 
+// one launch, whose only group of rows writes the weight's gradient itself
+bool norm_once(const ft_moe_rms_norm& d) { return d.rows <= kNormOnce && norm_rows(d.cols); }
+
 struct NormWork {
-  float *part, *stats;
+  float *stats, *part;
   int64_t bytes;
 };
-NormWork norm_work(const ft_moe_rms_norm& d, void* base) {
+// what a call with or without dweight uses
+NormWork norm_work(const ft_moe_rms_norm& d, bool dweight, void* base) {
   NormWork w{};
   Carve c{static_cast<uint8_t*>(base)};
-  w.part = reinterpret_cast<float*>(c.take(norm_groups(d.rows, d.cols) * norm_part_ld(d.cols) * 4));
-  w.stats = reinterpret_cast<float*>(c.take(int64_t(d.rows) * 16));
+  if (!norm_rows(d.cols)) w.stats = reinterpret_cast<float*>(c.take(int64_t(d.rows) * 16));
+  if (dweight && !norm_once(d))
+    w.part = reinterpret_cast<float*>(c.take(norm_groups(d.rows, d.cols) * norm_part_ld(d.cols) * 4));
   w.bytes = d.rows ? c.used : 0;
   return w;
 }
@@ -98,7 +103,7 @@ int ft_moe_rms_norm_work(const ft_moe_rms_norm* desc, int64_t* bytes) {
     ft_moe_rms_norm d;
     if (const int rc = check_norm(desc, d)) return rc;
     if (!bytes) return bad("bytes is NULL");
-    *bytes = norm_work(d, nullptr).bytes;
+    *bytes = norm_work(d, true, nullptr).bytes;
     return FT_OK;
   });
 }
@@ -110,7 +115,7 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm* desc, const void* sum, const
     ft_moe_rms_norm d;
     if (const int rc = check_norm(desc, d)) return rc;
     if (!dweight && (d.rows == 0 || (!dx && !dresidual))) return FT_OK;
-    const NormWork w = norm_work(d, work);
+    const NormWork w = norm_work(d, dweight != nullptr, work);
     if (const int rc = check_work(work, work_bytes, w.bytes)) return rc;
     const int64_t es = size_of(d.dtype), rs = size_of(d.residual_dtype);
     const Rows in[] = {rows_of(d, sum, d.ld_sum, rs), rows_of(d, dy, d.ld_y, es), rows_of(d, dsum, d.ld_residual, rs),
@@ -135,7 +140,8 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm* desc, const void* sum, const
     if (const int rc = g.enter(s, {arg(some, sum, rs, "sum"), arg(some, weight, es, "weight"), arg(some, dy, es, "dy"),
                                    arg(some && dsum, dsum, rs, "dsum"), arg(some && dx, dx, es, "dx"),
                                    arg(some && dresidual, dresidual, rs, "dresidual"),
-                                   arg(dweight != nullptr, dweight, es, "dweight"), arg(some, work, 16, "work")}))
+                                   arg(dweight != nullptr, dweight, es, "dweight"),
+                                   arg(w.bytes > 0, work, 16, "work")}))
       return rc;
     NormBackward a{};
     a.sum = sum;
@@ -144,9 +150,9 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm* desc, const void* sum, const
     a.dsum = dsum;
     a.dx = dx;
     a.dresidual = dresidual;
-    const bool once = some && dweight && d.rows <= kNormOnce && norm_rows(d.cols);
+    const bool once = some && dweight && norm_once(d);
     a.dweight = once ? dweight : nullptr;
-    a.part = dweight ? w.part : nullptr;
+    a.part = w.part;
     a.stats = w.stats;
     a.ld_sum = d.ld_sum;
     a.ld_y = d.ld_y;

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_backward(NormBackward a) {
       if (a.dresidual) dr.store(static_cast<R*>(a.dresidual) + row * a.ld_residual + p.c);
     }
   }
-  if (!a.part) return;
+  if (!a.part && !a.dweight) return;
 #pragma unroll
   for (int g = 0; g < PIECES; ++g) {
     const Place p(int(threadIdx.x) + g * THREADS, a.cols);

@@ -190,3 +190,16 @@ def test_struct_layouts():
         assert c[(n, "size")] == ctypes.sizeof(t), n
         for f, _ in t._fields_:
             assert c[(n, f)] == getattr(t, f).offset, (n, f)
+
+
+def test_norms_ask_for_the_scratch_memory_they_use():
+    """None for one or two rows that a workgroup holds, nor for any such rows without the weight's gradient."""
+    for cols in (8, 7168, 16384):
+        assert ft.ft_moe_rms_norm_work(_norm(rows=1, cols=cols)) == ft.ft_moe_rms_norm_work(_norm(rows=2, cols=cols)) == 0
+        # a part for each row and column, no more
+        assert ft.ft_moe_rms_norm_work(_norm(rows=4, cols=cols)) <= 4 * 4 * cols + 256
+    for cols in (7, 16385):
+        n = ft.ft_moe_rms_norm_work(_norm(rows=2, cols=cols))
+        assert n > 0
+        _refused(_backward, _norm(rows=2, cols=cols), work=_Buf(n - 1))
+        _refused(_backward, _norm(rows=2, cols=cols), dweight=None, work=None)

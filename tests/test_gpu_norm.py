@@ -240,3 +240,20 @@ def test_gradients_of_the_smallest_and_largest_rows(cols, type_, res):
         for k, v in ref.items():
             assert torch.isfinite(v[0]).all() and v[0].abs().max() < 2.0**127
             ac.check(got[k], v, f"{k} {size}")
+
+
+def test_gradients_without_scratch_memory():
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for rows, cols in ((1, 8), (2, 2050), (2, 16384)):
+        n = ac.Norm(rows, cols, "bf16", "fp32", pad=1)
+        got, ref = n.backward(work=none), n.backward_reference()
+        for k, v in ref.items():
+            ac.check(got[k], v, k)
+    for rows, cols in ((70, 2050), (3, 9)):
+        n = ac.Norm(rows, cols, "fp16", pad=1)
+        want, got = n.backward(), n.backward(dweight=False, work=none)
+        assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dresidual"], want["dresidual"])
+    # rows that no workgroup holds: what a call without the weight's gradient uses is less than one with it is told
+    n = ac.Norm(5, 20001, "bf16")
+    want, got = n.backward(), n.backward(dweight=False, work=torch.empty(5 * 16 + 176, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(got["dx"], want["dx"])
