@@ -41,6 +41,7 @@ struct AdaptersWork {
 };
 AdaptersWork adapters_work(const ft_moe_adapters& d, void* base) {
   AdaptersWork w{};
+  if (d.tokens == 0) return w;  // no tiles to cut
   Carve c{static_cast<uint8_t*>(base)};
   w.plan = adapter_plan(d.tokens, d.in, d.out, d.rank, d.adapters, int(size_of(d.base_dtype)), int(size_of(d.out_dtype)));
   w.ld_h = int32_t(up(d.rank, 4));

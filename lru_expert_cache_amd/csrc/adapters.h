@@ -77,7 +77,7 @@ struct Adapters {
 constexpr int adapter_out_blocks(int base_bytes, int out_bytes, int sub, int rank) {
   return out_bytes == 4 || (base_bytes == 4 && sub == 4) || rank > 64 || (sub == 1 && rank <= 16) ? 1 : 2;
 }
-// How a call is cut: a rule on sizes and types alone.
+// How a call of one token or more is cut: a rule on sizes and types alone.
 struct AdapterPlan {
   int32_t few, sub, windows, tile_cap, parts, out_blocks;
   int32_t once;      // both products in one launch: few tokens, up to 16 ranks

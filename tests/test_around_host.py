@@ -203,3 +203,19 @@ def test_norms_ask_for_the_scratch_memory_they_use():
         assert n > 0
         _refused(_backward, _norm(rows=2, cols=cols), work=_Buf(n - 1))
         _refused(_backward, _norm(rows=2, cols=cols), dweight=None, work=None)
+
+
+def test_scratch_sizes_of_calls_without_tokens():
+    """Asked for in a process of its own: a division by zero would end this one."""
+    import subprocess
+    import sys
+
+    code = ("import lru_expert_cache_amd as ft\n"
+            "for n in (1, 3, 4096):\n"
+            "    for rank in (1, 16, 256):\n"
+            "        assert ft.ft_moe_adapters_work(ft.make_adapters(ft.FT_DT_BF16, 0, 5000, 64, rank, n)) == 0\n"
+            "        assert ft.ft_moe_adapters_work(ft.make_adapters(ft.FT_DT_F16, 0, 64, 64, rank, n, out_dtype=ft.FT_DT_F32)) == 0\n"
+            "assert ft.ft_moe_rms_norm_work(ft.make_rms_norm(ft.FT_DT_BF16, 0, 32, 1e-6)) == 0\n"
+            "assert ft.ft_moe_balance_work(ft.make_balance(ft.FT_DT_F32, 0, 16, 2, 0.01)) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
