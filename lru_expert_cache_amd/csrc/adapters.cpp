@@ -45,6 +45,10 @@ AdaptersWork adapters_work(const ft_moe_adapters& d, void* base) {
   Carve c{static_cast<uint8_t*>(base)};
   w.plan = adapter_plan(d.tokens, d.in, d.out, d.rank, d.adapters, int(size_of(d.base_dtype)), int(size_of(d.out_dtype)));
   w.ld_h = int32_t(up(d.rank, 4));
+  if (w.plan.once) {  // h never leaves the workgroups: the smallest piece, so that every call with tokens has its `work`
+    w.bytes = kAlign;
+    return w;
+  }
   w.h = reinterpret_cast<float*>(c.take(int64_t(w.plan.parts) * d.tokens * w.ld_h * 4));
   if (!w.plan.few) {
     w.order = reinterpret_cast<int32_t*>(c.take(int64_t(d.tokens) * 4));

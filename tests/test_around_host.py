@@ -219,3 +219,11 @@ def test_scratch_sizes_of_calls_without_tokens():
             "assert ft.ft_moe_balance_work(ft.make_balance(ft.FT_DT_F32, 0, 16, 2, 0.01)) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+def test_adapters_ask_for_the_scratch_memory_they_use():
+    """One launch for both products keeps nothing in memory; two keep the sums of the first, at least."""
+    for tokens in (1, 64):
+        assert 0 < ft.ft_moe_adapters_work(_adapters(tokens=tokens, in_features=2048, rank=16)) <= 256
+        assert ft.ft_moe_adapters_work(_adapters(tokens=tokens, in_features=2048, rank=17)) >= tokens * 17 * 4
+    assert ft.ft_moe_adapters_work(_adapters(tokens=0)) == 0
