@@ -540,8 +540,10 @@ int ft_moe_int_gated_ffn(const ft_moe_gated_ffn *d, const void *x, const int8_t 
 /* Root-mean-square norm of a residual stream.
  *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
  * x, weight and y have type dtype; the stream's tensors (residual, sum and
- * their gradients) have residual_dtype.  The norm is taken of the unrounded s:
- * sum and y are rounded once each.  Sizes up to 2^24 - 1 per dimension. */
+ * their gradients) have residual_dtype.  The norm is taken of the unrounded s;
+ * sum and y are formed in 64 bits and rounded to 32 bits and then to their
+ * type (a value within 2^-24 of the middle between two 16-bit numbers may get
+ * the other of them).  Sizes up to 2^24 - 1 per dimension. */
 typedef struct {
   int32_t dtype;          /* FT_DT_* of x, weight, y and their gradients */
   int32_t residual_dtype; /* of residual, sum, dsum, dresidual: dtype or FT_DT_F32; 0 = dtype */
@@ -569,7 +571,8 @@ int ft_moe_rms_norm_forward(const ft_moe_rms_norm *d, const void *x, const void 
  * them: work may then be NULL. */
 int ft_moe_rms_norm_work(const ft_moe_rms_norm *d, int64_t *bytes);
 
-/* Gradients, from sum as the forward pass left it:
+/* Gradients, from sum as the forward pass left it (the two means in 64 bits,
+ * the rest in 32, and rounded to its type at the end):
  *   r = 1 / sqrt(mean(s^2) + eps), g = dy weight
  *   ds = r (g - s r^2 mean(g s)) + dsum,  dweight = sum over rows of dy s r
  * ds is the gradient of x and of residual alike; it is written as dx (dtype)
@@ -586,8 +589,9 @@ int ft_moe_rms_norm_backward(const ft_moe_rms_norm *d, const void *sum, const vo
  * x [T][K], A [n][R][K], B [n][N][R] (adapter i's rows follow adapter i - 1's),
  * base and y [T][N], ids [T] in any order.  A token whose id is not in
  * 0..n-1 has no adapter: y[t] = base[t].  A x is held in 32 bits and enters
- * the second product in two 16-bit parts: y is rounded once.  base is the
- * projection's result (of ft_moe_int_matmul, say; with FT_DT_F32 nothing of it
+ * the second product in two 16-bit parts; its sums, their product with scale
+ * and the addition of base are made in 32 bits, and rounded to y's type at the
+ * end.  base is the projection's result (of ft_moe_int_matmul, say; with FT_DT_F32 nothing of it
  * was rounded before), or NULL for 0.  Infinities and NaN in a row of x or
  * base stay in that row of y; A and B are finite (an infinity in them may give
  * NaN where the formula has an infinity, for their adapter's tokens only). */
@@ -618,7 +622,10 @@ int ft_moe_adapters_apply(const ft_moe_adapters *d, const void *x, const int32_t
  * out (not counted, sel -1, w 0, gradient 0) when valid[t] is 0 or all its
  * logits are -inf.  A logit of -inf, or NaN, is never chosen: ranks for which
  * no other is left hold sel -1 and w 0, and are not counted.  A NaN or +inf in
- * a token that counts makes loss and that token's gradients NaN. */
+ * a token that counts makes loss and that token's gradients NaN.
+ * The choice is for a program's own training step: ft_moe_layer_forward makes
+ * its own from router_w, by the same rule, takes no sel or w, and has no
+ * gradients. */
 typedef struct {
   int32_t dtype;     /* FT_DT_* of logits and dlogits */
   int32_t tokens;    /* T >= 0 */

@@ -16,7 +16,8 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   // out = 7168, rank 64) 26 / 25 / 29; 2048 tokens (2048, rank 16) 22 / 20 /
   // 22; 8192 tokens (2048, rank 64) 71 / 58 / 58; 8192 tokens (7168, rank 64)
   // 194 / 137 / 115; 1531 tokens (rank 8, a quarter of them single) 29 / 35 /
-  // -; rank 128, 8192 tokens: 320 / 189 / -.
+  // -; rank 128, 8192 tokens: 320 / 189 / -.  The host knows the table's size alone, and takes every adapter in it to be
+  // asked for: 8192 tokens (7168, rank 64) of 16 adapters in a table of 16 / 129 / 257 / 1024: 110 / 134 / 179 / 167 us.
   if (rank <= 128 && int64_t(tokens) * (rank > 16 ? 2 : 1) >= 2048 && tokens >= 32 * count) p.sub = 2;
   if (rank <= 64 && tokens >= 4096 && int64_t(in) + out >= 8192 && tokens >= 64 * count) p.sub = 4;
   p.windows = std::max(1, (tokens + kAdapterWindow - 1) / kAdapterWindow);
@@ -30,7 +31,9 @@ AdapterPlan adapter_plan(int32_t tokens, int32_t in, int32_t out, int32_t rank, 
   p.parts = int32_t(std::clamp<int64_t>(std::min<int64_t>((256 + tiles / 2) / tiles, in / 256), 1, 32));
   // One launch where a workgroup soon has all of A x: graphs of calls (rank 16, N 4096), one launch against two, us:
   // one / 8 / 32 tokens of as many adapters, K 2560: 6.6 / 8.0 / 8.4 against 7.4 / 8.3 / 8.9; 3584: 7.2 / 9.3 / 9.8
-  // against 7.5 / 8.7 / 9.4.  Calls by themselves save up to the launch's 2 us too.
+  // against 7.5 / 8.7 / 9.4.  Calls by themselves save up to the launch's 2 us too.  The width alone decides, for any
+  // number of tokens: one alone would still gain 0.3 us at 3584, where 8 and 32 lose 0.6 and 0.4.  Ranks above 16 have
+  // no such kernel (one token, rank 64, 2048 / 6144: 9.3 / 8.5 us in two launches).
   p.once = p.few && rank <= 16 && in <= 2560;
   p.out_step = 32 * (p.once ? 16 : 4 * adapter_out_blocks(base_bytes, out_bytes, p.sub, rank));
   // columns for about 1024 workgroups: each joins h's parts first (8192 tokens, 7168, rank 64: steps of 256 columns

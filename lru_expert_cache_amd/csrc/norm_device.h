@@ -4,7 +4,9 @@
 // row's codes are rint(y / scale), and have to be those of the exact y: all of
 // it is formed in 64 bits (s of 16-bit addends and p are then exact), which
 // leaves one y in about 2^40 on the wrong side of a border between two codes,
-// and costs little: the 64-bit units keep up with the memory.
+// and costs little: the 64-bit units keep up with the memory.  s and y go to
+// 16 bits by way of 32: the instructions that convert start from there, and what
+// that second rounding turns the other way lies within 2^-24 of a tie.
 //
 // Backward: with n = s r and g = dy weight, ds = r (g - n mean(g n)); only the
 // two sums are formed in 64 bits.

@@ -191,7 +191,8 @@ hipError_t launch_width(const A& a, hipStream_t s) {
   // Threads for up to four pieces each, the fewer the better: 8192 rows of 7168, us, by 256 x 4 / 512 x 2 / 1024 x 1:
   // codes and y 107 / 109 / 147, gradients (32-bit stream) 182 / 185 / 188; 32 rows of 6144: 5.2 / 5.2 / 6.3; 8192 rows
   // of 4096 by 128 x 4 / 256 x 2 / 512 x 1: codes and y 61 / 59 / 70; of 2048 by 128 x 2 / 256 x 1: 33 / 38, gradients
-  // 40 / 36.
+  // 40 / 36.  Chosen on 16-bit rows; 32-bit ones run at a copy's rate or past it by the same table (8192 x 2048 / 8192 x
+  // 4096 / 4096 x 7168, forward 51 / 99 / 89 us, with codes 56 / 108 / 97, gradients 52 / 105 / 96: 4.9 to 5.4 TB/s).
   if (a.cols <= 512) return launch<X, R, 64, 1>(a, s);
   if (a.cols <= 2048) return launch<X, R, 256, 1>(a, s);
   if (a.cols <= 4096) return launch<X, R, 256, 2>(a, s);

@@ -257,3 +257,11 @@ def test_gradients_without_scratch_memory():
     n = ac.Norm(5, 20001, "bf16")
     want, got = n.backward(), n.backward(dweight=False, work=torch.empty(5 * 16 + 176, dtype=torch.uint8, device="cuda"))
     assert torch.equal(got["dx"], want["dx"])
+
+
+@pytest.mark.parametrize("type_,res", TYPES)
+def test_rows_are_rounded_by_way_of_32_bits(type_, res):
+    """The sum, bit for bit: exact in 64 bits for 16-bit addends and rounded once to 32, then once to its type."""
+    n = ac.Norm(50, 1500, type_, res, seed=4)
+    s = (n.x.double() + n.residual.double()).float()
+    assert torch.equal(n.forward()["sum"], s.to(n.r))
