@@ -207,9 +207,11 @@ def test_norms_ask_for_the_scratch_memory_they_use():
 
 def test_scratch_sizes_of_calls_without_tokens():
     """Asked for in a process of its own: a division by zero would end this one."""
+    import os
     import subprocess
     import sys
 
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     code = ("import lru_expert_cache_amd as ft\n"
             "for n in (1, 3, 4096):\n"
             "    for rank in (1, 16, 256):\n"
@@ -217,7 +219,7 @@ def test_scratch_sizes_of_calls_without_tokens():
             "        assert ft.ft_moe_adapters_work(ft.make_adapters(ft.FT_DT_F16, 0, 64, 64, rank, n, out_dtype=ft.FT_DT_F32)) == 0\n"
             "assert ft.ft_moe_rms_norm_work(ft.make_rms_norm(ft.FT_DT_BF16, 0, 32, 1e-6)) == 0\n"
             "assert ft.ft_moe_balance_work(ft.make_balance(ft.FT_DT_F32, 0, 16, 2, 0.01)) > 0\n")
-    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120, cwd=root)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
 
 
